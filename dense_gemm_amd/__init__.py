@@ -3,7 +3,8 @@
 The functions named like the C ABI (include/dense_gemm.h) only marshal
 arguments: every step of the computation runs in the library's HIP kernels.
 `gemm()` is a convenience over torch tensors (torch is used for device memory
-and streams only).
+and streams only); so are `quantize_mx`, `gemm_mx`, `gemm_dq`,
+`act_checkpoint` and their companions for block-scaled matrices (mx.py).
 
 The library must have been built (python dense_gemm_amd/build.py); importing
 this package fails loudly when it is missing.
@@ -262,3 +263,9 @@ def gemm(A, B, C=None, transA=False, transB=False, alpha=1.0, beta=0.0, bias=Non
     if rc != DG_OK:
         raise GemmError(rc)
     return C
+
+
+# ---- block-scaled (MX) matrices --------------------------------------------------
+from . import mx as _mx  # noqa: E402
+from .mx import *  # noqa: E402,F401,F403
+EXPORTED += _mx.EXPORTED

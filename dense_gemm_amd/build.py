@@ -23,11 +23,13 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
 SOURCES = ["api.cpp", "gemm_simple.hip", "gemm_f32.hip", "gemm_f16.hip", "gemm_bf16.hip",
-           "gemm_f16_o32.hip", "gemm_bf16_o32.hip"]
+           "gemm_f16_o32.hip", "gemm_bf16_o32.hip", "api_mx.cpp", "mx_quantize.hip", "mx_gemm.hip",
+           "dq_gemm.hip"]
 # the control probes of the measurements, a library of their own
 PROBE_LIB = os.path.join(PKG, "libdense_gemm_probe.so")
 PROBE_SOURCES = ["probe.hip"]
-HEADERS = ["gemm_common.hpp", "gemm_mfma.hpp", "gemm_pipe.hpp", "gemm_tables16.hpp"]
+HEADERS = ["gemm_common.hpp", "gemm_mfma.hpp", "gemm_pipe.hpp", "gemm_tables16.hpp", "mx_common.hpp",
+           "mx_tile.hpp"]
 
 FLAGS = [
     "-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",

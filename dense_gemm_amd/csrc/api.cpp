@@ -17,6 +17,7 @@ namespace dg {
 launch_fn simple_launcher(int dtype, int ta, int tb);
 launch_fn scale_launcher(int dtype);
 launch_fn splitk_reduce_launcher(int dtype);
+int launch_status(hipError_t err);
 const launch_fn *f32_launchers(int config);
 const launch_fn *f16_launchers(int config);
 const launch_fn *f16_pipe_launchers(int config);
@@ -550,11 +551,7 @@ int run(int ta, int tb, int64_t M, int64_t N, int64_t K, float alpha, const void
             if (err == hipSuccess && p.splits > 1) err = dg::splitk_reduce_launcher(di)(p, s);
         }
     }
-    if (err != hipSuccess) {
-        g_last_hip_error = (int)err;
-        return DG_ERR_HIP;
-    }
-    return DG_OK;
+    return dg::launch_status(err);
 }
 
 // ---- scratch memory of dg_gemm_splitk_noalloc ---------------------------------
@@ -605,6 +602,19 @@ int scratch_for(void *stream, void **out)
 }
 
 }  // namespace
+
+namespace dg {
+
+// The status of a launch: keeps a failed call's hipError_t for
+// dg_last_hip_error.
+int launch_status(hipError_t err)
+{
+    if (err == hipSuccess) return DG_OK;
+    g_last_hip_error = (int)err;
+    return DG_ERR_HIP;
+}
+
+}  // namespace dg
 
 extern "C" {
 
@@ -775,12 +785,14 @@ const char *dg_status_string(int status)
                      "not aligned to its element)";
     case -19: return "invalid argument 19 (dg_gemm_ex: epilogue)";
     case -20: return "invalid argument 20 (dg_gemm_ex: dtype)";
+    case -21: return "invalid argument 21";
+    case -22: return "invalid argument 22";
     default: return "unknown status";
     }
 }
 
 int dg_last_hip_error(void) { return g_last_hip_error; }
 
-int dg_version(void) { return 400; }
+int dg_version(void) { return 500; }
 
 }  // extern "C"

@@ -1,0 +1,369 @@
+// Rounding to MX formats and back, and the activation passes that keep their
+// input in 8 bits.  Elementwise work, bound by memory: each kernel makes one
+// pass, 16 bytes or more per lane and access.
+//
+// Row kernels: a lane takes 8 consecutive elements of a row, so 4 lanes hold
+// a block of 32 and the block's largest magnitude comes from two lane
+// exchanges; a wave covers 512 columns of one row.  The scale byte is stored
+// by one lane of the four.
+#include "mx_common.hpp"
+
+namespace dg {
+
+namespace {
+
+
+
+// Eight elements of a row as one 16-byte access (two for fp32).  Rows need
+// only be aligned to their element: the GPU takes misaligned vector accesses
+// to global memory, so odd row strides go the same way as aligned ones.
+template <typename T> struct Eight {
+    typedef T V8 __attribute__((ext_vector_type(8)));
+    typedef V8 __attribute__((aligned(sizeof(T)))) V8u;
+};
+
+// Elements col .. col+7 of a row of n elements at `row` (zeros past n).
+template <typename T>
+__device__ __forceinline__ void load8(const T *row, int64_t col, int64_t n, float (&v)[8])
+{
+    if (col + 8 <= n) {
+        const typename Eight<T>::V8 a = *(const typename Eight<T>::V8u *)(row + col);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = (float)a[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = col + i < n ? (float)row[col + i] : 0.f;
+    }
+}
+
+// One rounding to T (nothing for fp32).
+template <typename T>
+__device__ __forceinline__ void store8(T *row, int64_t col, int64_t n, const float (&v)[8])
+{
+    typename Eight<T>::V8 a;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a[i] = (T)v[i];
+    if (col + 8 <= n) {
+        *(typename Eight<T>::V8u *)(row + col) = a;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (col + i < n) row[col + i] = a[i];
+    }
+}
+
+// Largest magnitude of the 32 elements held by 4 neighbouring lanes, as bits.
+__device__ __forceinline__ uint32_t block_amax(const float (&v)[8])
+{
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t b = __builtin_bit_cast(uint32_t, v[i]) & 0x7fffffffu;
+        m = b > m ? b : m;
+    }
+    uint32_t o = (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0xb1, 0xf, 0xf, true);   // lane ^ 1
+    m = o > m ? o : m;
+    o = (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x4e, 0xf, 0xf, true);            // lane ^ 2
+    return o > m ? o : m;
+}
+
+// Codes and scale of the 8 elements a lane holds, col a multiple of 8.
+template <int FORMAT>
+__device__ __forceinline__ void store_codes(const MxParams &p, int64_t row, int64_t col, const float (&v)[8])
+{
+    const uint32_t byte = mx_scale_byte(block_amax(v), FORMAT);
+    const u32x2 q = mx_encode8<FORMAT>(v, byte);
+    uint8_t *qr = p.Q + row * p.ldq;
+    if constexpr (FORMAT == MX_FP4) *(uint32_t *)(qr + col / 2) = q[0];
+    else *(u32x2 *)(qr + col) = q;
+    if ((threadIdx.x & 3) == 0)
+        p.S[((col >> 8) * p.lds + row) * 8 + ((col >> 5) & 7)] = (uint8_t)byte;
+}
+
+template <int FORMAT>
+__device__ __forceinline__ void load_codes(const MxParams &p, int64_t row, int64_t col, float (&v)[8])
+{
+    const uint8_t *qr = p.Q + row * p.ldq;
+    u32x2 q = {0u, 0u};
+    if constexpr (FORMAT == MX_FP4) q[0] = *(const uint32_t *)(qr + col / 2);
+    else q = *(const u32x2 *)(qr + col);
+    mx_decode8<FORMAT>(q, p.S[((col >> 8) * p.lds + row) * 8 + ((col >> 5) & 7)], v);
+}
+
+// The row kernels' places: item b is rows 4 * (b / chunks) .. +3 (one per
+// wave) and columns 512 * (b % chunks) .. +511 (8 per lane).  The padding up
+// to the next whole group is part of the stored row (zeros), so columns run to
+// the group's end.  A workgroup takes every gridDim.x-th item (the grid is
+// capped: a launch holds fewer than 2^32 threads).
+__device__ __forceinline__ bool place(const MxParams &p, int64_t b, int64_t &row, int64_t &col)
+{
+    const int64_t chunks = (mx_groups(p.cols) + 1) / 2;
+    row = (b / chunks) * 4 + (threadIdx.x >> 6);
+    col = (b % chunks) * 512 + (threadIdx.x & 63) * 8;
+    // whole groups of 32 lanes are in or out: a block's four lanes together
+    return row < p.rows && col < mx_groups(p.cols) * MX_GROUP;
+}
+
+__host__ __device__ __forceinline__ int64_t row_items(const MxParams &p)
+{
+    return (mx_groups(p.cols) + 1) / 2 * ((p.rows + 3) / 4);
+}
+
+__host__ __device__ __forceinline__ int64_t trans_items(const MxParams &p)
+{
+    return (p.rows + 31) / 32 * mx_groups(p.cols);
+}
+
+template <typename T, int FORMAT>
+__global__ __launch_bounds__(256) void mx_quantize_kernel(MxParams p)
+{
+    const int64_t n = row_items(p);
+    for (int64_t b = blockIdx.x; b < n; b += gridDim.x) {
+        int64_t row, col;
+        if (!place(p, b, row, col)) continue;
+        float v[8];
+        load8<T>((const T *)p.X + row * p.ldx, col, p.cols, v);
+        store_codes<FORMAT>(p, row, col, v);
+    }
+}
+
+// X stored cols x rows: a workgroup rounds 256 k of 32 rows (one scale
+// group), through LDS: the loads run along the stored rows (lanes along n),
+// then each thread takes one block of 32 k of one row.  Rows of the LDS tile
+// are padded by one word, so the column reads of 32 lanes fall on distinct
+// banks.
+template <typename T, int FORMAT>
+__global__ __launch_bounds__(256) void mx_quantize_t_kernel(MxParams p)
+{
+    __shared__ float tile[MX_GROUP][33];
+    const int64_t nb = (p.rows + 31) / 32, items = trans_items(p);
+    const int tid = threadIdx.x, n = tid & 31, kq = tid >> 5;
+    const T *X = (const T *)p.X;
+    for (int64_t b = blockIdx.x; b < items; b += gridDim.x) {
+        const int64_t n0 = (b % nb) * 32, k0 = (b / nb) * MX_GROUP;
+#pragma unroll 8
+        for (int i = 0; i < 32; ++i) {
+            const int k = i * 8 + kq;
+            float x = 0.f;
+            if (k0 + k < p.cols && n0 + n < p.rows) x = (float)X[(k0 + k) * p.ldx + n0 + n];
+            tile[k][n] = x;
+        }
+        __syncthreads();
+        if (n0 + n < p.rows) {
+            float v[4][8];
+            uint32_t m = 0;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const float x = tile[kq * 32 + i][n];
+                v[i >> 3][i & 7] = x;
+                const uint32_t a = __builtin_bit_cast(uint32_t, x) & 0x7fffffffu;
+                m = a > m ? a : m;
+            }
+            const uint32_t byte = mx_scale_byte(m, FORMAT);
+            uint8_t *q = p.Q + (n0 + n) * p.ldq + (FORMAT == MX_FP4 ? k0 / 2 + kq * 16 : k0 + kq * 32);
+            u32x2 o[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] = mx_encode8<FORMAT>(v[i], byte);
+            if constexpr (FORMAT == MX_FP4) {
+                *(u32x4 *)q = (u32x4){o[0][0], o[1][0], o[2][0], o[3][0]};
+            } else {
+                *(u32x4 *)q = (u32x4){o[0][0], o[0][1], o[1][0], o[1][1]};
+                *(u32x4 *)(q + 16) = (u32x4){o[2][0], o[2][1], o[3][0], o[3][1]};
+            }
+            p.S[((k0 >> 8) * p.lds + n0 + n) * 8 + kq] = (uint8_t)byte;
+        }
+        __syncthreads();      // the tile is free for the next item
+    }
+}
+
+template <typename T, int FORMAT>
+__global__ __launch_bounds__(256) void mx_dequantize_kernel(MxParams p)
+{
+    const int64_t n = row_items(p);
+    for (int64_t b = blockIdx.x; b < n; b += gridDim.x) {
+        int64_t row, col;
+        if (!place(p, b, row, col) || col >= p.cols) continue;
+        float v[8];
+        load_codes<FORMAT>(p, row, col, v);
+        store8<T>((T *)p.Y + row * p.ldy, col, p.cols, v);
+    }
+}
+
+// h = act(z) and z in 8 bits, one read of z.  H may be Z itself: a lane
+// reads its elements before it writes them.
+template <typename T, int FORMAT>
+__global__ __launch_bounds__(256) void act_checkpoint_kernel(MxParams p)
+{
+    const int64_t n = row_items(p);
+    for (int64_t b = blockIdx.x; b < n; b += gridDim.x) {
+        int64_t row, col;
+        if (!place(p, b, row, col)) continue;
+        float v[8];
+        load8<T>((const T *)p.X + row * p.ldx, col, p.cols, v);
+        store_codes<FORMAT>(p, row, col, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = activate(p.act, v[i]);
+        store8<T>((T *)p.Y + row * p.ldy, col, p.cols, v);
+    }
+}
+
+// act'(z).  relu: 1 above zero, else 0 (NaN stays NaN).  gelu = z Phi(z):
+// Phi(z) + z phi(z), with phi the normal density and Phi by the same
+// approximation of erfc as the forward (Abramowitz & Stegun 7.1.26), on
+// q = erfc(|z| / sqrt 2): Phi = 1 - q/2 for z >= 0 and q/2 below.  exp(-z^2/2)
+// serves both terms.  For |z| past 14 the density underflows; z is clamped
+// there so that an infinity gives 1 or 0 and not inf * 0 (NaN stays NaN).
+__device__ __forceinline__ float act_slope(int act, float z)
+{
+    if (act == ACT_RELU) return z > 0.f ? 1.f : (z <= 0.f ? 0.f : z);
+    z = z > 14.f ? 14.f : (z < -14.f ? -14.f : z);
+    const float a = __builtin_fabsf(z) * 0.70710678118654752f;
+    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.3275911f, a, 1.f));
+    float poly = __builtin_fmaf(t, 1.061405429f, -1.453152027f);
+    poly = __builtin_fmaf(t, poly, 1.421413741f);
+    poly = __builtin_fmaf(t, poly, -0.284496736f);
+    poly = __builtin_fmaf(t, poly, 0.254829592f);
+    const float ex = __expf(-a * a);
+    const float hq = 0.5f * poly * t * ex;
+    const float cdf = z >= 0.f ? 1.f - hq : hq;
+    return __builtin_fmaf(z * 0.3989422804014327f, ex, cdf);
+}
+
+// dZ = dH * act'(z8), and the column sums of dZ (before its rounding) into
+// one row of partial sums per slice of rows.  Workgroup (c, s) takes 512
+// columns and the rows of slice s, its four waves every fourth of them; the
+// waves' sums meet in LDS, in wave order, so the sum's order is fixed.
+template <typename T, int FORMAT>
+__global__ __launch_bounds__(256) void act_backward_kernel(MxParams p)
+{
+    __shared__ float part[4][512];
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int64_t col = (int64_t)blockIdx.x * 512 + lane * 8;
+    const int64_t r0 = p.rows * blockIdx.y / p.slices, r1 = p.rows * (blockIdx.y + 1) / p.slices;
+    float sum[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum[i] = 0.f;
+    if (col < p.cols) {
+#pragma unroll 2
+        for (int64_t row = r0 + wave; row < r1; row += 4) {
+            float z[8], d[8];
+            load8<T>((const T *)p.X + row * p.ldx, col, p.cols, d);
+            load_codes<FORMAT>(p, row, col, z);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                d[i] *= act_slope(p.act, z[i]);
+                sum[i] += d[i];
+            }
+            store8<T>((T *)p.Y + row * p.ldy, col, p.cols, d);
+        }
+    }
+    if (!p.dbias) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) part[wave][lane * 8 + i] = sum[i];
+    __syncthreads();
+    for (int c = threadIdx.x; c < 512; c += 256) {
+        const int64_t gc = (int64_t)blockIdx.x * 512 + c;
+        if (gc < p.cols)
+            p.ws[(int64_t)blockIdx.y * p.cols + gc] = ((part[0][c] + part[1][c]) + part[2][c]) + part[3][c];
+    }
+}
+
+// dbias = the slices' partial sums in increasing order: 16 threads a column
+// (each every 16th slice), then those 16 sums in order.
+__global__ __launch_bounds__(256) void column_sum_kernel(const float *ws, float *dbias, int64_t cols, int slices)
+{
+    __shared__ float part[16][17];
+    const int c = threadIdx.x & 15, q = threadIdx.x >> 4;
+    for (int64_t c0 = (int64_t)blockIdx.x * 16; c0 < cols; c0 += (int64_t)gridDim.x * 16) {
+        const int64_t col = c0 + c;
+        float s = 0.f;
+        if (col < cols)
+            for (int i = q; i < slices; i += 16) s += ws[(int64_t)i * cols + col];
+        part[q][c] = s;
+        __syncthreads();
+        if (q == 0 && col < cols) {
+            for (int i = 1; i < 16; ++i) s += part[i][c];
+            dbias[col] = s;
+        }
+        __syncthreads();
+    }
+}
+
+template <typename... Args>
+hipError_t launch(const void *f, dim3 grid, dim3 block, hipStream_t s, Args... a)
+{
+    void *args[] = {&a...};
+    return hipLaunchKernel(f, grid, block, args, 0, s);
+}
+
+typedef void (*kernel_fn)(MxParams);
+
+// Workgroups for n items of work (2^23 at most: 2^31 threads).
+dim3 grid_for(int64_t n) { return dim3((unsigned)(n < (1 << 23) ? n : (1 << 23))); }
+
+template <typename T, int F>
+kernel_fn quantize_fn(const MxParams &p)
+{
+    return p.trans ? mx_quantize_t_kernel<T, F> : mx_quantize_kernel<T, F>;
+}
+template <typename T, int F>
+kernel_fn dequantize_fn(const MxParams &)
+{
+    return mx_dequantize_kernel<T, F>;
+}
+template <typename T, int F>
+kernel_fn checkpoint_fn(const MxParams &)
+{
+    return act_checkpoint_kernel<T, F>;
+}
+template <typename T, int F>
+kernel_fn backward_fn(const MxParams &)
+{
+    return act_backward_kernel<T, F>;
+}
+
+#define DG_BY_FORMAT8(fn, T) (p.format == MX_FP8 ? fn<T, MX_FP8>(p) : fn<T, MX_INT8>(p))
+#define DG_BY_FORMAT(fn, T)                                                                        \
+    (p.format == MX_FP4 ? fn<T, MX_FP4>(p) : p.format == MX_FP8 ? fn<T, MX_FP8>(p) : fn<T, MX_INT8>(p))
+#define DG_BY_TYPE(by, fn) \
+    (p.type == ELEM_F32 ? by(fn, float) : p.type == ELEM_F16 ? by(fn, _Float16) : by(fn, __bf16))
+
+}  // namespace
+
+hipError_t launch_mx_quantize(const MxParams &p, hipStream_t s)
+{
+    return launch((const void *)DG_BY_TYPE(DG_BY_FORMAT, quantize_fn), grid_for(p.trans ? trans_items(p) : row_items(p)), dim3(256), s, p);
+}
+
+hipError_t launch_mx_dequantize(const MxParams &p, hipStream_t s)
+{
+    return launch((const void *)DG_BY_TYPE(DG_BY_FORMAT, dequantize_fn), grid_for(row_items(p)), dim3(256), s, p);
+}
+
+hipError_t launch_act_checkpoint(const MxParams &p, hipStream_t s)
+{
+    return launch((const void *)DG_BY_TYPE(DG_BY_FORMAT8, checkpoint_fn), grid_for(row_items(p)), dim3(256), s, p);
+}
+
+// Row slices of the backward: about 2048 workgroups (8 per compute unit)
+// over the column chunks, at least 4 rows each (one per wave).
+int act_backward_slices(int64_t rows, int64_t cols)
+{
+    const int64_t chunks = (cols + 511) / 512;
+    int64_t s = 2048 / chunks;
+    if (s > (rows + 3) / 4) s = (rows + 3) / 4;
+    return s < 1 ? 1 : (int)s;
+}
+
+hipError_t launch_act_backward(const MxParams &p, hipStream_t s)
+{
+    if (p.slices > 0) {
+        const dim3 grid((unsigned)((p.cols + 511) / 512), (unsigned)p.slices);
+        const hipError_t e = launch((const void *)DG_BY_TYPE(DG_BY_FORMAT8, backward_fn), grid, dim3(256), s, p);
+        if (e != hipSuccess || !p.dbias) return e;
+    }
+    return launch((const void *)&column_sum_kernel, grid_for((p.cols + 15) / 16), dim3(256), s,
+                  (const float *)p.ws, p.dbias, p.cols, (int)p.slices);
+}
+
+}  // namespace dg

@@ -107,6 +107,10 @@ typedef DG_ENUM(dg_dtype) {
 } dg_dtype_t;
 /* Epilogue activations of dg_gemm_ex. */
 typedef DG_ENUM(dg_epilogue) { DG_EPI_NONE = 0, DG_EPI_RELU = 1, DG_EPI_GELU = 2 } dg_epilogue_t;
+/* Element types of the plain matrices beside MX matrices. */
+typedef DG_ENUM(dg_elem) { DG_ELEM_F32 = 0, DG_ELEM_F16 = 1, DG_ELEM_BF16 = 2 } dg_elem_t;
+/* Formats of MX matrices (see "Block-scaled (MX) matrices" below). */
+typedef DG_ENUM(dg_mx) { DG_MXFP4 = 0, DG_MXFP8 = 1, DG_MXINT8 = 2 } dg_mx_t;
 #undef DG_ENUM
 
 #define DG_OK 0
@@ -251,6 +255,143 @@ size_t dg_gemm_splitk_workspace_size(int64_t M, int64_t N, int splits);
 int dg_select_kernel(dg_op_t transA, dg_op_t transB, int64_t M, int64_t N, int64_t K, const void *A,
                      int64_t lda, const void *B, int64_t ldb, const void *C, int64_t ldc,
                      dg_dtype_t dtype);
+
+/* ---- Block-scaled (MX) matrices ------------------------------------------------
+ *
+ * An MX matrix of rows x cols holds each row in blocks of 32 elements (the
+ * last one may be short).  A block has one scale 2^e and elements of 4 or 8
+ * bits, after the OCP Microscaling Formats (MX) specification v1.0:
+ *   DG_MXFP4   E2M1: +-{0, 0.5, 1, 1.5, 2, 3, 4, 6}        emax = 2
+ *   DG_MXFP8   E4M3: up to 448                              emax = 8
+ *   DG_MXINT8  a signed integer in 64ths, -127 .. 127       emax = 0
+ * Rounding (dg_mx_quantize, dg_act_checkpoint): with m the largest magnitude
+ * of the block, e = max(floor(log2(m)) - emax, -127) (-127 for m = 0), and
+ * each element is x / 2^e rounded to nearest even and saturated to the
+ * format's largest.  A block that holds a NaN or an infinity gets a NaN
+ * scale and zero elements: all of its values are then NaN.
+ *
+ * Storage, two buffers in device memory:
+ *   Q  elements, row r at byte r * ldq; mxfp4 two elements to a byte, the
+ *      even one in the low 4 bits.  A row holds whole groups of 256 elements
+ *      (128 bytes of mxfp4, 256 of the others; dg_mx_row_bytes); elements at
+ *      or past cols are zero (the products rely on it).  Q is 16-byte
+ *      aligned, ldq a multiple of 16.
+ *   S  scales, one byte e + 127 each (255: NaN); the scale of block b of row
+ *      r is byte ((b / 8) * lds + r) * 8 + b % 8, so the 8 scales of a row's
+ *      group lie together and a group's rows one after the other.  S is
+ *      8-byte aligned, lds >= rows (dg_mx_scale_bytes).
+ * Rows r0 .. of a matrix are the matrix at Q + r0 * ldq and S + r0 * 8 with
+ * the same ldq and lds; columns from a multiple of 256 on, at Q + (128 or
+ * 256) * g and S + g * lds * 8.  Nothing outside a matrix's own rows and
+ * groups is written; scales of blocks past cols within the last group are
+ * written as 0.
+ *
+ * Pointers, streams, asynchrony and errors as dg_gemm: -i names an invalid
+ * argument by its position (types and formats are checked before the pointers
+ * whose alignment depends on them), and nothing is enqueued then.  Plain matrices are aligned to their element.  Sizes are at
+ * most 2^31 - 1.  No call allocates memory, and no call keeps state: calls on
+ * different streams do not interfere unless they share a workspace or an
+ * output. */
+
+/* Bytes of one row of Q, or -i. */
+int64_t dg_mx_row_bytes(dg_mx_t format, int64_t cols);
+
+/* Bytes of S for group stride lds, or -i. */
+int64_t dg_mx_scale_bytes(int64_t lds, int64_t cols);
+
+/* (Q, S) = op(X) in `format`.  op(X) is rows x cols; transX = DG_OP_T: X is
+ * stored cols x rows.  ldx >= max(1, cols) (rows with transX).
+ *   1 transX, 2 rows, 3 cols, 4 X, 5 ldx, 6 type, 7 format, 8 Q, 9 ldq, 10 S,
+ *   11 lds, 12 stream. */
+int dg_mx_quantize(dg_op_t transX, int64_t rows, int64_t cols, const void *X, int64_t ldx, dg_elem_t type,
+                   dg_mx_t format, void *Q, int64_t ldq, void *S, int64_t lds, void *stream);
+
+/* X = the values of (Q, S), rounded once to the element type (exact in fp32
+ * and bf16 within their range; in fp16 for values that fp16 holds).
+ *   1 rows, 2 cols, 3 format, 4 Q, 5 ldq, 6 S, 7 lds, 8 X, 9 ldx, 10 type,
+ *   11 stream. */
+int dg_mx_dequantize(int64_t rows, int64_t cols, dg_mx_t format, const void *Q, int64_t ldq, const void *S,
+                     int64_t lds, void *X, int64_t ldx, dg_elem_t type, void *stream);
+
+/* C = act(alpha * A B^T + beta * C + bias): A is M x K in DG_MXFP4 or
+ * DG_MXFP8, B is N x K in DG_MXFP4, both with their blocks along K; C (and the
+ * bias, N elements, NULL for none) of type `type`; the epilogue of dg_gemm_ex.
+ * Products and sums on the scaled matrix cores with fp32 accumulators, one
+ * rounding of the result.  Two DG_MXFP4 operands are summed exactly to the
+ * fp32 rounding of each step of 64 k; with a DG_MXFP8 operand the hardware
+ * aligns the products of a step to the step's largest and drops what lies
+ * more than 2^13 below it, so an fp32 C then carries about 2.5e-6 relative
+ * error by norm (below a 16-bit C's rounding).
+ *   M == 0 or N == 0: nothing is done; K == 0 or alpha == 0: A and B are not
+ *   read, C = act(beta * C + bias); beta == 0: C is not read.
+ *   1 M, 2 N, 3 K, 4 alpha, 5 formatA, 6 A, 7 lda (bytes), 8 SA, 9 ldsa,
+ *   10 formatB, 11 B, 12 ldb (bytes), 13 SB, 14 ldsb, 15 beta, 16 C, 17 ldc,
+ *   18 type, 19 bias, 20 epilogue, 21 stream. */
+int dg_gemm_mx(int64_t M, int64_t N, int64_t K, float alpha, dg_mx_t formatA, const void *A, int64_t lda,
+               const void *SA, int64_t ldsa, dg_mx_t formatB, const void *B, int64_t ldb, const void *SB,
+               int64_t ldsb, float beta, void *C, int64_t ldc, dg_elem_t type, const void *bias,
+               dg_epilogue_t epilogue, void *stream);
+
+/* dg_gemm_mx with a forced kernel (argument 22; DG_KERNEL_AUTO: the
+ * library's choice), for tests and measurement; DG_ERR_UNSUPPORTED when it
+ * cannot run the problem.  The choice for packed operands, and the kernels'
+ * names (NULL when out of range). */
+int dg_gemm_mx_with_kernel(int64_t M, int64_t N, int64_t K, float alpha, dg_mx_t formatA, const void *A,
+                           int64_t lda, const void *SA, int64_t ldsa, dg_mx_t formatB, const void *B, int64_t ldb,
+                           const void *SB, int64_t ldsb, float beta, void *C, int64_t ldc, dg_elem_t type,
+                           const void *bias, dg_epilogue_t epilogue, void *stream, int kernel);
+int dg_gemm_mx_select(int64_t M, int64_t N, int64_t K);
+const char *dg_gemm_mx_kernel_name(int kernel);
+
+/* C = alpha * op(A) B + beta * C: A is fp16 or bf16 (typeA), stored M x K or
+ * K x M (transA); B is K x N in any MX format, its blocks along N; C of A's type
+ * or fp32 (typeC).  The products of a backward pass: dX = dY W with W kept in
+ * 4 bits (transA = DG_OP_N), dW = dY^T X with X kept in 8 bits (DG_OP_T).
+ * B's values are brought to A's type (exact for a B that was rounded from a
+ * matrix of that type; in fp16 others round, or overflow to infinity) and
+ * multiplied on the 16-bit matrix cores with fp32 sums, one rounding of the
+ * result.  Special values as dg_gemm.
+ *   splits, workspace: as dg_gemm_splitk (0: the library's choice,
+ *   dg_gemm_dq_choose; the workspace holds splits * M * N fp32 partials, see
+ *   dg_gemm_splitk_workspace_size, and is needed only when more than one
+ *   range results).
+ *   DG_ERR_UNSUPPORTED: rows of B so long that 64 of them exceed 2^31 bytes.
+ *   1 transA, 2 M, 3 N, 4 K, 5 alpha, 6 A, 7 lda, 8 typeA, 9 formatB, 10 B,
+ *   11 ldb (bytes), 12 SB, 13 ldsb, 14 beta, 15 C, 16 ldc, 17 typeC,
+ *   18 splits, 19 workspace (NULL or not 16-byte aligned), 20
+ *   workspace_bytes (too few), 21 stream. */
+int dg_gemm_dq(dg_op_t transA, int64_t M, int64_t N, int64_t K, float alpha, const void *A, int64_t lda,
+               dg_elem_t typeA, dg_mx_t formatB, const void *B, int64_t ldb, const void *SB, int64_t ldsb,
+               float beta, void *C, int64_t ldc, dg_elem_t typeC, int splits, void *workspace,
+               size_t workspace_bytes, void *stream);
+
+/* The K ranges dg_gemm_dq uses with splits = 0, or -i (1 M, 2 N, 3 K). */
+int dg_gemm_dq_choose(int64_t M, int64_t N, int64_t K);
+
+/* H = act(Z) (relu or gelu, as the epilogues of dg_gemm_ex), and Z kept in 8
+ * bits (DG_MXFP8 or DG_MXINT8) for dg_act_backward, in one pass.  H may be Z
+ * itself (with ldh = ldz).
+ *   1 rows, 2 cols, 3 Z, 4 ldz, 5 H, 6 ldh, 7 type, 8 activation, 9 format,
+ *   10 Q, 11 ldq, 12 S, 13 lds, 14 stream. */
+int dg_act_checkpoint(int64_t rows, int64_t cols, const void *Z, int64_t ldz, void *H, int64_t ldh,
+                      dg_elem_t type, dg_epilogue_t activation, dg_mx_t format, void *Q, int64_t ldq, void *S,
+                      int64_t lds, void *stream);
+
+/* dZ = dH * act'(z) with z the values of (Q, S) (kept by dg_act_checkpoint or
+ * dg_mx_quantize): relu'(z) = 1 for z > 0, else 0; gelu'(z) = Phi(z) + z phi(z).
+ * dZ may be dH itself (with ldz = ldh).  dbias (fp32, cols elements; NULL for
+ * none) receives the column sums of dZ before its rounding, in a fixed order
+ * of summation; it needs a workspace of dg_act_backward_workspace_size bytes
+ * (16-byte aligned, caller-owned, contents unspecified on return).
+ *   1 rows, 2 cols, 3 dH, 4 ldh, 5 format, 6 Q, 7 ldq, 8 S, 9 lds, 10 dZ,
+ *   11 ldz, 12 type, 13 activation, 14 dbias, 15 workspace (NULL or
+ *   misaligned while dbias is given), 16 workspace_bytes (too few), 17
+ *   stream. */
+int dg_act_backward(int64_t rows, int64_t cols, const void *dH, int64_t ldh, dg_mx_t format, const void *Q,
+                    int64_t ldq, const void *S, int64_t lds, void *dZ, int64_t ldz, dg_elem_t type,
+                    dg_epilogue_t activation, float *dbias, void *workspace, size_t workspace_bytes,
+                    void *stream);
+size_t dg_act_backward_workspace_size(int64_t rows, int64_t cols);
 
 /* Number of kernels in the table, and a static name for kernel i (NULL when
  * i is out of range).  Names read "<dtype>_<tiles>_<variant>". */

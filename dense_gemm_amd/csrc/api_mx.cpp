@@ -58,8 +58,7 @@ const MxFamily kMx[] = {
     {"mx_32x16_rows", 32, 16, 1, false},
     {"mx_64x64_tile", 64, 64, 4, true},
     {"mx_128x128_tile", 128, 128, 4, true},
-    {"mx_256x256_tile_w8", 256, 256, 4, true},
-    {"mx_256x256_tile_w4", 256, 256, 4, true},
+    {"mx_256x256_tile", 256, 256, 4, true},
 };
 constexpr int kNumMx = sizeof(kMx) / sizeof(kMx[0]);
 
@@ -71,36 +70,86 @@ bool mx_supports(int k, int64_t M, int64_t N, int64_t lda, int64_t ldb)
     return offsets_fit(lda) && offsets_fit(ldb) && tm * tn < (1 << 22);
 }
 
-int mx_choose(int64_t M, int64_t N, int64_t lda, int64_t ldb)
+// The kernel by its time (us) under a model of each: a fixed part, and a part
+// per slab (128 k, or 256 k of two mxfp4 operands) for as many rounds of tiles
+// as the compute units need (and C's way out at 4 TB/s for the 64 x 64 tile).  Fitted to back-to-back times at 32 shapes (M 1 to
+// 8192, N 1024 to 8192, K 512 to 8192); a 64 x 64 tile's units share about 270
+// tiles a round, a 128 x 128 one's 212 (two fit a unit, at less than twice the
+// speed), and a 256 x 256 one's 256, whose last round costs 0.82 when partly
+// filled.  The row kernels read B once per 16 (or 32) rows of A and their
+// own rows of A for every 16 columns.  Measured on both sides of the choice
+// (M x N x K, mxfp8 times mxfp4): 16 x 8192 x 8192 rows 15.3, tile 17.8 us;
+// 32 x 8192 x 8192 rows 22.9, tile 17.9; 64 x 2048 x 2048 rows 4.8, tile 6.8;
+// 512 x 5632 x 2048 64-tile 12.4, 128-tile 12.2; 1024 x 8192 x 8192 128-tile
+// 60.6, 256-tile 80.3; mxfp4 both, 2048 x 8192 x 4096 128-tile 46.8, 256-tile
+// 40.6.
+int mx_choose(bool a4, int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb)
 {
-    int k;
-    if (M <= 16) k = 0;
-    else if (M <= 32) k = 1;
-    else if (ceil_div(M, 128) * ceil_div(N, 128) < 256) k = 2;
-    else if (ceil_div(M, 256) * ceil_div(N, 256) < 256) k = 3;
-    else k = 4;
-    return mx_supports(k, M, N, lda, ldb) ? k : 1;
+    const double slabs = (double)ceil_div(K, a4 ? 256 : 128);
+    auto tiles = [&](int64_t b) { return (double)ceil_div(M, b) * (double)ceil_div(N, b); };
+    auto at_least_1 = [](double x) { return x > 1 ? x : 1.; };
+    // a row workgroup's start costs as much as 600 k
+    const double nk = (double)ceil_div(N, 16) * ((double)K + 600), mb = (double)M * (double)N * 2e-6;
+    const double t256 = tiles(256), full = (double)(int64_t)(t256 / 256);
+    const double cost[kNumMx] = {
+        2.5 + (1.6e-6 + (a4 ? 0.05e-6 : 0.1e-6) * (double)(M < 16 ? M : 16)) * (double)ceil_div(M, 16) * nk,
+        2.7 + 5.0e-6 * (double)ceil_div(M, 32) * nk,
+        3.1 + slabs * (a4 ? 0.28 : 0.23) * at_least_1(tiles(64) / 270) + mb / 4,
+        5.8 + slabs * (a4 ? 0.50 : 0.36) * at_least_1(tiles(128) / 212),
+        9.0 + slabs * (a4 ? 1.4 : 1.2) * (full + (t256 > full * 256 ? (full > 0 ? 0.82 : 1.) : 0.)),
+    };
+    int best = -1;
+    for (int k = 0; k < kNumMx; ++k)
+        if (mx_supports(k, M, N, lda, ldb) && (best < 0 || cost[k] < cost[best])) best = k;
+    return best;
 }
 
-// ---- the kernels of dg_gemm_dq: BM x 128 tiles ---------------------------------
-const int kDqRows[] = {32, 128, 256};
+// ---- the kernels of dg_gemm_dq -------------------------------------------------
+struct DqTile {
+    int bm, bn;
+    double fixed, slab;      // us: the fixed part, and a slab of 64 k
+};
+const DqTile kDq[] = {{32, 128, 3.0, 0.38}, {64, 128, 3.0, 0.58}, {128, 128, 4.0, 0.75}, {256, 256, 10.0, 1.38}};
+constexpr int kNumDq = sizeof(kDq) / sizeof(kDq[0]);
 
-int dq_choose(int64_t M, int64_t N)
-{
-    const int64_t tn = ceil_div(N, 128);
-    if (M <= 32) return 0;
-    return ceil_div(M, 256) * tn >= 256 ? 2 : 1;
-}
+// K ranges of `splits` (each a multiple of 64 but the last).
+int64_t dq_chunk(int64_t K, int splits) { return ceil_div(ceil_div(K, splits), 64) * 64; }
 
-// K ranges: enough workgroups to cover the 256 compute units, at least 8
-// slabs of 64 each; no split once half the units have a tile.
-int dq_splits(int64_t tiles, int64_t K)
+// Tile and K ranges by their time (us) under a model fitted to back-to-back
+// times of 21 shapes: a fixed part, and a part per slab that grows with the
+// workgroups beyond one per compute unit (0.8 of a slab for each further one,
+// whole rounds for the 256 x 256 tile, which fills a unit's LDS), and for
+// more than one range the second launch and the partials' way to memory and
+// back at 4 TB/s.  `splits` > 0 fixes the ranges.  Measured on both sides
+// (M x N x K, us): 512 x 2048 x 5632 in 4 ranges 25.9, in one 54.1; 2048 x 1024
+// x 1024 in one range 11.9, in two 23.6; 1024 x 2048 x 8192 128-tile in 4 ranges
+// 57, 64-tile in one 94; 4096^3 256-tile 109, 128-tile 134.
+void dq_choose(int64_t M, int64_t N, int64_t K, bool direct, int splits, int *tile, int *ranges)
 {
-    if (tiles >= 128) return 1;
-    int64_t s = ceil_div(K, 64) / 8;
-    const int64_t want = ceil_div(256, tiles);
-    if (s > want) s = want;
-    return s < 1 ? 1 : (int)s;
+    double best = 1e300;
+    const double out = (double)M * (double)N;
+    const int fixed_splits[] = {splits}, tried[] = {1, 2, 3, 4, 6, 8, 12, 16};
+    const int *list = splits > 0 ? fixed_splits : tried;
+    const int n = splits > 0 ? 1 : (int)(sizeof(tried) / sizeof(tried[0]));
+    for (int k = 0; k < kNumDq; ++k) {
+        if (k == 3 && !direct) continue;
+        const double tiles = (double)ceil_div(M, kDq[k].bm) * (double)ceil_div(N, kDq[k].bn);
+        for (int i = 0; i < n; ++i) {
+            const int64_t chunk = dq_chunk(K, list[i]), s = ceil_div(K, chunk);
+            // ranges of at least 4 slabs, and no more partials than 256 MiB, where the choice is free
+            if (splits == 0 && s > 1 && (chunk < 256 || (double)s * out * 4 > 268435456.0)) continue;
+            const double w = tiles * (double)s / 256, full = (double)(int64_t)w;
+            const double rounds = k == 3 ? full + (w > full ? (full > 0 ? 0.82 : 1.) : 0.) : w > 1 ? 1 + 0.8 * (w - 1) : 1;
+            // (with every unit at work on the largest tile the clock drops)
+            double t = kDq[k].fixed + (double)(chunk / 64) * kDq[k].slab * (direct ? 1. : 1.2) * rounds * (k == 3 && w > 0.9 ? 1.15 : 1.);
+            if (s > 1) t += 3.5 + (double)s * out * 8 / 4e6;
+            if (t < best) {
+                best = t;
+                *tile = k;
+                *ranges = (int)s;
+            }
+        }
+    }
 }
 
 }  // namespace
@@ -318,8 +367,8 @@ int dg_gemm_mx_with_kernel(int64_t M, int64_t N, int64_t K, float alpha, dg_mx_t
     p.ldsb = ldsb;
     p.ctype = type;
     if (!reads) return dg::launch_status(dg::scale_launcher(c_dtype(type))(p.g, (hipStream_t)stream));
-    if (kernel == DG_KERNEL_AUTO) kernel = mx_choose(M, N, lda, ldb);
-    if (!mx_supports(kernel, M, N, lda, ldb)) return DG_ERR_UNSUPPORTED;
+    if (kernel == DG_KERNEL_AUTO) kernel = mx_choose(formatA == DG_MXFP4, M, N, K, lda, ldb);
+    if (kernel < 0 || !mx_supports(kernel, M, N, lda, ldb)) return DG_ERR_UNSUPPORTED;
     const MxFamily &f = kMx[kernel];
     p.g.tiles_m = (int32_t)ceil_div(M, f.bm);
     p.g.tiles_n = (int32_t)ceil_div(N, f.bn);
@@ -335,12 +384,13 @@ int dg_gemm_mx(int64_t M, int64_t N, int64_t K, float alpha, dg_mx_t formatA, co
                                   type, bias, epilogue, stream, DG_KERNEL_AUTO);
 }
 
-int dg_gemm_mx_select(int64_t M, int64_t N, int64_t K)
+int dg_gemm_mx_select(dg_mx_t formatA, int64_t M, int64_t N, int64_t K)
 {
-    if (M < 0 || M > kMaxDim) return -1;
-    if (N < 0 || N > kMaxDim) return -2;
-    if (K < 0 || K > kMaxDim - dg::MX_GROUP) return -3;
-    return mx_choose(M, N, row_bytes(DG_MXFP8, K), row_bytes(DG_MXFP4, K));
+    if (formatA != DG_MXFP4 && formatA != DG_MXFP8) return -1;
+    if (M < 0 || M > kMaxDim) return -2;
+    if (N < 0 || N > kMaxDim) return -3;
+    if (K < 0 || K > kMaxDim - dg::MX_GROUP) return -4;
+    return mx_choose(formatA == DG_MXFP4, M, N, K, row_bytes(formatA, K), row_bytes(DG_MXFP4, K));
 }
 
 const char *dg_gemm_mx_kernel_name(int kernel) { return kernel >= 0 && kernel < kNumMx ? kMx[kernel].name : nullptr; }
@@ -351,7 +401,9 @@ int dg_gemm_dq_choose(int64_t M, int64_t N, int64_t K)
     if (N < 0 || N > kMaxDim) return -2;
     if (K < 0 || K > kMaxDim) return -3;
     if (M == 0 || N == 0 || K == 0) return 1;
-    return dq_splits(ceil_div(M, kDqRows[dq_choose(M, N)]) * ceil_div(N, 128), K);
+    int tile = 0, ranges = 1;
+    dq_choose(M, N, K, true, 0, &tile, &ranges);
+    return ranges;
 }
 
 int dg_gemm_dq(dg_op_t transA, int64_t M, int64_t N, int64_t K, float alpha, const void *A, int64_t lda,
@@ -399,13 +451,13 @@ int dg_gemm_dq(dg_op_t transA, int64_t M, int64_t N, int64_t K, float alpha, con
     const int cd = c_dtype(typeC);
     if (!reads) return dg::launch_status(dg::scale_launcher(cd)(p.g, (hipStream_t)stream));
 
-    const int k = dq_choose(M, N);
-    const int64_t tm = ceil_div(M, kDqRows[k]), tn = ceil_div(N, 128);
-    if (splits == 0) splits = dq_splits(tm * tn, K);
-    const int64_t chunk = ceil_div(ceil_div(K, splits), 64) * 64;
-    splits = (int)ceil_div(K, chunk);
-    // a slab of B (64 rows) is addressed with 32-bit byte offsets
-    if (64 * ldb >= ((int64_t)1 << 31) || tm * tn * splits >= (1 << 22)) return DG_ERR_UNSUPPORTED;
+    const int direct = aligned(A, 4) && lda % 2 == 0 && offsets_fit(lda * 2) && (transA == DG_OP_N || M % 8 == 0);
+    int k = 0;
+    // (the choice of ranges is dg_gemm_dq_choose's, which knows no alignment)
+    if (splits == 0) dq_choose(M, N, K, true, 0, &k, &splits);
+    dq_choose(M, N, K, direct, splits, &k, &splits);
+    const int64_t tm = ceil_div(M, kDq[k].bm), tn = ceil_div(N, kDq[k].bn), chunk = dq_chunk(K, splits);
+    if (tm * tn * splits >= (1 << 22)) return DG_ERR_UNSUPPORTED;    // a launch of fewer than 2^31 threads
     if (splits > 1) {
         if (workspace == nullptr || !aligned(workspace, 16)) return -19;
         if ((size_t)splits * (size_t)M * (size_t)N * 4 > workspace_bytes) return -20;
@@ -416,7 +468,6 @@ int dg_gemm_dq(dg_op_t transA, int64_t M, int64_t N, int64_t K, float alpha, con
     p.g.tiles_m = (int32_t)tm;
     p.g.tiles_n = (int32_t)tn;
     p.g.group_m = 4;
-    const int direct = aligned(A, 4) && lda % 2 == 0 && offsets_fit(lda * 2) && (transA == DG_OP_N || M % 8 == 0);
     int rc = dg::launch_status(dg::dq_gemm_launcher(typeA, k, formatB, transA, direct)(p, (hipStream_t)stream));
     if (rc == DG_OK && splits > 1) rc = dg::launch_status(dg::splitk_reduce_launcher(cd)(p.g, (hipStream_t)stream));
     return rc;

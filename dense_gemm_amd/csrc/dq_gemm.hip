@@ -9,25 +9,23 @@
 // brought to A's type, where every value of the three formats is exact, and
 // multiplied by v_mfma_f32_32x32x16 with fp32 sums.
 //
-// Per slab of 64 k, with everything fetched by direct global->LDS loads two
-// slabs ahead: A in the layout of the dense kernels, B and its scales as
-// stored (8 bytes of scales per k).  Each thread then takes 16 bytes of B
-// from LDS, converts them (one scale for all of them) and writes 16-bit
-// elements into a second buffer, once per workgroup and slab rather than
-// once per wave, while the previous slab's matrix instructions run.
+// Per slab of 64 k: A goes to LDS by direct loads, in the layout of the dense
+// kernels; B's codes are converted in registers, 16 bytes per thread and piece
+// with one scale, and written to LDS as 16-bit elements once per workgroup (not
+// once per wave that uses them).
 //
-// B's 16-bit buffer is [64 k][128 n], rows of 256 bytes: the 64-byte quad q
-// (32 n) of row k sits at quad q ^ (k & 3), and its 16-byte chunk c at chunk
+// B's 16-bit buffer is [64 k][BN], rows of BN * 2 bytes: the 64-byte quad q
+// (32 n) of row k sits at quad q ^ swz(k), and its 16-byte chunk c at chunk
 // c ^ (k & 3).  The fragment reads (ds_read_b64_tr_b16, four rows of a quad per
 // 16 lanes) see four distinct quads, and the 16 lanes of a write, which hold
-// the same chunk number of two or four rows, 16 distinct chunks.
+// the same chunk numbers of two or four rows, distinct chunks.
 #include "mx_tile.hpp"
 
 namespace dg {
 
 namespace {
 
-constexpr int DQ_BK = 64, DQ_BN = 128;
+constexpr int DQ_BK = 64;
 
 // Two 16-bit values of T from the low or high half of codes q.
 template <typename T, int FB>
@@ -75,86 +73,67 @@ struct Decode {
     }
 };
 
-// B's raw ring slot and 16-bit buffer.
-template <typename T, int FB, int NW>
+// B: codes in registers, 16-bit elements in LDS.
+template <typename T, int FB, int BN, int NW>
 struct DqOperand {
     typedef T V8 __attribute__((ext_vector_type(8)));
     typedef __attribute__((address_space(3))) V8 lds_v8_t;
-    typedef __attribute__((address_space(3))) u32x4 lds_u32x4_t;
-    typedef __attribute__((address_space(3))) uint8_t lds_u8_t;
-    static constexpr int RROW = FB == MX_FP4 ? DQ_BN / 2 : DQ_BN;      // raw bytes per k
-    static constexpr int PIECES = RROW / 16;                            // 16-byte pieces per k
-    static constexpr int RAW = DQ_BK * RROW;
-    static constexpr int RAW_BYTES = RAW + DQ_BK * 8;                   // and the scales
-    static constexpr int BYTES = DQ_BK * DQ_BN * 2;
-    static constexpr int RTOT = RAW / 1024;                             // wave-wide loads
-    static constexpr int RLOADS = RTOT < NW ? 1 : RTOT / NW;            // per wave (some twice)
-    static constexpr int LOADS = RLOADS + 1;
+    static constexpr int ROW = BN * 2;                                  // LDS bytes per k
+    static constexpr int BYTES = DQ_BK * ROW;
+    static constexpr int EPP = FB == MX_FP4 ? 32 : 16;                  // elements of a 16-byte piece
+    static constexpr int PIECES = BN / EPP;                             // pieces per k
     static constexpr int THREADS = NW * 64;
-    static constexpr int PER = (DQ_BK * PIECES + THREADS - 1) / THREADS;   // pieces per thread
-    const char *base, *sbase;
-    int64_t ldq;
-    uint32_t off[RLOADS], soff;
-    int wave, lane;
+    static constexpr int PER = DQ_BK * PIECES / THREADS;                // pieces per thread
+    static constexpr int CH = EPP / 8;                                  // 16-byte output chunks per piece
+    static_assert(PER >= 1 && PER * THREADS == DQ_BK * PIECES, "whole pieces per thread");
 
-    __device__ __forceinline__ void init(const MxGemmParams &p, int k_begin, int n0, int w, int l)
+    __device__ static __forceinline__ int swz(int k) { return BN >= 128 ? k & 3 : (k >> 1) & 1; }
+
+    const uint8_t *q0, *s0;      // this thread's first piece and its scale, of the current slab
+    int64_t ldq;
+    int tid, lane;
+    u32x4 raw[PER];
+    uint32_t byte[PER];
+
+    __device__ __forceinline__ void init(const MxGemmParams &p, int k_begin, int n0, int t)
     {
-        wave = w;
-        lane = l;
+        tid = t;
+        lane = t & 63;
         ldq = p.g.ldb;
-        base = (const char *)p.g.B + (int64_t)k_begin * ldq + (FB == MX_FP4 ? n0 / 2 : n0);
-        sbase = (const char *)p.SB + ((int64_t)(n0 / MX_GROUP) * p.ldsb + k_begin) * 8;
-        offsets(DQ_BK);
+        const int n = n0 + (t % PIECES) * EPP;
+        const int64_t k = k_begin + t / PIECES;
+        q0 = (const uint8_t *)p.g.B + k * ldq + (FB == MX_FP4 ? n / 2 : n);
+        s0 = p.SB + ((int64_t)(n / MX_GROUP) * p.ldsb + k) * 8 + (n % MX_GROUP) / 32;
     }
-    // byte offsets of this lane's loads; rows at or past krem come from the
-    // slab's last valid row (their elements are zeroed on conversion)
-    __device__ __forceinline__ void offsets(int krem)
+    // piece i of the current slab; WHOLE: every k of the slab lies before K,
+    // else rows at or past krem are zeros
+    template <bool WHOLE>
+    __device__ __forceinline__ void load(int i, int krem)
     {
-#pragma unroll
-        for (int i = 0; i < RLOADS; ++i) {
-            const int b = ((i * NW + wave) % RTOT) * 1024 + lane * 16;
-            const int k = b / RROW;
-            off[i] = (uint32_t)((int64_t)(k < krem ? k : krem - 1) * ldq + b % RROW);
+        const int dk = i * (THREADS / PIECES);
+        if (WHOLE || tid / PIECES + dk < krem) {
+            raw[i] = *(const u32x4 *)(q0 + dk * ldq);
+            byte[i] = s0[dk * 8];
+        } else {
+            raw[i] = (u32x4){0u, 0u, 0u, 0u};
+            byte[i] = 127;
         }
-        const int d = (wave & 1) * 64 + lane;
-        soff = (uint32_t)((d / 2 < krem ? d / 2 : krem - 1) * 8 + (d & 1) * 4);
     }
-    __device__ __forceinline__ void issue(lds_char_t *raw)
+    __device__ __forceinline__ void advance()
     {
-#pragma unroll
-        for (int i = 0; i < RLOADS; ++i)
-            load_lds16(off[i], buffer_rsrc(base), (unsigned)(uintptr_t)(raw + ((i * NW + wave) % RTOT) * 1024));
-        load_lds4(soff, buffer_rsrc(sbase), (unsigned)(uintptr_t)(raw + RAW + (wave & 1) * 256));
-        base += DQ_BK * ldq;
-        sbase += DQ_BK * 8;
+        q0 += DQ_BK * ldq;
+        s0 += DQ_BK * 8;
     }
-    // this thread's pieces of a raw slot into the 16-bit buffer; blk0: the
-    // tile's first block within its group
-    __device__ __forceinline__ void convert(const lds_char_t *raw, lds_char_t *dst, int blk0, int krem) const
+    // output chunk c of piece i into the buffer
+    __device__ __forceinline__ void convert(lds_char_t *buf, int i, int c) const
     {
-        const int tid = wave * 64 + lane;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int t = i * THREADS + tid;
-            if (DQ_BK * PIECES % THREADS != 0 && t >= DQ_BK * PIECES) break;
-            const int k = t / PIECES, pc = t % PIECES;
-            const u32x4 q = *(const lds_u32x4_t *)(raw + t * 16);
-            const int blk = FB == MX_FP4 ? pc : pc >> 1;               // 32 n: the quad, too
-            const float sc = mx_scale(*(const lds_u8_t *)(raw + RAW + k * 8 + blk0 + blk));
-            lds_char_t *row = dst + k * (DQ_BN * 2) + ((blk ^ (k & 3)) << 6);
-            constexpr int CH = FB == MX_FP4 ? 4 : 2;                   // 16-byte chunks of the output
-#pragma unroll
-            for (int c = 0; c < CH; ++c) {
-                V8 v;
-                if constexpr (FB == MX_FP4) v = Decode<T, FB>::eight(q[c], 0, sc);
-                else v = Decode<T, FB>::eight(q[2 * c], q[2 * c + 1], sc);
-                if (k >= krem)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] = (T)0.f;
-                const int ch = FB == MX_FP4 ? c : 2 * (pc & 1) + c;
-                *(lds_v8_t *)(row + ((ch ^ (k & 3)) << 4)) = v;
-            }
-        }
+        const int k = tid / PIECES + i * (THREADS / PIECES), pc = tid % PIECES;
+        const int quad = pc * EPP / 32, ch = FB == MX_FP4 ? c : 2 * (pc & 1) + c;
+        const float sc = mx_scale(byte[i]);
+        V8 v;
+        if constexpr (FB == MX_FP4) v = Decode<T, FB>::eight(raw[i][c], 0, sc);
+        else v = Decode<T, FB>::eight(raw[i][2 * c], raw[i][2 * c + 1], sc);
+        *(lds_v8_t *)(buf + k * ROW + ((quad ^ swz(k)) << 6) + ((ch ^ (k & 3)) << 4)) = v;
     }
     // columns b0 .. b0+31, step kk of 16 k (the transposing read: in each
     // 16-lane group, lanes 4t .. 4t+3 name row t of a 4 x 16 block)
@@ -163,86 +142,172 @@ struct DqOperand {
         const int g = lane >> 4, t = (lane & 15) >> 2, s = lane & 3;
         const int k0 = 16 * kk + 8 * (g >> 1) + t;
         const int ch = 2 * (g & 1) + (s >> 1);
-        const lds_char_t *p0 = buf + k0 * (DQ_BN * 2) + (((b0 >> 5) ^ t) << 6) + ((ch ^ t) << 4) + (s & 1) * 8;
+        const lds_char_t *p0 = buf + k0 * ROW + (((b0 >> 5) ^ swz(t)) << 6) + ((ch ^ t) << 4) + (s & 1) * 8;
         const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t *)p0);
-        const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t *)(p0 + 4 * (DQ_BN * 2)));
+        const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t *)(p0 + 4 * ROW));
         typedef short i16x8 __attribute__((ext_vector_type(8)));
         const i16x8 v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
         return __builtin_bit_cast(V8, v);
     }
 };
 
-// A through registers, for rows that the direct loads do not take (2-byte
-// aligned, or a ragged m-contiguous extent): 16-byte pieces by unaligned
-// vector loads, into the direct loads' LDS layout.
+// A's slab in LDS, 16-byte pieces in the order of the direct loads: piece
+// (i * NW + wave) * 64 + lane holds 8 elements that begin at (mn, k) = at(i).
+//   k-contiguous (A stored M x K): the layout of the dense kernels, [BM][64]
+//     with chunk c of row r at c ^ ((r >> 1) & 7);
+//   m-contiguous (K x M): [64][BM], quad q of row k at q ^ swz(k) as in B's
+//     buffer, any BM that is a multiple of 32.
 template <typename T, int BM, bool KCONT, int NW>
-struct RegOperand {
-    typedef PipeOperandH<T, BM, KCONT, NW, 16> Lay;
+struct DqA {
     typedef T V8 __attribute__((ext_vector_type(8)));
     typedef V8 __attribute__((aligned(2))) V8u;
-    V8 r[Lay::LOADS];
-    const T *g;
+    typedef __attribute__((address_space(3))) V8 lds_v8_t;
+    static constexpr int BYTES = BM * DQ_BK * 2;
+    static constexpr int LOADS = BYTES / (NW * 1024);
+    static_assert(LOADS * NW * 1024 == BYTES, "whole loads");
+    static constexpr int ROW = KCONT ? DQ_BK * 2 : BM * 2;
+    const T *base;               // the current slab's tile origin
     int64_t ld;
+    uint32_t off[LOADS];         // direct loads: byte offsets from base
+    V8 r[LOADS];                 // through registers
     int mn0, ext, wave, lane;
 
-    __device__ __forceinline__ void init(const T *p, int64_t l, int m0, int e, int w, int ln)
+    __device__ static __forceinline__ int swz(int k) { return BM % 128 == 0 ? k & 3 : BM % 64 == 0 ? (k >> 1) & 1 : 0; }
+
+    __device__ __forceinline__ void at(int i, int &mn, int &k) const
     {
-        g = p;
+        const int id = (i * NW + wave) * 64 + lane;
+        if constexpr (KCONT) {
+            mn = id >> 3;
+            k = ((id & 7) ^ ((mn >> 1) & 7)) * 8;
+        } else {
+            const int p = id % (ROW / 16);
+            k = id / (ROW / 16);
+            mn = ((p >> 2) ^ swz(k)) * 32 + (p & 3) * 8;
+        }
+    }
+    // direct: a row (or piece) past the matrix is fetched from the last one; it
+    // only feeds outputs that are never stored
+    __device__ __forceinline__ void init(const T *g, int64_t l, int m0, int e, int w, int ln, bool direct)
+    {
         ld = l;
         mn0 = m0;
         ext = e;
         wave = w;
         lane = ln;
+        base = KCONT ? g + (int64_t)m0 * l : g + m0;
+        if (!direct) return;
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) {
+            int mn, k;
+            at(i, mn, k);
+            if constexpr (KCONT) {
+                const int row = m0 + mn < e ? mn : e - 1 - m0;
+                off[i] = (uint32_t)(((int64_t)row * l + k) * 2);
+            } else {
+                const int col = m0 + mn < e ? mn : e - 8 - m0;
+                off[i] = (uint32_t)(((int64_t)k * l + col) * 2);
+            }
+        }
     }
-    __device__ __forceinline__ void load(int k0, int Kl)
+    __device__ __forceinline__ void advance() { base += KCONT ? DQ_BK : DQ_BK * ld; }
+    __device__ __forceinline__ void issue_one(lds_char_t *st, int i)
+    {
+        load_lds16(off[i], buffer_rsrc((const char *)base), (unsigned)(uintptr_t)(st + (i * NW + wave) * 1024));
+    }
+    // through registers, k at or past krem and rows past the matrix as zeros;
+    // rows need be aligned to their elements only
+    __device__ __forceinline__ void load(int krem)
     {
 #pragma unroll
-        for (int i = 0; i < Lay::LOADS; ++i) {
-            const int rbase = (i * NW + wave) * Lay::ROWS_PER_LOAD;
-            const T *src;
-            int valid;
-            if constexpr (KCONT) {
-                const int row = rbase + (lane >> 3), c = (lane & 7) ^ ((row >> 1) & 7);
-                src = g + (int64_t)(mn0 + row) * ld + k0 + c * 8;
-                valid = mn0 + row < ext ? Kl - k0 - c * 8 : 0;
-            } else {
-                const int k = rbase + lane / (Lay::ROW_BYTES / 16), p = lane % (Lay::ROW_BYTES / 16);
-                const int col = mn0 + ((p >> 2) ^ Lay::swz(k)) * 32 + (p & 3) * 8;
-                src = g + (int64_t)(k0 + k) * ld + col;
-                valid = k0 + k < Kl ? ext - col : 0;
-            }
+        for (int i = 0; i < LOADS; ++i) {
+            int mn, k;
+            at(i, mn, k);
+            const T *src = base + (KCONT ? (int64_t)mn * ld + k : (int64_t)k * ld + mn);
+            const int valid = KCONT ? (mn0 + mn < ext ? krem - k : 0) : (k < krem ? ext - mn0 - mn : 0);
             if (valid >= 8) {
                 r[i] = *(const V8u *)src;
             } else {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) r[i][e] = e < valid ? src[e] : (T)0.f;
+                for (int e = 0; e < 8; ++e) {
+                    T x = (T)0.f;
+                    if (e < valid) x = src[e];
+                    r[i][e] = x;
+                }
             }
         }
     }
     __device__ __forceinline__ void store(lds_char_t *st) const
     {
 #pragma unroll
-        for (int i = 0; i < Lay::LOADS; ++i)
-            *(__attribute__((address_space(3))) V8 *)(st + (i * NW + wave) * 1024 + lane * 16) = r[i];
+        for (int i = 0; i < LOADS; ++i) *(lds_v8_t *)(st + (i * NW + wave) * 1024 + lane * 16) = r[i];
+    }
+    // the same for a whole slab of a matrix of at least 8 m, without a branch
+    // (which would wait for the loads): rows past the matrix come from its
+    // last one; an m-contiguous piece that crosses the end is read from the
+    // last 8 elements and moved to its place when it is stored
+    __device__ __forceinline__ void load_whole()
+    {
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) {
+            int mn, k;
+            at(i, mn, k);
+            const int last = ext - mn0 - (KCONT ? 1 : 8);
+            const int64_t m = mn < last ? mn : last;
+            r[i] = *(const V8u *)(base + (KCONT ? m * ld + k : (int64_t)k * ld + m));
+        }
+    }
+    __device__ __forceinline__ void store_whole(lds_char_t *st) const
+    {
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) {
+            V8 x = r[i];
+            if constexpr (!KCONT) {
+                int mn, k;
+                at(i, mn, k);
+                const int n = mn - (ext - mn0 - 8);      // elements to drop, when above 0
+                u32x4 w = __builtin_bit_cast(u32x4, x);
+                w = n > 0 && (n & 4) ? (u32x4){w[2], w[3], 0u, 0u} : w;
+                w = n > 0 && (n & 2) ? (u32x4){w[1], w[2], w[3], 0u} : w;
+                w = n > 0 && (n & 1) ? (u32x4){w[0] >> 16 | w[1] << 16, w[1] >> 16 | w[2] << 16, w[2] >> 16 | w[3] << 16, w[3] >> 16}
+                                     : w;
+                x = __builtin_bit_cast(V8, w);
+            }
+            *(lds_v8_t *)(st + (i * NW + wave) * 1024 + lane * 16) = x;
+        }
+    }
+    // rows b0 .. b0+31, step kk of 16 k
+    __device__ __forceinline__ V8 frag(const lds_char_t *st, int b0, int kk) const
+    {
+        if constexpr (KCONT) {
+            const int row = b0 + (lane & 31), c = 2 * kk + (lane >> 5);
+            return *(const lds_v8_t *)(st + row * ROW + ((c ^ ((row >> 1) & 7)) << 4));
+        } else {
+            const int g = lane >> 4, t = (lane & 15) >> 2, s = lane & 3;
+            const int k0 = 16 * kk + 8 * (g >> 1) + t;
+            const lds_char_t *p0 = st + k0 * ROW + (((b0 >> 5) ^ swz(t)) << 6) + (16 * (g & 1) + 4 * s) * 2;
+            const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t *)p0);
+            const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t *)(p0 + 4 * ROW));
+            typedef short i16x8 __attribute__((ext_vector_type(8)));
+            const i16x8 v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+            return __builtin_bit_cast(V8, v);
+        }
     }
 };
 
 // DIRECT: A by direct loads (4-byte aligned rows, an m-contiguous extent of
 // whole 16-byte pieces), else through registers.
-template <typename T, int FB, bool TA, bool DIRECT, int BM, int WM, int WN>
-__global__ __launch_bounds__(64 * (BM / WM) * (DQ_BN / WN), 2) void dq_gemm_kernel(MxGemmParams p)
+template <typename T, int FB, bool TA, bool DIRECT, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), 2) void dq_gemm_kernel(MxGemmParams p)
 {
-    constexpr int WAVES_N = DQ_BN / WN, NW = (BM / WM) * WAVES_N;
-    constexpr int TM = WM / 32, TN = WN / 32, KPW = DQ_BK / 16;
-    typedef PipeOperandH<T, BM, !TA, NW, 16> OpA;
-    typedef RegOperand<T, BM, !TA, NW> RegA;
-    typedef DqOperand<T, FB, NW> OpB;
+    constexpr int WAVES_N = BN / WN, NW = (BM / WM) * WAVES_N;
+    constexpr int TM = WM / 32, TN = WN / 32, NM = TM * TN, KPW = DQ_BK / 16;
+    typedef DqA<T, BM, !TA, NW> OpA;
+    typedef DqOperand<T, FB, BN, NW> OpB;
     typedef T V8 __attribute__((ext_vector_type(8)));
-    constexpr int SA = 3, SR = 3;                      // stages of A and of raw B
-    constexpr int LOADS = (DIRECT ? OpA::LOADS : 0) + OpB::LOADS;
-    constexpr int A_AT = 0, B_AT = SA * OpA::BYTES, R_AT = B_AT + 2 * OpB::BYTES;
-    constexpr int SMEM = R_AT + SR * OpB::RAW_BYTES;
-    static_assert(SMEM <= 160 * 1024 && NW * kEpiBytes<WN> <= SMEM, "LDS");
+    constexpr int B_AT = 2 * OpA::BYTES, RING = B_AT + 2 * OpB::BYTES, EPI = NW * kEpiBytes<WN>;
+    constexpr int SMEM = RING > EPI ? RING : EPI;
+    static_assert(SMEM <= 160 * 1024, "LDS");
     __shared__ __attribute__((aligned(1024))) char smem_raw[SMEM];
     lds_char_t *smem = (lds_char_t *)smem_raw;
 
@@ -252,32 +317,14 @@ __global__ __launch_bounds__(64 * (BM / WM) * (DQ_BN / WN), 2) void dq_gemm_kern
     int bid, split, k_begin, Kl, tm, tn;
     split_of(p.g, bid, split, k_begin, Kl);
     tile_coords(bid, p.g, tm, tn);
-    const int m0 = tm * BM, n0 = tn * DQ_BN;
+    const int m0 = tm * BM, n0 = tn * BN;
     const int nk = (Kl + DQ_BK - 1) / DQ_BK, krem = Kl - (nk - 1) * DQ_BK;
-    const int blk0 = (n0 % MX_GROUP) / 32;
 
     OpA ga;
-    RegA ra;
     OpB gb;
-    const T *A = (const T *)p.g.A + (TA ? (int64_t)k_begin * p.g.lda : (int64_t)k_begin);
-    if constexpr (DIRECT) ga.init(A, p.g.lda, m0, p.g.M, wave, lane);
-    else ra.init(A, p.g.lda, m0, p.g.M, wave, lane);
-    gb.init(p, k_begin, n0, wave, lane);
-
-    auto a_at = [&](int s) { return smem + A_AT + (s % SA) * OpA::BYTES; };
-    auto b_at = [&](int s) { return smem + B_AT + (s & 1) * OpB::BYTES; };
-    auto r_at = [&](int s) { return smem + R_AT + (s % SR) * OpB::RAW_BYTES; };
-    auto issue_a = [&](int s) {
-        if constexpr (DIRECT) {
-            if (s == nk - 1 && krem < DQ_BK) ga.issue_tail(a_at(s), wave, lane, krem);
-            else ga.issue(a_at(s), wave);
-        }
-    };
-    auto issue_r = [&](int s) {
-        if (s == nk - 1 && krem < DQ_BK) gb.offsets(krem);
-        gb.issue(r_at(s));
-    };
-    auto convert = [&](int s) { gb.convert(r_at(s), b_at(s), blk0, s == nk - 1 ? krem : DQ_BK); };
+    ga.init((const T *)p.g.A + (TA ? (int64_t)k_begin * p.g.lda : (int64_t)k_begin), p.g.lda, m0, p.g.M, wave, lane,
+            DIRECT);
+    gb.init(p, k_begin, n0, wave * 64 + lane);
 
     f32x16 acc[TM][TN];
 #pragma unroll
@@ -287,82 +334,156 @@ __global__ __launch_bounds__(64 * (BM / WM) * (DQ_BN / WN), 2) void dq_gemm_kern
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
 
-    // prologue: raw slabs 0 .. SR-1, A slabs 0 .. SA-2, slab 0 converted
+    auto a_at = [&](int s) { return smem + (s & 1) * OpA::BYTES; };
+    auto b_at = [&](int s) { return smem + B_AT + (s & 1) * OpB::BYTES; };
+    V8 fa[2][TM], fb[2][TN];
+    auto frag = [&](int set, int s, int step, int f) {
+        if (f < TM) fa[set][f] = ga.frag(a_at(s), wm0 + 32 * f, step);
+        else fb[set][f - TM] = gb.frag(b_at(s), wn0 + 32 * (f - TM), step);
+    };
+    // A through registers without a branch: a whole slab, and 8 m at least
+    auto whole = [&](int s) { return p.g.M >= 8 && (s < nk - 1 || krem == DQ_BK); };
+    // a slab at once (the prologue and the end): A by direct loads into
+    // its stage (a short last slab through registers), or into registers until
+    // the slab is converted
+    auto load = [&](int s) {
+        const int rem = s == nk - 1 ? krem : DQ_BK;
+        if (!DIRECT && whole(s)) {
+            ga.load_whole();
+        } else if (!DIRECT) {
+            ga.load(rem);
+        } else if (rem < DQ_BK) {
+            ga.load(rem);
+            ga.store(a_at(s));
+        } else {
 #pragma unroll
-    for (int s = 0; s < SR; ++s)
-        if (s < nk) issue_r(s);
+            for (int i = 0; i < OpA::LOADS; ++i) ga.issue_one(a_at(s), i);
+        }
+        ga.advance();
 #pragma unroll
-    for (int s = 0; s < SA - 1; ++s)
-        if (s < nk) issue_a(s);
-    if constexpr (!DIRECT) {
-        ra.load(0, Kl);
-        ra.store(a_at(0));
-        if (nk > 1) ra.load(DQ_BK, Kl);
-    }
+        for (int i = 0; i < OpB::PER; ++i) gb.template load<false>(i, rem);
+        gb.advance();
+    };
+    auto convert = [&](int s) {
+        if (!DIRECT && whole(s)) ga.store_whole(a_at(s));
+        else if (!DIRECT) ga.store(a_at(s));
+#pragma unroll
+        for (int i = 0; i < OpB::PER; ++i)
+#pragma unroll
+            for (int c = 0; c < OpB::CH; ++c) gb.convert(b_at(s), i, c);
+    };
+
+    load(0);
+    convert(0);
+    if (nk > 1) load(1);
     wait_vmcnt<0>();
     __syncthreads();
-    convert(0);
+#pragma unroll
+    for (int f = 0; f < TM + TN; ++f) frag(0, 0, 0, f);
 
-    for (int kt = 0; kt < nk; ++kt) {
-        // A's slab kt and raw slab kt+1 (loaded two steps ago) have landed, slab
-        // kt is converted, and every wave is done with A's slab kt-1, raw slab
-        // kt and B's slab kt-1
-        if (kt + 2 < nk) wait_vmcnt<LOADS>();
-        else wait_vmcnt<0>();
-        __syncthreads();
-        if (kt + SA - 1 < nk) issue_a(kt + SA - 1);
-        if (kt + SR < nk) issue_r(kt + SR);
-        if constexpr (!DIRECT) {
-            if (kt + 1 < nk) ra.store(a_at(kt + 1));
-            if (kt + 2 < nk) ra.load((kt + 2) * DQ_BK, Kl);
-        }
-        const lds_char_t *sa = a_at(kt), *sb = b_at(kt);
-        V8 fa[KPW][TM], fb[KPW][TN];
+    // Slab kt.  Fragments are double-buffered per step of 16 k.  The barrier
+    // sits before the last step: by then slab kt+1's A has landed and its B is
+    // converted (during step 2, so that the loads have three steps to arrive);
+    // the last step runs from registers while the first fragments of slab kt+1
+    // are read and slab kt+2 is loaded.  FAST: slabs kt+1 and kt+2 exist and
+    // are whole, so the conversion and the loads are spread between the matrix
+    // instructions.
+    auto slab = [&](auto fast_tag, int kt) {
+        constexpr bool FAST = decltype(fast_tag)::value;
+        constexpr int NC = OpB::PER * OpB::CH, cur = (KPW - 1) & 1;
 #pragma unroll
-        for (int s = 0; s < KPW; ++s) {
-#pragma unroll
-            for (int i = 0; i < TM; ++i) fa[s][i] = ga.frag(sa, wm0 + 32 * i, s, lane);
-#pragma unroll
-            for (int j = 0; j < TN; ++j) fb[s][j] = gb.frag(sb, wn0 + 32 * j, s);
-        }
-        if (kt + 1 < nk) convert(kt + 1);
-#pragma unroll
-        for (int s = 0; s < KPW; ++s)
+        for (int s = 0; s + 1 < KPW; ++s)
 #pragma unroll
             for (int i = 0; i < TM; ++i)
 #pragma unroll
-                for (int j = 0; j < TN; ++j) acc[i][j] = mfma_32x32x16(fa[s][i], fb[s][j], acc[i][j]);
-    }
+                for (int j = 0; j < TN; ++j) {
+                    const int m = i * TN + j;
+#pragma unroll
+                    for (int f = 0; f < TM + TN; ++f)
+                        if (f * NM / (TM + TN) == m) frag((s & 1) ^ 1, kt, s + 1, f);
+                    if (FAST && s == KPW - 2) {
+                        if (!DIRECT && m == 0) ga.store_whole(a_at(kt + 1));
+#pragma unroll
+                        for (int c = 0; c < NC; ++c)
+                            if (c * NM / NC == m) gb.convert(b_at(kt + 1), c / OpB::CH, c % OpB::CH);
+                    }
+                    acc[i][j] = mfma_32x32x16(fa[s & 1][i], fb[s & 1][j], acc[i][j]);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+        if (!FAST && kt + 1 < nk) convert(kt + 1);
+        wait_vmcnt<0>();
+        __syncthreads();
+        if (!FAST && kt + 2 < nk) load(kt + 2);
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                const int m = i * TN + j;
+                if constexpr (FAST) {
+#pragma unroll
+                    for (int l = 0; l < OpB::PER; ++l)
+                        if (l * NM / OpB::PER == m) gb.template load<true>(l, DQ_BK);
+                    if constexpr (DIRECT) {
+#pragma unroll
+                        for (int l = 0; l < OpA::LOADS; ++l)
+                            if (l * NM / OpA::LOADS == m) ga.issue_one(a_at(kt), l);
+                    } else {
+                        if (m == 0) ga.load_whole();
+                    }
+                }
+                // (after the last slab these reads fetch a stale stage, never used)
+#pragma unroll
+                for (int f = 0; f < TM + TN; ++f)
+                    if (f * NM / (TM + TN) == m) frag(cur ^ 1, kt + 1, 0, f);
+                acc[i][j] = mfma_32x32x16(fa[cur][i], fb[cur][j], acc[i][j]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        if constexpr (FAST) {
+            ga.advance();
+            gb.advance();
+        }
+    };
+    int kt = 0;
+    int nfast = (krem == DQ_BK ? nk : nk - 1) - 2;
+    if (!DIRECT && !whole(0)) nfast = 0;
+    for (; kt < nfast; ++kt) slab(std::true_type(), kt);
+    for (; kt < nk; ++kt) slab(std::false_type(), kt);
 
     __syncthreads();  // every wave is done with the ring
     store_tile<TM, TN>(p, smem + wave * kEpiBytes<WN>, acc, m0 + wm0, n0 + wn0, lane, split);
 }
 
-template <typename T, int FB, bool TA, bool DIRECT, int BM, int WM, int WN>
+template <typename T, int FB, bool TA, bool DIRECT, int BM, int BN, int WM, int WN>
 hipError_t launch_dq(const MxGemmParams &p, hipStream_t s)
 {
     const unsigned nwg = (unsigned)p.g.tiles_m * (unsigned)p.g.tiles_n * (unsigned)p.g.splits;
     MxGemmParams arg = p;
     void *args[] = {&arg};
-    return hipLaunchKernel((const void *)&dq_gemm_kernel<T, FB, TA, DIRECT, BM, WM, WN>, dim3(nwg),
-                           dim3(64 * (BM / WM) * (DQ_BN / WN)), args, 0, s);
+    return hipLaunchKernel((const void *)&dq_gemm_kernel<T, FB, TA, DIRECT, BM, BN, WM, WN>, dim3(nwg),
+                           dim3(64 * (BM / WM) * (BN / WN)), args, 0, s);
 }
 
 }  // namespace
 
 // [config][format][transA][direct]
-#define DG_DQ4(T, FB, BM, WM, WN)                                                                   \
-    {{launch_dq<T, FB, false, false, BM, WM, WN>, launch_dq<T, FB, false, true, BM, WM, WN>},       \
-     {launch_dq<T, FB, true, false, BM, WM, WN>, launch_dq<T, FB, true, true, BM, WM, WN>}}
-#define DG_DQ12(T, BM, WM, WN)                                                                      \
-    {DG_DQ4(T, MX_FP4, BM, WM, WN), DG_DQ4(T, MX_FP8, BM, WM, WN), DG_DQ4(T, MX_INT8, BM, WM, WN)}
+#define DG_DQ4(T, FB, ...)                                                                          \
+    {{launch_dq<T, FB, false, false, __VA_ARGS__>, launch_dq<T, FB, false, true, __VA_ARGS__>},     \
+     {launch_dq<T, FB, true, false, __VA_ARGS__>, launch_dq<T, FB, true, true, __VA_ARGS__>}}
+// A through registers: not on the 256 x 256 tile, where it would spill
+#define DG_DQ4D(T, FB, ...)                                                                         \
+    {{nullptr, launch_dq<T, FB, false, true, __VA_ARGS__>}, {nullptr, launch_dq<T, FB, true, true, __VA_ARGS__>}}
+#define DG_DQ12D(T, ...)                                                                            \
+    {DG_DQ4D(T, MX_FP4, __VA_ARGS__), DG_DQ4D(T, MX_FP8, __VA_ARGS__), DG_DQ4D(T, MX_INT8, __VA_ARGS__)}
+#define DG_DQ12(T, ...)                                                                             \
+    {DG_DQ4(T, MX_FP4, __VA_ARGS__), DG_DQ4(T, MX_FP8, __VA_ARGS__), DG_DQ4(T, MX_INT8, __VA_ARGS__)}
 template <typename T>
 mx_launch_fn dq_launcher_of(int config, int format, int ta, int direct)
 {
     static const mx_launch_fn table[][3][2][2] = {
-        DG_DQ12(T, 32, 32, 32),
-        DG_DQ12(T, 128, 64, 32),
-        DG_DQ12(T, 256, 64, 64),
+        DG_DQ12(T, 32, 128, 32, 32),
+        DG_DQ12(T, 64, 128, 32, 64),
+        DG_DQ12(T, 128, 128, 64, 64),
+        DG_DQ12D(T, 256, 256, 128, 64),
     };
     return table[config][format][ta][direct];
 }

@@ -147,10 +147,10 @@ __device__ __forceinline__ void mx_decode8(u32x2 q, uint32_t byte, float (&v)[8]
             v[4 * h + 3] = __builtin_amdgcn_cvt_f32_fp8((int)q[h], 3) * sc;
         }
     } else {
-        // q/64 first (exact), so that no scale needs to go below 2^-127
+        // the scale of one 64th: 2^-133 at the least, an exact subnormal
+        const float s64 = sc * 0.015625f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            v[i] = (float)((int32_t)(q[i >> 2] << (24 - 8 * (i & 3))) >> 24) * 0.015625f * sc;
+        for (int i = 0; i < 8; ++i) v[i] = (float)((int32_t)(q[i >> 2] << (24 - 8 * (i & 3))) >> 24) * s64;
     }
 }
 

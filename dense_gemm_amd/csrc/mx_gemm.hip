@@ -137,7 +137,7 @@ struct MxScales {
 // slab STAGES ahead is loaded into the stage just finished (A's loads there,
 // B's and the scales' during the following step).
 template <int FA, int BM, int BN, int WM, int WN, int STAGES>
-__global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), WM == 128 && WN == 128 ? 1 : 2) void mx_gemm_kernel(MxGemmParams p)
+__global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), 2) void mx_gemm_kernel(MxGemmParams p)
 {
     constexpr int WAVES_N = BN / WN, NW = (BM / WM) * WAVES_N;
     constexpr int TM = WM / 32, TN = WN / 32, NM = TM * TN;
@@ -369,8 +369,7 @@ __global__ __launch_bounds__(512) void mx_skinny_kernel(MxGemmParams p)
     f32x4 acc[MT];
 #pragma unroll
     for (int t = 0; t < MT; ++t) acc[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
-    // U of the wave's groups at a time, all loads first; a group past the end
-    // is read from the last one and left out of the sum
+    // U of the wave's groups at a time, all loads first
     constexpr int U = MT == 1 ? 4 : 2;
     for (int g0 = wave; g0 < groups; g0 += NWV * U) {
         Frag<MX_FP4> b[U][2];
@@ -378,7 +377,8 @@ __global__ __launch_bounds__(512) void mx_skinny_kernel(MxGemmParams p)
         uint64_t ub[U], ua[U][MT];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int64_t g = g0 + u * NWV < groups ? g0 + u * NWV : groups - 1;
+            const int64_t g = g0 + u * NWV;
+            if (g >= groups) break;
             ub[u] = *(const uint64_t *)(SB + g * p.ldsb * 8);
 #pragma unroll
             for (int s = 0; s < 2; ++s) b[u][s].v = *(const i32x4 *)(B + g * 128 + s * 64);
@@ -471,7 +471,6 @@ mx_launch_fn mx_gemm_launcher(int config, int format_a)
         {launch_tile<MX_FP4, 64, 64, 32, 32, 4>, launch_tile<MX_FP8, 64, 64, 32, 32, 4>},
         {launch_tile<MX_FP4, 128, 128, 64, 64, 2>, launch_tile<MX_FP8, 128, 128, 64, 64, 3>},
         {launch_tile<MX_FP4, 256, 256, 128, 64, 2>, launch_tile<MX_FP8, 256, 256, 128, 64, 2>},
-        {launch_tile<MX_FP4, 256, 256, 128, 128, 2>, launch_tile<MX_FP8, 256, 256, 128, 128, 2>},
     };
     return table[config][format_a == MX_FP8];
 }

@@ -111,7 +111,7 @@ __host__ __device__ __forceinline__ int64_t row_items(const MxParams &p)
 
 __host__ __device__ __forceinline__ int64_t trans_items(const MxParams &p)
 {
-    return (p.rows + 31) / 32 * mx_groups(p.cols);
+    return (p.rows + 63) / 64 * mx_groups(p.cols);
 }
 
 template <typename T, int FORMAT>
@@ -127,36 +127,39 @@ __global__ __launch_bounds__(256) void mx_quantize_kernel(MxParams p)
     }
 }
 
-// X stored cols x rows: a workgroup rounds 256 k of 32 rows (one scale
-// group), through LDS: the loads run along the stored rows (lanes along n),
-// then each thread takes one block of 32 k of one row.  Rows of the LDS tile
-// are padded by one word, so the column reads of 32 lanes fall on distinct
-// banks.
+// X stored cols x rows: a workgroup rounds 256 k of 64 rows (one scale
+// group), through LDS: a wave loads 64 consecutive n of one k at a time, all 32
+// of its loads in flight together, then each thread takes one block of 32 k of
+// one row.  Rows of the LDS tile are padded by one word, so the writes and the
+// column reads of 64 lanes fall on distinct banks.
 template <typename T, int FORMAT>
-__global__ __launch_bounds__(256) void mx_quantize_t_kernel(MxParams p)
+__global__ __launch_bounds__(512) void mx_quantize_t_kernel(MxParams p)
 {
-    __shared__ float tile[MX_GROUP][33];
-    const int64_t nb = (p.rows + 31) / 32, items = trans_items(p);
-    const int tid = threadIdx.x, n = tid & 31, kq = tid >> 5;
+    __shared__ float tile[MX_GROUP][65];
+    const int64_t nb = (p.rows + 63) / 64, items = trans_items(p);
+    const int tid = threadIdx.x, n = tid & 63, kq = tid >> 6;
     const T *X = (const T *)p.X;
     for (int64_t b = blockIdx.x; b < items; b += gridDim.x) {
-        const int64_t n0 = (b % nb) * 32, k0 = (b / nb) * MX_GROUP;
-#pragma unroll 8
+        const int64_t n0 = (b % nb) * 64, k0 = (b / nb) * MX_GROUP;
+        const bool in = n0 + n < p.rows;
+        const T *x0 = X + (k0 + kq) * p.ldx + n0 + n;
+        T x[32];
+#pragma unroll
         for (int i = 0; i < 32; ++i) {
-            const int k = i * 8 + kq;
-            float x = 0.f;
-            if (k0 + k < p.cols && n0 + n < p.rows) x = (float)X[(k0 + k) * p.ldx + n0 + n];
-            tile[k][n] = x;
+            x[i] = (T)0.f;
+            if (in && k0 + i * 8 + kq < p.cols) x[i] = x0[(int64_t)i * 8 * p.ldx];
         }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) tile[i * 8 + kq][n] = (float)x[i];
         __syncthreads();
-        if (n0 + n < p.rows) {
+        if (in) {
             float v[4][8];
             uint32_t m = 0;
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
-                const float x = tile[kq * 32 + i][n];
-                v[i >> 3][i & 7] = x;
-                const uint32_t a = __builtin_bit_cast(uint32_t, x) & 0x7fffffffu;
+                const float y = tile[kq * 32 + i][n];
+                v[i >> 3][i & 7] = y;
+                const uint32_t a = __builtin_bit_cast(uint32_t, y) & 0x7fffffffu;
                 m = a > m ? a : m;
             }
             const uint32_t byte = mx_scale_byte(m, FORMAT);
@@ -209,24 +212,23 @@ __global__ __launch_bounds__(256) void act_checkpoint_kernel(MxParams p)
 
 // act'(z).  relu: 1 above zero, else 0 (NaN stays NaN).  gelu = z Phi(z):
 // Phi(z) + z phi(z), with phi the normal density and Phi by the same
-// approximation of erfc as the forward (Abramowitz & Stegun 7.1.26), on
-// q = erfc(|z| / sqrt 2): Phi = 1 - q/2 for z >= 0 and q/2 below.  exp(-z^2/2)
-// serves both terms.  For |z| past 14 the density underflows; z is clamped
-// there so that an infinity gives 1 or 0 and not inf * 0 (NaN stays NaN).
+// approximation of erfc as the forward (Abramowitz & Stegun 7.1.26) on
+// q = erfc(|z| / sqrt 2): Phi = 1 - q/2 for z >= 0 and q/2 below (its constants
+// carry the 1/sqrt 2 and the 1/2).  exp(-z^2/2) serves both terms.  In z phi(z)
+// z is clamped to 14, where the density has underflowed, so that an infinity
+// gives 1 or 0 and not inf * 0 (a NaN comes through Phi).
 __device__ __forceinline__ float act_slope(int act, float z)
 {
     if (act == ACT_RELU) return z > 0.f ? 1.f : (z <= 0.f ? 0.f : z);
-    z = z > 14.f ? 14.f : (z < -14.f ? -14.f : z);
-    const float a = __builtin_fabsf(z) * 0.70710678118654752f;
-    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.3275911f, a, 1.f));
-    float poly = __builtin_fmaf(t, 1.061405429f, -1.453152027f);
-    poly = __builtin_fmaf(t, poly, 1.421413741f);
-    poly = __builtin_fmaf(t, poly, -0.284496736f);
-    poly = __builtin_fmaf(t, poly, 0.254829592f);
-    const float ex = __expf(-a * a);
-    const float hq = 0.5f * poly * t * ex;
+    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.3275911f * 0.70710678f, __builtin_fabsf(z), 1.f));
+    float poly = __builtin_fmaf(t, 0.5f * 1.061405429f, 0.5f * -1.453152027f);
+    poly = __builtin_fmaf(t, poly, 0.5f * 1.421413741f);
+    poly = __builtin_fmaf(t, poly, 0.5f * -0.284496736f);
+    poly = __builtin_fmaf(t, poly, 0.5f * 0.254829592f);
+    const float ex = __builtin_amdgcn_exp2f(z * z * -0.72134752f);   // 2^(-z^2/2 * log2 e)
+    const float hq = poly * t * ex;
     const float cdf = z >= 0.f ? 1.f - hq : hq;
-    return __builtin_fmaf(z * 0.3989422804014327f, ex, cdf);
+    return __builtin_fmaf(__builtin_amdgcn_fmed3f(z, -14.f, 14.f) * 0.3989422804014327f, ex, cdf);
 }
 
 // dZ = dH * act'(z8), and the column sums of dZ (before its rounding) into
@@ -244,17 +246,25 @@ __global__ __launch_bounds__(256) void act_backward_kernel(MxParams p)
 #pragma unroll
     for (int i = 0; i < 8; ++i) sum[i] = 0.f;
     if (col < p.cols) {
-#pragma unroll 2
-        for (int64_t row = r0 + wave; row < r1; row += 4) {
-            float z[8], d[8];
-            load8<T>((const T *)p.X + row * p.ldx, col, p.cols, d);
-            load_codes<FORMAT>(p, row, col, z);
+        // up to four rows' loads in flight
+        for (int64_t row = r0 + wave; row < r1; row += 16) {
+            float z[4][8], d[4][8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                d[i] *= act_slope(p.act, z[i]);
-                sum[i] += d[i];
-            }
-            store8<T>((T *)p.Y + row * p.ldy, col, p.cols, d);
+            for (int u = 0; u < 4; ++u)
+                if (row + 4 * u < r1) {
+                    load8<T>((const T *)p.X + (row + 4 * u) * p.ldx, col, p.cols, d[u]);
+                    load_codes<FORMAT>(p, row + 4 * u, col, z[u]);
+                }
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (row + 4 * u < r1) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        d[u][i] *= act_slope(p.act, z[u][i]);
+                        sum[i] += d[u][i];
+                    }
+                    store8<T>((T *)p.Y + (row + 4 * u) * p.ldy, col, p.cols, d[u]);
+                }
         }
     }
     if (!p.dbias) return;
@@ -278,6 +288,7 @@ __global__ __launch_bounds__(256) void column_sum_kernel(const float *ws, float 
         const int64_t col = c0 + c;
         float s = 0.f;
         if (col < cols)
+#pragma unroll 8
             for (int i = q; i < slices; i += 16) s += ws[(int64_t)i * cols + col];
         part[q][c] = s;
         __syncthreads();
@@ -332,7 +343,8 @@ kernel_fn backward_fn(const MxParams &)
 
 hipError_t launch_mx_quantize(const MxParams &p, hipStream_t s)
 {
-    return launch((const void *)DG_BY_TYPE(DG_BY_FORMAT, quantize_fn), grid_for(p.trans ? trans_items(p) : row_items(p)), dim3(256), s, p);
+    return launch((const void *)DG_BY_TYPE(DG_BY_FORMAT, quantize_fn), grid_for(p.trans ? trans_items(p) : row_items(p)),
+                  dim3(p.trans ? 512 : 256), s, p);
 }
 
 hipError_t launch_mx_dequantize(const MxParams &p, hipStream_t s)

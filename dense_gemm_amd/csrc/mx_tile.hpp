@@ -31,11 +31,13 @@ template <typename TC, int W>
 __device__ __forceinline__ void store_staged(const GemmParams &p, const lds_char_t *stg, int row0, int col0, int lane)
 {
     typedef __attribute__((address_space(3))) f32x4 lds_f32x4_t;
+    // 16-byte accesses of C; its rows need only be aligned to their element
     typedef TC VC __attribute__((ext_vector_type(16 / sizeof(TC))));
+    typedef VC __attribute__((aligned(sizeof(TC)))) VCu;
     constexpr int PER = 16 / sizeof(TC);                 // elements of a 16-byte access
     constexpr int LPR = W / 8, RPP = 64 / LPR;           // lanes per row, rows per pass
     const int lc = (lane % LPR) * 8, gcol = col0 + lc;
-    const bool vec = p.c_vec && gcol + 8 <= p.N;
+    const bool vec = gcol + 8 <= p.N;
     // the lane's 8 columns are the same in every pass: their bias is read once
     float bias[8];
 #pragma unroll
@@ -56,7 +58,7 @@ __device__ __forceinline__ void store_staged(const GemmParams &p, const lds_char
             if (vec) {
 #pragma unroll
                 for (int q = 0; q < 8 / PER; ++q) {
-                    const VC x = *(const VC *)(c + q * PER);
+                    const VC x = *(const VCu *)(c + q * PER);
 #pragma unroll
                     for (int e = 0; e < PER; ++e) v[q * PER + e] = __builtin_fmaf(p.beta, (float)x[e], v[q * PER + e]);
                 }
@@ -81,7 +83,7 @@ __device__ __forceinline__ void store_staged(const GemmParams &p, const lds_char
                 VC x;
 #pragma unroll
                 for (int e = 0; e < PER; ++e) x[e] = (TC)v[q * PER + e];
-                *(VC *)(c + q * PER) = x;
+                *(VCu *)(c + q * PER) = x;
             }
         } else {
 #pragma unroll

@@ -39,7 +39,7 @@ _SIGNATURES = {
                                   "epilogue stream"),
     "dg_gemm_mx_with_kernel": (_ci, _GEMM_MX + [_ci], "M N K alpha formatA A lda SA ldsa formatB B ldb SB ldsb beta C "
                                                       "ldc type bias epilogue stream kernel"),
-    "dg_gemm_mx_select": (_ci, [_i64, _i64, _i64], "M N K"),
+    "dg_gemm_mx_select": (_ci, [_ci, _i64, _i64, _i64], "formatA M N K"),
     "dg_gemm_mx_kernel_name": (ctypes.c_char_p, [_ci], "kernel"),
     "dg_gemm_dq": (_ci, [_ci, _i64, _i64, _i64, _f32, _vp, _i64, _ci] + _MX + [_f32, _vp, _i64, _ci, _ci, _vp, _sz, _vp],
                    "transA M N K alpha A lda typeA formatB B ldb SB ldsb beta C ldc typeC splits workspace "
@@ -56,10 +56,11 @@ EXPORTED = sorted(_SIGNATURES)
 __all__ = EXPORTED + ["MxMatrix", "MxError", "MX_FORMATS", "DG_ELEM_F32", "DG_ELEM_F16", "DG_ELEM_BF16", "DG_MXFP4",
                       "DG_MXFP8", "DG_MXINT8", "quantize_mx", "dequantize_mx", "gemm_mx", "gemm_dq", "act_checkpoint",
                       "act_backward", "mx_kernel_names"]
+_functions = {}
 for _name, (_res, _args, _) in _SIGNATURES.items():
     _f = getattr(_lib, _name)
     _f.restype, _f.argtypes = _res, _args
-    globals()[_name] = _f
+    _functions[_name] = globals()[_name] = _f
 
 
 def mx_kernel_names() -> list[str]:
@@ -100,30 +101,32 @@ class MxMatrix:
             raise ValueError(f"format must be one of {sorted(MX_FORMATS)}")
         groups = -(-cols // GROUP)
         nb = groups * (GROUP // 2 if code == DG_MXFP4 else GROUP)
-        if q.dtype != torch.uint8 or s.dtype != torch.uint8 or q.device != s.device:
+        if q.dtype != torch.uint8 or s.dtype != torch.uint8 or q.get_device() != s.get_device():
             raise TypeError("q and s must be uint8 tensors on one device")
-        if q.dim() != 2 or q.shape[0] != rows or q.shape[1] < nb or (q.shape[1] > 1 and q.stride(1) != 1):
+        qs, qt, st = q.shape, q.stride(), s.stride()
+        if len(qs) != 2 or qs[0] != rows or qs[1] < nb or (qt[1] != 1 and qs[1] > 1):
             raise ValueError(f"q must be [{rows}, {nb}] bytes or wider, with unit column stride")
-        if tuple(s.shape) != (groups, rows, 8) or (s.numel() and (s.stride(2) != 1 or (rows > 1 and s.stride(1) != 8))):
+        if s.shape != (groups, rows, 8) or (groups and rows and (st[2] != 1 or (rows > 1 and st[1] != 8))):
             raise ValueError(f"s must be [{groups}, {rows}, 8] with rows 8 bytes apart")
         self.format, self.rows, self.cols, self.q, self.s, self.code = format, rows, cols, q, s, code
         # a single row or group gives no stride: any valid one will do
-        self.ldq = q.stride(0) if rows > 1 and nb > 0 else nb
+        self.ldq = qt[0] if rows > 1 and nb > 0 else nb
         if groups > 1:
-            if s.stride(0) % 8:
+            if st[0] % 8:
                 raise ValueError("the groups of s must be a multiple of 8 bytes apart")
-            self.lds = s.stride(0) // 8
+            self.lds = st[0] // 8
         else:
             self.lds = rows
 
     @classmethod
-    def empty(cls, format: str, rows: int, cols: int, device) -> "MxMatrix":
-        """Uninitialised storage."""
+    def empty(cls, format: str, rows: int, cols: int, device, stream=None) -> "MxMatrix":
+        """Uninitialised storage (`stream`: the one it is first used on, when it
+        is not the current one)."""
         code = MX_FORMATS.get(format)
         if code is None:
             raise ValueError(f"format must be one of {sorted(MX_FORMATS)}")
-        return cls(format, rows, cols, torch.empty(rows, dg_mx_row_bytes(code, cols), dtype=torch.uint8, device=device),  # noqa: F821
-                   torch.empty(-(-cols // GROUP), rows, 8, dtype=torch.uint8, device=device))
+        return cls(format, rows, cols, _empty((rows, dg_mx_row_bytes(code, cols)), torch.uint8, device, stream),  # noqa: F821
+                   _empty((-(-cols // GROUP), rows, 8), torch.uint8, device, stream))
 
     @property
     def device(self):
@@ -135,11 +138,16 @@ class MxMatrix:
 
 def _plain(t, name, rows, cols):
     """The row stride of a plain 2-D matrix of that shape."""
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+    if t.shape != (rows, cols):
         raise ValueError(f"{name} must be [{rows}, {cols}]")
-    if cols > 1 and t.stride(1) != 1:
+    ld, one = t.stride()
+    if one != 1 and cols > 1:
         raise ValueError(f"{name} must have unit column stride (row-major rows)")
-    return max(t.stride(0), cols, 1) if rows > 1 else max(cols, 1)
+    if rows <= 1:
+        return max(cols, 1)
+    if ld < cols:
+        raise ValueError(f"{name} has overlapping rows (a row stride below {cols})")
+    return max(ld, 1)
 
 
 def _elem(t, name):
@@ -149,30 +157,50 @@ def _elem(t, name):
     return code
 
 
-def _call(function, device, stream, tensors, *args, after=()):
-    """One library call on `stream` (or the current one) of `device`, with that
-    device current (`after`: arguments behind the stream).  Tensors handed to a stream of the caller's stay allocated
-    until that stream has passed them."""
+# A device's current stream and the current device without building torch's
+# objects for them (a microsecond and a half a call); the public way where
+# torch lacks these.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _stream_of(stream, tensors):
+    """The handle of the caller's stream, or of the current one, on the device
+    of the tensors (None among them: not given).  Tensors handed to a stream of
+    the caller's stay allocated until that stream has passed them."""
+    index = tensors[0].get_device()
     for t in tensors:
-        if t is not None and t.device != device:
+        if t is not None and t.get_device() != index:
             raise ValueError("all matrices must be on one device")
-    if device.type != "cuda":
+    if index < 0:
         raise ValueError("the matrices must be on a GPU")
     if stream is None:
-        handle = torch.cuda.current_stream(device).cuda_stream
+        return index, _raw_stream(index)
+    if stream.device.index != index:
+        raise ValueError("stream belongs to another device than the matrices")
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+    return index, stream.cuda_stream
+
+
+def _empty(shape, dtype, device, stream):
+    """Uninitialised memory that belongs to the stream the call runs on (the
+    allocator reuses freed blocks in the order of their own stream)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _call(function, index, *args):
+    """One library call with device `index` current."""
+    f = _functions[function]
+    if index == _current_device():
+        rc = f(*args)
     else:
-        if stream.device != device:
-            raise ValueError("stream belongs to another device than the matrices")
-        handle = stream.cuda_stream
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
-    f = globals()[function]
-    if device.index == torch.cuda.current_device():
-        rc = f(*args, handle, *after)
-    else:
-        with torch.cuda.device(device):
-            rc = f(*args, handle, *after)
+        with torch.cuda.device(index):
+            rc = f(*args)
     if rc != DG_OK:
         raise MxError(function, rc)
 
@@ -181,26 +209,29 @@ def quantize_mx(X, format="mxfp4", trans=False, out=None, stream=None) -> MxMatr
     """X (or its transpose) rounded to an MX format, blocks of 32 along the
     result's rows.  X is 2-D float32, float16 or bfloat16 with unit column
     stride.  `out` (an MxMatrix) is written when given, and sets the format."""
-    if X.dim() != 2:
+    shape = X.shape
+    if len(shape) != 2:
         raise ValueError("X must be 2-D")
-    rows, cols = (X.shape[1], X.shape[0]) if trans else (X.shape[0], X.shape[1])
+    rows, cols = shape[::-1] if trans else shape
     if out is None:
-        out = MxMatrix.empty(format, rows, cols, X.device)
+        out = MxMatrix.empty(format, rows, cols, X.device, stream)
     elif out.rows != rows or out.cols != cols:
         raise ValueError(f"out must be {rows} x {cols}")
-    ldx = _plain(X, "X", X.shape[0], X.shape[1])
-    _call("dg_mx_quantize", X.device, stream, (X, out.q, out.s), bool(trans), rows, cols, X.data_ptr(), ldx,
-          _elem(X, "X"), out.code, out.q.data_ptr(), out.ldq, out.s.data_ptr(), out.lds)
+    ldx, code = _plain(X, "X", *shape), _elem(X, "X")
+    index, handle = _stream_of(stream, (X, out.q, out.s))
+    _call("dg_mx_quantize", index, bool(trans), rows, cols, X.data_ptr(), ldx, code, out.code, out.q.data_ptr(),
+          out.ldq, out.s.data_ptr(), out.lds, handle)
     return out
 
 
 def dequantize_mx(m: MxMatrix, dtype=torch.float32, out=None, stream=None):
     """The values of an MX matrix as a plain one, of `dtype` or out's."""
     if out is None:
-        out = torch.empty(m.rows, m.cols, dtype=dtype, device=m.device)
+        out = _empty((m.rows, m.cols), dtype, m.device, stream)
     ldx = _plain(out, "out", m.rows, m.cols)
-    _call("dg_mx_dequantize", out.device, stream, (m.q, m.s, out), m.rows, m.cols, m.code, m.q.data_ptr(), m.ldq,
-          m.s.data_ptr(), m.lds, out.data_ptr(), ldx, _elem(out, "out"))
+    index, handle = _stream_of(stream, (out, m.q, m.s))
+    _call("dg_mx_dequantize", index, m.rows, m.cols, m.code, m.q.data_ptr(), m.ldq, m.s.data_ptr(), m.lds, out.data_ptr(),
+          ldx, _elem(out, "out"), handle)
     return out
 
 
@@ -216,15 +247,16 @@ def gemm_mx(A: MxMatrix, B: MxMatrix, C=None, alpha=1.0, beta=0.0, bias=None, ac
     if C is None:
         if beta != 0.0:
             raise ValueError("beta != 0 needs C")
-        C = torch.empty(M, N, dtype=out_dtype, device=A.device)
+        C = _empty((M, N), out_dtype, A.device, stream)
     if activation not in EPILOGUES:
         raise ValueError(f"activation must be one of {sorted(EPILOGUES)}")
     if bias is not None and (bias.dtype != C.dtype or bias.dim() != 1 or bias.shape[0] != N or (N > 1 and bias.stride(0) != 1)):
         raise ValueError(f"bias must be a contiguous 1-D tensor of {N} elements of C's dtype")
     ldc = _plain(C, "C", M, N)
-    _call("dg_gemm_mx_with_kernel", A.device, stream, (A.q, A.s, B.q, B.s, C, bias), M, N, K, alpha, A.code,
-          A.q.data_ptr(), A.ldq, A.s.data_ptr(), A.lds, B.code, B.q.data_ptr(), B.ldq, B.s.data_ptr(), B.lds, beta, C.data_ptr(), ldc, _elem(C, "C"),
-          None if bias is None else bias.data_ptr(), EPILOGUES[activation], after=(kernel,))
+    index, handle = _stream_of(stream, (A.q, A.s, B.q, B.s, C, bias))
+    _call("dg_gemm_mx_with_kernel", index, M, N, K, alpha, A.code, A.q.data_ptr(), A.ldq, A.s.data_ptr(), A.lds, B.code,
+          B.q.data_ptr(), B.ldq, B.s.data_ptr(), B.lds, beta, C.data_ptr(), ldc, _elem(C, "C"),
+          None if bias is None else bias.data_ptr(), EPILOGUES[activation], handle, kernel)
     return C
 
 
@@ -247,18 +279,18 @@ def gemm_dq(A, B: MxMatrix, C=None, transA=False, alpha=1.0, beta=0.0, out_dtype
     if C is None:
         if beta != 0.0:
             raise ValueError("beta != 0 needs C")
-        C = torch.empty(M, N, dtype=out_dtype or A.dtype, device=A.device)
+        C = _empty((M, N), out_dtype or A.dtype, A.device, stream)
     if C.dtype not in (A.dtype, torch.float32):
         raise TypeError("C must have A's dtype or float32")
     lda, ldc = _plain(A, "A", A.shape[0], A.shape[1]), _plain(C, "C", M, N)
     if splits == 0:
         splits = dg_gemm_dq_choose(M, N, K)  # noqa: F821
     if workspace is None and splits > 1:
-        workspace = torch.empty(dg_gemm_splitk_workspace_size(M, N, splits), dtype=torch.uint8, device=A.device)
+        workspace = _empty(dg_gemm_splitk_workspace_size(M, N, splits), torch.uint8, A.device, stream)
     ws, wsb = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    _call("dg_gemm_dq", A.device, stream, (A, B.q, B.s, C, workspace), bool(transA), M, N, K, alpha, A.data_ptr(), lda,
-          _ELEM[A.dtype], B.code, B.q.data_ptr(), B.ldq, B.s.data_ptr(), B.lds, beta, C.data_ptr(), ldc, _ELEM[C.dtype],
-          splits, ws, wsb)
+    index, handle = _stream_of(stream, (A, B.q, B.s, C, workspace))
+    _call("dg_gemm_dq", index, bool(transA), M, N, K, alpha, A.data_ptr(), lda, _ELEM[A.dtype], B.code, B.q.data_ptr(),
+          B.ldq, B.s.data_ptr(), B.lds, beta, C.data_ptr(), ldc, _ELEM[C.dtype], splits, ws, wsb, handle)
     return C
 
 
@@ -272,16 +304,17 @@ def act_checkpoint(Z, activation="gelu", H=None, out=None, format="mxint8", stre
     if activation not in _ACTIVATIONS:
         raise ValueError(f"activation must be one of {sorted(_ACTIVATIONS)}")
     if H is None:
-        H = torch.empty(rows, cols, dtype=Z.dtype, device=Z.device)
+        H = _empty((rows, cols), Z.dtype, Z.device, stream)
     elif H.dtype != Z.dtype:
         raise TypeError("H must have Z's dtype")
     if out is None:
-        out = MxMatrix.empty(format, rows, cols, Z.device)
+        out = MxMatrix.empty(format, rows, cols, Z.device, stream)
     elif out.rows != rows or out.cols != cols:
         raise ValueError(f"out must be {rows} x {cols}")
     ldz, ldh = _plain(Z, "Z", rows, cols), _plain(H, "H", rows, cols)
-    _call("dg_act_checkpoint", Z.device, stream, (Z, H, out.q, out.s), rows, cols, Z.data_ptr(), ldz, H.data_ptr(), ldh,
-          _elem(Z, "Z"), _ACTIVATIONS[activation], out.code, out.q.data_ptr(), out.ldq, out.s.data_ptr(), out.lds)
+    index, handle = _stream_of(stream, (Z, H, out.q, out.s))
+    _call("dg_act_checkpoint", index, rows, cols, Z.data_ptr(), ldz, H.data_ptr(), ldh, _elem(Z, "Z"),
+          _ACTIVATIONS[activation], out.code, out.q.data_ptr(), out.ldq, out.s.data_ptr(), out.lds, handle)
     return H, out
 
 
@@ -294,7 +327,7 @@ def act_backward(dH, kept: MxMatrix, activation="gelu", dZ=None, dbias=None, wor
     if activation not in _ACTIVATIONS:
         raise ValueError(f"activation must be one of {sorted(_ACTIVATIONS)}")
     if dZ is None:
-        dZ = torch.empty(rows, cols, dtype=dH.dtype, device=dH.device)
+        dZ = _empty((rows, cols), dH.dtype, dH.device, stream)
     elif dZ.dtype != dH.dtype:
         raise TypeError("dZ must have dH's dtype")
     ldh, ldz = _plain(dH, "dH", rows, cols), _plain(dZ, "dZ", rows, cols)
@@ -302,9 +335,10 @@ def act_backward(dH, kept: MxMatrix, activation="gelu", dZ=None, dbias=None, wor
         if dbias.dtype != torch.float32 or dbias.dim() != 1 or dbias.shape[0] != cols or (cols > 1 and dbias.stride(0) != 1):
             raise ValueError(f"dbias must be a contiguous float32 tensor of {cols} elements")
         if workspace is None:
-            workspace = torch.empty(dg_act_backward_workspace_size(rows, cols), dtype=torch.uint8, device=dH.device)  # noqa: F821
+            workspace = _empty(dg_act_backward_workspace_size(rows, cols), torch.uint8, dH.device, stream)  # noqa: F821
     ws, wsb = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    _call("dg_act_backward", dH.device, stream, (dH, kept.q, kept.s, dZ, dbias, workspace), rows, cols, dH.data_ptr(), ldh,
-          kept.code, kept.q.data_ptr(), kept.ldq, kept.s.data_ptr(), kept.lds, dZ.data_ptr(), ldz, _elem(dH, "dH"),
-          _ACTIVATIONS[activation], None if dbias is None else dbias.data_ptr(), ws, wsb)
+    index, handle = _stream_of(stream, (dH, kept.q, kept.s, dZ, dbias, workspace))
+    _call("dg_act_backward", index, rows, cols, dH.data_ptr(), ldh, kept.code, kept.q.data_ptr(), kept.ldq,
+          kept.s.data_ptr(), kept.lds, dZ.data_ptr(), ldz, _elem(dH, "dH"), _ACTIVATIONS[activation],
+          None if dbias is None else dbias.data_ptr(), ws, wsb, handle)
     return dZ

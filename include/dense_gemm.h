@@ -334,13 +334,13 @@ int dg_gemm_mx(int64_t M, int64_t N, int64_t K, float alpha, dg_mx_t formatA, co
 
 /* dg_gemm_mx with a forced kernel (argument 22; DG_KERNEL_AUTO: the
  * library's choice), for tests and measurement; DG_ERR_UNSUPPORTED when it
- * cannot run the problem.  The choice for packed operands, and the kernels'
- * names (NULL when out of range). */
+ * cannot run the problem.  The choice for packed operands (or -i: 1 formatA,
+ * 2 M, 3 N, 4 K), and the kernels' names (NULL when out of range). */
 int dg_gemm_mx_with_kernel(int64_t M, int64_t N, int64_t K, float alpha, dg_mx_t formatA, const void *A,
                            int64_t lda, const void *SA, int64_t ldsa, dg_mx_t formatB, const void *B, int64_t ldb,
                            const void *SB, int64_t ldsb, float beta, void *C, int64_t ldc, dg_elem_t type,
                            const void *bias, dg_epilogue_t epilogue, void *stream, int kernel);
-int dg_gemm_mx_select(int64_t M, int64_t N, int64_t K);
+int dg_gemm_mx_select(dg_mx_t formatA, int64_t M, int64_t N, int64_t K);
 const char *dg_gemm_mx_kernel_name(int kernel);
 
 /* C = alpha * op(A) B + beta * C: A is fp16 or bf16 (typeA), stored M x K or
@@ -355,7 +355,7 @@ const char *dg_gemm_mx_kernel_name(int kernel);
  *   dg_gemm_dq_choose; the workspace holds splits * M * N fp32 partials, see
  *   dg_gemm_splitk_workspace_size, and is needed only when more than one
  *   range results).
- *   DG_ERR_UNSUPPORTED: rows of B so long that 64 of them exceed 2^31 bytes.
+ *   DG_ERR_UNSUPPORTED: an output of 2^22 tiles or more (about 2^34 elements).
  *   1 transA, 2 M, 3 N, 4 K, 5 alpha, 6 A, 7 lda, 8 typeA, 9 formatB, 10 B,
  *   11 ldb (bytes), 12 SB, 13 ldsb, 14 beta, 15 C, 16 ldc, 17 typeC,
  *   18 splits, 19 workspace (NULL or not 16-byte aligned), 20

@@ -275,18 +275,21 @@ def test_dq_product_exact(ty, fmt, transA):
             assert torch.isnan(C[:, N:]).all()
 
 
-@pytest.mark.parametrize("M,N,K", [(3, 50, 700), (140, 200, 700), (2100, 4000, 200), (6000, 2500, 100)])
+@pytest.mark.parametrize("M,N,K", [(3, 50, 700), (140, 200, 700), (1800, 1801, 300), (2100, 4000, 200), (6000, 2500, 100)])
 def test_dq_product_large_tiles_and_types(M, N, K):
-    """Each tile of the library (the last two shapes fill the GPU with the
-    largest), 16-bit outputs, alpha and beta: fp32 epilogue, half a step."""
+    """Each tile of the library, 16-bit outputs, alpha and beta: fp32 epilogue, half a step."""
     rng = np.random.default_rng(31)
     for ty in ("f16", "bf16"):
         B, b = stored(rng, K, N, "mxfp8", spread=1, whole=True)
         a = rng.integers(-4, 5, (K, M)).astype(np.float64)
-        A = torch.from_numpy(a).to(T[ty]).to(DEV)
         c0 = plain(rng, M, N, T[ty])
         base = np64(c0)
-        dg.gemm_dq(A, B, C=c0, transA=True, alpha=0.25, beta=2.0)
+        if ty == "f16":
+            A = torch.from_numpy(a).to(T[ty]).to(DEV)
+            dg.gemm_dq(A, B, C=c0, transA=True, alpha=0.25, beta=2.0)
+        else:
+            A = torch.from_numpy(np.ascontiguousarray(a.T)).to(T[ty]).to(DEV)
+            dg.gemm_dq(A, B, C=c0, alpha=0.25, beta=2.0)
         s = a.T @ b
         want = 0.25 * s + 2.0 * base
         tol = 3 * 2.0 ** -24 * (np.abs(0.25 * s) + np.abs(2 * base))

@@ -177,17 +177,24 @@ def test_empty_problems_do_nothing():
 def test_kernel_choice():
     names = dg.mx_kernel_names()
     assert len(names) == len(set(names)) and dg.dg_gemm_mx_kernel_name(-1) is None
-    for M in (1, 16, 17, 32, 33, 200, 512, 4096, 8192):
-        for N in (1, 64, 2048, 8192):
-            assert 0 <= dg.dg_gemm_mx_select(M, N, 2048) < len(names)
-    assert "rows" in names[dg.dg_gemm_mx_select(1, 5632, 2048)]
-    assert "256x256" in names[dg.dg_gemm_mx_select(8192, 8192, 8192)]
-    assert dg.dg_gemm_mx_select(-1, 1, 1) == -1 and dg.dg_gemm_mx_select(1, -1, 1) == -2 and dg.dg_gemm_mx_select(1, 1, -1) == -3
+    pick = lambda M, N, K, fa=dg.DG_MXFP8: names[dg.dg_gemm_mx_select(fa, M, N, K)]  # noqa: E731
+    for fa in (dg.DG_MXFP4, dg.DG_MXFP8):
+        # single tokens: the kernel that reads the weights once
+        for N, K in ((64, 64), (5632, 2048), (8192, 8192)):
+            assert pick(1, N, K, fa) == "mx_16x16_rows"
+        assert pick(8192, 8192, 8192, fa) == "mx_256x256_tile"
+    # the faster kernel when measured on either side
+    assert pick(16, 8192, 8192) == "mx_16x16_rows" and pick(64, 2048, 2048) == "mx_32x16_rows"
+    assert pick(32, 8192, 8192) == "mx_64x64_tile" and pick(128, 5632, 2048) == "mx_64x64_tile"
+    assert pick(1024, 8192, 8192) == "mx_128x128_tile"
+    assert pick(2048, 8192, 4096, dg.DG_MXFP4) == "mx_256x256_tile"
+    assert [dg.dg_gemm_mx_select(*a) for a in ((2, 1, 1, 1), (1, -1, 1, 1), (1, 1, -1, 1), (1, 1, 1, -1))] == [-1, -2, -3, -4]
     assert dg.dg_gemm_mx_with_kernel(*MX.values(), len(names)) == dg.DG_ERR_UNSUPPORTED
     # rows too long for the tiled kernels' 32-bit offsets: refused when forced
     far = dict(MX, lda=1 << 23, M=100, ldsa=100)
     assert dg.dg_gemm_mx_with_kernel(*far.values(), len(names) - 1) == dg.DG_ERR_UNSUPPORTED
-    assert dg.dg_gemm_dq(*dict(DQ, ldb=1 << 25).values()) == dg.DG_ERR_UNSUPPORTED
+    big = 2 ** 30
+    assert dg.dg_gemm_dq(*dict(DQ, M=big, N=big, lda=64, ldb=big, ldc=big).values()) == dg.DG_ERR_UNSUPPORTED
 
 
 def test_split_choice():
@@ -210,6 +217,7 @@ def test_torch_functions_refuse():
     for call in (
         lambda: dg.quantize_mx(x),                                       # not on a GPU
         lambda: dg.quantize_mx(x[0]),
+        lambda: dg.quantize_mx(x[:1].expand(4, 40)),                     # rows on top of each other
         lambda: dg.quantize_mx(x, out=_mx("mxfp4", 4, 41)),
         lambda: dg.quantize_mx(torch.zeros(40, 4).t(), out=a8),
         lambda: dg.quantize_mx(x, format="fp4"),

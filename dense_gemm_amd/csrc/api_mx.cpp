@@ -108,22 +108,25 @@ int mx_choose(bool a4, int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb
 struct DqTile {
     int bm, bn;
     double fixed, slab;      // us: the fixed part, and a slab of 64 k
+    int resident;            // workgroups that fit a compute unit (LDS)
+    double share;            // of a slab's time, for each of them
 };
-const DqTile kDq[] = {{32, 128, 3.0, 0.38}, {64, 128, 3.0, 0.58}, {128, 128, 4.0, 0.75}, {256, 256, 10.0, 1.38}};
+const DqTile kDq[] = {{32, 128, 3.0, 0.50, 4, 0.45}, {64, 128, 3.0, 0.60, 3, 0.58}, {128, 128, 4.0, 0.74, 2, 0.635},
+                      {256, 256, 10.0, 1.38, 1, 1.0}};
 constexpr int kNumDq = sizeof(kDq) / sizeof(kDq[0]);
 
 // K ranges of `splits` (each a multiple of 64 but the last).
 int64_t dq_chunk(int64_t K, int splits) { return ceil_div(ceil_div(K, splits), 64) * 64; }
 
 // Tile and K ranges by their time (us) under a model fitted to back-to-back
-// times of 21 shapes: a fixed part, and a part per slab that grows with the
-// workgroups beyond one per compute unit (0.8 of a slab for each further one,
-// whole rounds for the 256 x 256 tile, which fills a unit's LDS), and for
-// more than one range the second launch and the partials' way to memory and
-// back at 4 TB/s.  `splits` > 0 fixes the ranges.  Measured on both sides
-// (M x N x K, us): 512 x 2048 x 5632 in 4 ranges 25.9, in one 54.1; 2048 x 1024
-// x 1024 in one range 11.9, in two 23.6; 1024 x 2048 x 8192 128-tile in 4 ranges
-// 57, 64-tile in one 94; 4096^3 256-tile 109, 128-tile 134.
+// times of 21 shapes: a fixed part; a part per slab for as many rounds as the
+// workgroups need, a round longer once a compute unit's workgroups fill its
+// LDS bandwidth (`share` of a slab each); and for more than one range the
+// second launch and the partials' way to memory and back at 6 TB/s.
+// `splits` > 0 fixes the ranges.  Measured on both sides (M x N x K, us):
+// 512 x 2048 x 5632 in 4 ranges 25.9, in one 54.1; 2048 x 1024 x 1024 in one
+// range 11.9, in two 23.6; 1024 x 2048 x 8192 128-tile in 4 ranges 51.6, 64-tile
+// in one 91; 4096^3 256-tile 109, 128-tile 134.
 void dq_choose(int64_t M, int64_t N, int64_t K, bool direct, int splits, int *tile, int *ranges)
 {
     double best = 1e300;
@@ -138,11 +141,13 @@ void dq_choose(int64_t M, int64_t N, int64_t K, bool direct, int splits, int *ti
             const int64_t chunk = dq_chunk(K, list[i]), s = ceil_div(K, chunk);
             // ranges of at least 4 slabs, and no more partials than 256 MiB, where the choice is free
             if (splits == 0 && s > 1 && (chunk < 256 || (double)s * out * 4 > 268435456.0)) continue;
-            const double w = tiles * (double)s / 256, full = (double)(int64_t)w;
-            const double rounds = k == 3 ? full + (w > full ? (full > 0 ? 0.82 : 1.) : 0.) : w > 1 ? 1 + 0.8 * (w - 1) : 1;
+            const double w = tiles * (double)s / 256, full = (double)(int64_t)(w / kDq[k].resident);
+            auto round = [&](double wgs) { return kDq[k].share * wgs > 1 ? kDq[k].share * wgs : 1.; };
+            const double rest = w - full * kDq[k].resident;
+            const double rounds = full * round(kDq[k].resident) + (rest > 0 ? (k == 3 && full > 0 ? 0.82 : round(rest)) : 0.);
             // (with every unit at work on the largest tile the clock drops)
             double t = kDq[k].fixed + (double)(chunk / 64) * kDq[k].slab * (direct ? 1. : 1.2) * rounds * (k == 3 && w > 0.9 ? 1.15 : 1.);
-            if (s > 1) t += 3.5 + (double)s * out * 8 / 4e6;
+            if (s > 1) t += 3.0 + (double)s * (0.4 + out * 8 / 6e6);
             if (t < best) {
                 best = t;
                 *tile = k;

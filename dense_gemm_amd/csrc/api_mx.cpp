@@ -122,7 +122,8 @@ int64_t dq_chunk(int64_t K, int splits) { return ceil_div(ceil_div(K, splits), 6
 // times of 21 shapes: a fixed part; a part per slab for as many rounds as the
 // workgroups need, a round longer once a compute unit's workgroups fill its
 // LDS bandwidth (`share` of a slab each); and for more than one range the
-// second launch and the partials' way to memory and back at 6 TB/s.
+// second launch and the partials' way to memory and back at 6 TB/s, or at 4
+// once they outgrow the caches.
 // `splits` > 0 fixes the ranges.  Measured on both sides (M x N x K, us):
 // 512 x 2048 x 5632 in 4 ranges 25.9, in one 54.1; 2048 x 1024 x 1024 in one
 // range 11.9, in two 23.6; 1024 x 2048 x 8192 128-tile in 4 ranges 51.6, 64-tile
@@ -147,7 +148,7 @@ void dq_choose(int64_t M, int64_t N, int64_t K, bool direct, int splits, int *ti
             const double rounds = full * round(kDq[k].resident) + (rest > 0 ? (k == 3 && full > 0 ? 0.82 : round(rest)) : 0.);
             // (with every unit at work on the largest tile the clock drops)
             double t = kDq[k].fixed + (double)(chunk / 64) * kDq[k].slab * (direct ? 1. : 1.2) * rounds * (k == 3 && w > 0.9 ? 1.15 : 1.);
-            if (s > 1) t += 3.0 + (double)s * (0.4 + out * 8 / 6e6);
+            if (s > 1) t += 3.0 + (double)s * (0.4 + out * 8 / ((double)s * out * 4 < 64e6 ? 6e6 : 4e6));
             if (t < best) {
                 best = t;
                 *tile = k;

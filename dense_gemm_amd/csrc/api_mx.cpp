@@ -319,6 +319,7 @@ int dg_act_backward(int64_t rows, int64_t cols, const void *dH, int64_t ldh, dg_
     p.act = activation;
     p.dbias = dbias;
     p.ws = (float *)workspace;
+    p.band = dg::act_backward_band(rows, cols);
     p.slices = rows > 0 ? dg::act_backward_slices(rows, cols) : 0;   // no rows: the sums are zero
     return dg::launch_status(dg::launch_act_backward(p, (hipStream_t)stream));
 }

@@ -50,13 +50,14 @@ struct MxParams {
     int32_t act;          // ACT_RELU, ACT_GELU
     float *dbias;         // backward: column sums of dZ (NULL: none)
     float *ws;            // backward: partial column sums, [slices][cols]
-    int32_t slices;       // row slices of the backward's launch
+    int32_t slices, band; // row slices of the backward's launch, rows of a band (4, 8 or 16)
 };
 
 hipError_t launch_mx_quantize(const MxParams &p, hipStream_t s);
 hipError_t launch_mx_dequantize(const MxParams &p, hipStream_t s);
 hipError_t launch_act_checkpoint(const MxParams &p, hipStream_t s);
 hipError_t launch_act_backward(const MxParams &p, hipStream_t s);
+int act_backward_band(int64_t rows, int64_t cols);
 int act_backward_slices(int64_t rows, int64_t cols);
 
 #ifdef __HIPCC__

@@ -19,6 +19,18 @@
 // c ^ (k & 3).  The fragment reads (ds_read_b64_tr_b16, four rows of a quad per
 // 16 lanes) see four distinct quads, and the 16 lanes of a write, which hold
 // the same chunk numbers of two or four rows, distinct chunks.
+//
+// Measured: 4096^3 (mxfp4) 109 us, 1.26 PFLOP/s, the rate of a large bf16
+// product of the library that ships with torch (1.24); 5632 x 2048 x 16384 (tn,
+// mxint8) 360 us, 1.05 PFLOP/s on the 176 compute units that have a tile, mxfp8
+// 335.  The matrix cores are busy at the clock they hold under load there.
+// Smaller outputs are bound by LDS bytes: a 128 x 128 tile moves 106 KB a slab
+// for a quarter of the work of the 256 x 256 tile's 256 KB, and converted
+// elements go in at about 48 bytes a clock.  Tried and left: B's codes through
+// an LDS ring, more slabs deep (no faster at 512 x 2048 x 5632, slower at
+// 2048^3); the 128 x 128 tile in two K groups of four waves (62 us against 68 in
+// one range there, 185 against 134 at 4096^3); a 192 x 256 tile (335 us at the tn
+// product's mxfp8, as the 256 x 256 one); four 128 x 128 waves (380 against 360).
 #include "mx_tile.hpp"
 
 namespace dg {

@@ -193,6 +193,15 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _workspace(workspace):
+    """Address and size of a caller's workspace (0 of None)."""
+    if workspace is None:
+        return None, 0
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
 def _call(function, index, *args):
     """One library call with device `index` current."""
     f = _functions[function]
@@ -287,7 +296,7 @@ def gemm_dq(A, B: MxMatrix, C=None, transA=False, alpha=1.0, beta=0.0, out_dtype
         splits = dg_gemm_dq_choose(M, N, K)  # noqa: F821
     if workspace is None and splits > 1:
         workspace = _empty(dg_gemm_splitk_workspace_size(M, N, splits), torch.uint8, A.device, stream)
-    ws, wsb = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    ws, wsb = _workspace(workspace)
     index, handle = _stream_of(stream, (A, B.q, B.s, C, workspace))
     _call("dg_gemm_dq", index, bool(transA), M, N, K, alpha, A.data_ptr(), lda, _ELEM[A.dtype], B.code, B.q.data_ptr(),
           B.ldq, B.s.data_ptr(), B.lds, beta, C.data_ptr(), ldc, _ELEM[C.dtype], splits, ws, wsb, handle)
@@ -336,7 +345,7 @@ def act_backward(dH, kept: MxMatrix, activation="gelu", dZ=None, dbias=None, wor
             raise ValueError(f"dbias must be a contiguous float32 tensor of {cols} elements")
         if workspace is None:
             workspace = _empty(dg_act_backward_workspace_size(rows, cols), torch.uint8, dH.device, stream)  # noqa: F821
-    ws, wsb = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    ws, wsb = _workspace(workspace)
     index, handle = _stream_of(stream, (dH, kept.q, kept.s, dZ, dbias, workspace))
     _call("dg_act_backward", index, rows, cols, dH.data_ptr(), ldh, kept.code, kept.q.data_ptr(), kept.ldq,
           kept.s.data_ptr(), kept.lds, dZ.data_ptr(), ldz, _elem(dH, "dH"), _ACTIVATIONS[activation],

@@ -324,6 +324,8 @@ int dg_mx_dequantize(int64_t rows, int64_t cols, dg_mx_t format, const void *Q, 
  * error by norm (below a 16-bit C's rounding).
  *   M == 0 or N == 0: nothing is done; K == 0 or alpha == 0: A and B are not
  *   read, C = act(beta * C + bias); beta == 0: C is not read.
+ *   DG_ERR_UNSUPPORTED: more tiles or rows than a launch holds (outputs of
+ *   about 2^38 elements).
  *   1 M, 2 N, 3 K, 4 alpha, 5 formatA, 6 A, 7 lda (bytes), 8 SA, 9 ldsa,
  *   10 formatB, 11 B, 12 ldb (bytes), 13 SB, 14 ldsb, 15 beta, 16 C, 17 ldc,
  *   18 type, 19 bias, 20 epilogue, 21 stream. */

@@ -232,6 +232,7 @@ def test_torch_functions_refuse():
         lambda: dg.gemm_dq(torch.zeros(3, 7, dtype=torch.float16), w),
         lambda: dg.gemm_dq(torch.zeros(3, 5, dtype=torch.float16), w, beta=1.0),
         lambda: dg.gemm_dq(torch.zeros(3, 5, dtype=torch.float16), w),
+        lambda: dg.gemm_dq(torch.zeros(3, 5, dtype=torch.float16), w, workspace=torch.zeros(64, 2)[:, 0]),
         lambda: dg.act_checkpoint(x, "none"),
         lambda: dg.act_checkpoint(x, "gelu", out=_mx("mxfp8", 4, 39)),
         lambda: dg.act_checkpoint(x, "gelu"),

@@ -275,7 +275,7 @@ int dg_act_checkpoint(int64_t rows, int64_t cols, const void *Z, int64_t ldz, vo
 size_t dg_act_backward_workspace_size(int64_t rows, int64_t cols)
 {
     if (rows <= 0 || cols <= 0 || rows > kMaxDim || cols > kMaxDim) return 0;
-    return (size_t)dg::act_backward_slices(rows, cols) * (size_t)cols * 4;
+    return (size_t)dg::act_backward_slices(rows, cols, true) * (size_t)cols * 4;
 }
 
 int dg_act_backward(int64_t rows, int64_t cols, const void *dH, int64_t ldh, dg_mx_t format, const void *Q, int64_t ldq,
@@ -319,8 +319,8 @@ int dg_act_backward(int64_t rows, int64_t cols, const void *dH, int64_t ldh, dg_
     p.act = activation;
     p.dbias = dbias;
     p.ws = (float *)workspace;
-    p.band = dg::act_backward_band(rows, cols);
-    p.slices = rows > 0 ? dg::act_backward_slices(rows, cols) : 0;   // no rows: the sums are zero
+    p.band = dg::act_backward_band(rows, cols, dbias != nullptr);
+    p.slices = rows > 0 ? dg::act_backward_slices(rows, cols, dbias != nullptr) : 0;   // no rows: the sums are zero
     return dg::launch_status(dg::launch_act_backward(p, (hipStream_t)stream));
 }
 

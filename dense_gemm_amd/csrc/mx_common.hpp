@@ -50,15 +50,15 @@ struct MxParams {
     int32_t act;          // ACT_RELU, ACT_GELU
     float *dbias;         // backward: column sums of dZ (NULL: none)
     float *ws;            // backward: partial column sums, [slices][cols]
-    int32_t slices, band; // row slices of the backward's launch, rows of a band (4, 8 or 16)
+    int32_t slices, band; // row slices of the backward's launch, rows of a band (8, 16 or 32)
 };
 
 hipError_t launch_mx_quantize(const MxParams &p, hipStream_t s);
 hipError_t launch_mx_dequantize(const MxParams &p, hipStream_t s);
 hipError_t launch_act_checkpoint(const MxParams &p, hipStream_t s);
 hipError_t launch_act_backward(const MxParams &p, hipStream_t s);
-int act_backward_band(int64_t rows, int64_t cols);
-int act_backward_slices(int64_t rows, int64_t cols);
+int act_backward_band(int64_t rows, int64_t cols, bool sums);
+int act_backward_slices(int64_t rows, int64_t cols, bool sums);
 
 #ifdef __HIPCC__
 

@@ -7,9 +7,12 @@
 // exchanges; a wave covers 512 columns of one row.  The scale byte is stored
 // by one lane of the four.  At 32768 x 5632 (bf16): rounding to mxfp8 100 us
 // (5.6 TB/s), to mxfp4 88 (5.3), back from mxfp8 101 (5.5); the checkpoint 158
-// us with relu (5.9), 174 with gelu (5.3); the backward 183 with relu (5.1), 198
-// with gelu and 204 with the column sums (4.5).  A plain copy of 1 GiB runs at
-// 5.1 TB/s on this card.
+// us with relu (5.9), 176 with gelu (5.3); the backward 169 with relu or gelu
+// (5.5) and 184 with the column sums (5.0).  A plain copy of 1 GiB runs at 5.1
+// TB/s on this card.  Stores stay ordinary ones: non-temporal stores of H, dZ
+// and Y gain 3-25% when the pass is timed alone at this size and lose where the
+// result is read next (checkpoint and the product on it, 2048 x 5632 by 2048:
+// 64.6 us against 57.5).
 #include "mx_common.hpp"
 
 namespace dg {
@@ -31,7 +34,7 @@ template <typename T>
 __device__ __forceinline__ void load8(const T *row, int64_t col, int64_t n, float (&v)[8])
 {
     if (col + 8 <= n) {
-        const typename Eight<T>::V8 a = *(const typename Eight<T>::V8u *)(row + col);
+                const typename Eight<T>::V8 a = *(const typename Eight<T>::V8u *)(row + col);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = (float)a[i];
     } else {
@@ -284,48 +287,49 @@ __device__ __forceinline__ float act_slope(int act, float z)
 
 // dZ = dH * act'(z8), and the column sums of dZ (before its rounding) into
 // one row of partial sums per slice of rows.  Workgroup (c, s) takes 512
-// columns and every slices-th band of rows from band s on (so the bands
-// under way at a time lie side by side in memory), its four waves every fourth
-// row, four rows' loads in flight each; the waves' sums meet in LDS, in wave
-// order, so the sum's order is fixed.
+// columns and every slices-th band of rows from band s on; its eight waves take
+// every eighth row of a band, one row at a time: what is in flight over the
+// chip is then one stretch of memory that moves forward with the dispatch.  (With
+// four rows' loads in flight per wave, or fewer workgroups that stay and stride
+// over the rows, the streams spread: 32768 x 5632 with relu and no sums took
+// 202-262 us against 168.)  The waves' sums meet in LDS, in wave order, so
+// the sum's order is fixed.
 template <typename T, int FORMAT>
-__global__ __launch_bounds__(256) void act_backward_kernel(MxParams p)
+__global__ __launch_bounds__(512) void act_backward_kernel(MxParams p)
 {
-    __shared__ float part[4][512];
+    __shared__ float part[8][512];
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     const int64_t col = (int64_t)blockIdx.x * 512 + lane * 8;
     float sum[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) sum[i] = 0.f;
     if (col < p.cols) {
-        for (int64_t row = (int64_t)blockIdx.y * p.band + wave; row < p.rows; row += (int64_t)p.slices * p.band) {
-            float z[4][8], d[4][8];
+        for (int64_t r0 = (int64_t)blockIdx.y * p.band; r0 < p.rows; r0 += (int64_t)p.slices * p.band) {
+            const int64_t end = r0 + p.band < p.rows ? r0 + p.band : p.rows;
+#pragma unroll 1
+            for (int64_t row = r0 + wave; row < end; row += 8) {
+                float z[8], d[8];
+                load8<T>((const T *)p.X + row * p.ldx, col, p.cols, d);
+                load_codes<FORMAT>(p, row, col, z);
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-                if (4 * u < p.band && row + 4 * u < p.rows) {
-                    load8<T>((const T *)p.X + (row + 4 * u) * p.ldx, col, p.cols, d[u]);
-                    load_codes<FORMAT>(p, row + 4 * u, col, z[u]);
+                for (int i = 0; i < 8; ++i) {
+                    d[i] *= act_slope(p.act, z[i]);
+                    sum[i] += d[i];
                 }
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-                if (4 * u < p.band && row + 4 * u < p.rows) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        d[u][i] *= act_slope(p.act, z[u][i]);
-                        sum[i] += d[u][i];
-                    }
-                    store8<T>((T *)p.Y + (row + 4 * u) * p.ldy, col, p.cols, d[u]);
-                }
+                store8<T>((T *)p.Y + row * p.ldy, col, p.cols, d);
+            }
         }
     }
     if (!p.dbias) return;
 #pragma unroll
     for (int i = 0; i < 8; ++i) part[wave][lane * 8 + i] = sum[i];
     __syncthreads();
-    for (int c = threadIdx.x; c < 512; c += 256) {
-        const int64_t gc = (int64_t)blockIdx.x * 512 + c;
-        if (gc < p.cols)
-            p.ws[(int64_t)blockIdx.y * p.cols + gc] = ((part[0][c] + part[1][c]) + part[2][c]) + part[3][c];
+    const int64_t gc = (int64_t)blockIdx.x * 512 + threadIdx.x;
+    if (gc < p.cols) {
+        float t = part[0][threadIdx.x];
+#pragma unroll
+        for (int w = 1; w < 8; ++w) t += part[w][threadIdx.x];
+        p.ws[(int64_t)blockIdx.y * p.cols + gc] = t;
     }
 }
 
@@ -408,32 +412,31 @@ hipError_t launch_act_checkpoint(const MxParams &p, hipStream_t s)
     return launch((const void *)DG_BY_TYPE(DG_BY_FORMAT8, checkpoint_fn), grid_for(row_items(p)), dim3(256), s, p);
 }
 
-// Rows of a band of the backward: 16, so that a wave has four rows' loads in
-// flight, or fewer where that would leave fewer than two workgroups per compute
-// unit.  fp16, with the column sums, bands of 4 / 8 / 16: 64 x 5632 5.8 / 6.9 /
-// 8.8 us, 512 x 5632 10.8 / 9.5 / 10.1, 2048^2 14.3 / 12.1 / 10.4, 8192 x 5632
-// 61.2 / 60.5 / 58.5.
-int act_backward_band(int64_t rows, int64_t cols)
+// Rows of a band of the backward: 32 (four a wave) where that leaves four
+// workgroups per compute unit; else 16 for the column sums, which halves the
+// partial sums, or 8.  Bands of 8 / 16 / 32, fp16, relu, with the sums: 512 x 5632
+// 7.6 / 7.4 / 8.3 us, 2048^2 8.4 / 7.7 / 9.4, 8192 x 5632 49 / 44 / 41, 32768 x 5632
+// 207 / 186 / 182; without: 512 x 5632 4.0 / 4.6 / 5.8, 2048^2 4.7 / 5.0 / 6.0.
+int act_backward_band(int64_t rows, int64_t cols, bool sums)
 {
     const int64_t chunks = (cols + 511) / 512;
-    return (rows + 15) / 16 * chunks >= 512 ? 16 : (rows + 7) / 8 * chunks >= 512 ? 8 : 4;
+    if ((rows + 31) / 32 * chunks >= 1024) return 32;
+    return sums && (rows + 15) / 16 * chunks >= 256 ? 16 : 8;
 }
 
-// Row slices: about 2048 workgroups (8 per compute unit) over the column
-// chunks, at least a band each.
-int act_backward_slices(int64_t rows, int64_t cols)
+// Row slices: a band each, up to 4096 (the grid's second dimension is small, and
+// so is the workspace).
+int act_backward_slices(int64_t rows, int64_t cols, bool sums)
 {
-    const int64_t chunks = (cols + 511) / 512, band = act_backward_band(rows, cols);
-    int64_t s = 2048 / chunks;
-    if (s > (rows + band - 1) / band) s = (rows + band - 1) / band;
-    return s < 1 ? 1 : (int)s;
+    const int64_t band = act_backward_band(rows, cols, sums), s = (rows + band - 1) / band;
+    return s < 4096 ? (int)s : 4096;
 }
 
 hipError_t launch_act_backward(const MxParams &p, hipStream_t s)
 {
     if (p.slices > 0) {
         const dim3 grid((unsigned)((p.cols + 511) / 512), (unsigned)p.slices);
-        const hipError_t e = launch((const void *)DG_BY_TYPE(DG_BY_FORMAT8, backward_fn), grid, dim3(256), s, p);
+        const hipError_t e = launch((const void *)DG_BY_TYPE(DG_BY_FORMAT8, backward_fn), grid, dim3(512), s, p);
         if (e != hipSuccess || !p.dbias) return e;
     }
     return launch((const void *)&column_sum_kernel, grid_for((p.cols + 15) / 16), dim3(256), s,

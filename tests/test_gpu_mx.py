@@ -614,3 +614,20 @@ def test_long_rows_and_many_rows():
     A[0, -1], A[1, 0] = 1, 1
     got = dg.gemm_dq(A, tail, out_dtype=torch.float32)
     assert torch.equal(got, torch.stack([h[-1, cols // 256 * 256:], h[0, cols // 256 * 256:]]).float())
+
+
+@pytest.mark.parametrize("rows,cols", [(8, 9), (33, 8), (511, 5631), (4096 * 8 + 5, 24), (131072 + 37, 8)])
+def test_backward_bands_and_slices(rows, cols):
+    # a band short of its eight waves, 16- and 32-row bands, more bands than slices
+    g = torch.Generator(device="cuda").manual_seed(rows + cols)
+    z = torch.randn(rows, cols, generator=g, device="cuda")
+    d = torch.randn(rows, cols, generator=g, device="cuda").to(torch.bfloat16)
+    m = dg.quantize_mx(z, format="mxfp8")
+    db = torch.empty(cols, device="cuda")
+    out = dg.act_backward(d, m, "relu", dbias=db)
+    want = torch.where(dg.dequantize_mx(m, dtype=torch.float32) > 0, d.double(), 0.0)
+    assert torch.equal(out.double(), want)
+    assert torch.equal(dg.act_backward(d, m, "relu"), out)
+    # fp32 sums: below one rounding per row added
+    bound = rows * 2.0 ** -24 * want.abs().sum(0)
+    assert ((db.double() - want.sum(0)).abs() <= bound + 1e-30).all()

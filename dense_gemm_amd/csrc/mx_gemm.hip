@@ -145,7 +145,7 @@ struct MxScales {
 // twice as long).  256 x 256: eight 128 x 64 waves; four 128 x 128 ones, a
 // quarter fewer LDS reads, took 268 us.  What bounds it is the matrix cores at
 // the clock that they hold under this load.  128 x 128 (two workgroups a
-// unit) and 64 x 64 (three) serve outputs with fewer tiles than units, where a
+// unit) and 64 x 64 (two, three with mxfp8) serve outputs with fewer tiles than units, where a
 // slab's latency counts: 0.23 us a slab of the 64 x 64 tile, 0.36 of the
 // 128 x 128 one.
 template <int FA, int BM, int BN, int WM, int WN, int STAGES>

@@ -424,12 +424,15 @@ int act_backward_band(int64_t rows, int64_t cols, bool sums)
     return sums && (rows + 15) / 16 * chunks >= 256 ? 16 : 8;
 }
 
-// Row slices: a band each, up to 4096 (the grid's second dimension is small, and
-// so is the workspace).
+// Row slices: a band each, up to 4096 (the grid's second dimension and the
+// workspace stay small) and to a grid of 2^22 workgroups (2^31 threads).
 int act_backward_slices(int64_t rows, int64_t cols, bool sums)
 {
-    const int64_t band = act_backward_band(rows, cols, sums), s = (rows + band - 1) / band;
-    return s < 4096 ? (int)s : 4096;
+    const int64_t chunks = (cols + 511) / 512, band = act_backward_band(rows, cols, sums);
+    int64_t s = (rows + band - 1) / band;
+    if (s > 4096) s = 4096;
+    if (s > (1 << 22) / chunks) s = (1 << 22) / chunks;
+    return s < 1 ? 1 : (int)s;
 }
 
 hipError_t launch_act_backward(const MxParams &p, hipStream_t s)

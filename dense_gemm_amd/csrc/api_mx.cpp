@@ -12,7 +12,7 @@ namespace dg {
 launch_fn scale_launcher(int dtype);
 launch_fn splitk_reduce_launcher(int dtype);
 int launch_status(hipError_t err);
-mx_launch_fn mx_gemm_launcher(int config, int format_a);
+mx_launch_fn mx_gemm_launcher(int config, int format_a, bool exact);
 mx_launch_fn dq_gemm_launcher(int type, int config, int format, int ta, int direct);
 }  // namespace dg
 
@@ -82,8 +82,11 @@ bool mx_supports(int k, int64_t M, int64_t N, int64_t lda, int64_t ldb)
 // 32 x 8192 x 8192 rows 22.9, tile 17.9; 64 x 2048 x 2048 rows 4.8, tile 6.8;
 // 512 x 5632 x 2048 64-tile 12.4, 128-tile 12.2; 1024 x 8192 x 8192 128-tile
 // 60.6, 256-tile 80.3; mxfp4 both, 2048 x 8192 x 4096 128-tile 46.8, 256-tile
-// 40.6.
-int mx_choose(bool a4, int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb)
+// 40.6.  `exact` (mxfp8 with an fp32 C) takes two matrix instructions for one on the
+// tiled kernels: 32 x 8192 x 8192 rows 23, 64-tile 31; 512 x 5632 x 2048 64-tile
+// 17.4, 128-tile 19.7; 1024 x 8192 x 8192 128-tile 102, 64-tile 139; 4096^3 256-tile
+// 100, 128-tile 106.
+int mx_choose(bool a4, bool exact, int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb)
 {
     const double slabs = (double)ceil_div(K, a4 ? 256 : 128);
     auto tiles = [&](int64_t b) { return (double)ceil_div(M, b) * (double)ceil_div(N, b); };
@@ -94,9 +97,9 @@ int mx_choose(bool a4, int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb
     const double cost[kNumMx] = {
         2.5 + (1.6e-6 + (a4 ? 0.05e-6 : 0.1e-6) * (double)(M < 16 ? M : 16)) * (double)ceil_div(M, 16) * nk,
         2.7 + 5.0e-6 * (double)ceil_div(M, 32) * nk,
-        3.1 + slabs * (a4 ? 0.28 : 0.23) * at_least_1(tiles(64) / 270) + mb / 4,
-        5.8 + slabs * (a4 ? 0.50 : 0.36) * at_least_1(tiles(128) / 212),
-        9.0 + slabs * (a4 ? 1.4 : 1.2) * (full + (t256 > full * 256 ? (full > 0 ? 0.82 : 1.) : 0.)),
+        3.1 + slabs * (a4 ? 0.28 : exact ? 0.42 : 0.23) * at_least_1(tiles(64) / (exact ? 430 : 270)) + mb / 4,
+        5.8 + slabs * (a4 ? 0.50 : exact ? 0.70 : 0.36) * at_least_1(tiles(128) / 212),
+        9.0 + slabs * (a4 ? 1.4 : exact ? 2.6 : 1.2) * (full + (t256 > full * 256 ? (full > 0 ? 0.82 : 1.) : 0.)),
     };
     int best = -1;
     for (int k = 0; k < kNumMx; ++k)
@@ -374,13 +377,14 @@ int dg_gemm_mx_with_kernel(int64_t M, int64_t N, int64_t K, float alpha, dg_mx_t
     p.ldsb = ldsb;
     p.ctype = type;
     if (!reads) return dg::launch_status(dg::scale_launcher(c_dtype(type))(p.g, (hipStream_t)stream));
-    if (kernel == DG_KERNEL_AUTO) kernel = mx_choose(formatA == DG_MXFP4, M, N, K, lda, ldb);
+    const bool exact = formatA == DG_MXFP8 && type == DG_ELEM_F32;
+    if (kernel == DG_KERNEL_AUTO) kernel = mx_choose(formatA == DG_MXFP4, exact, M, N, K, lda, ldb);
     if (kernel < 0 || !mx_supports(kernel, M, N, lda, ldb)) return DG_ERR_UNSUPPORTED;
     const MxFamily &f = kMx[kernel];
     p.g.tiles_m = (int32_t)ceil_div(M, f.bm);
     p.g.tiles_n = (int32_t)ceil_div(N, f.bn);
     p.g.group_m = f.group_m;
-    return dg::launch_status(dg::mx_gemm_launcher(kernel, formatA)(p, (hipStream_t)stream));
+    return dg::launch_status(dg::mx_gemm_launcher(kernel, formatA, exact)(p, (hipStream_t)stream));
 }
 
 int dg_gemm_mx(int64_t M, int64_t N, int64_t K, float alpha, dg_mx_t formatA, const void *A, int64_t lda, const void *SA,
@@ -397,7 +401,7 @@ int dg_gemm_mx_select(dg_mx_t formatA, int64_t M, int64_t N, int64_t K)
     if (M < 0 || M > kMaxDim) return -2;
     if (N < 0 || N > kMaxDim) return -3;
     if (K < 0 || K > kMaxDim - dg::MX_GROUP) return -4;
-    return mx_choose(formatA == DG_MXFP4, M, N, K, row_bytes(formatA, K), row_bytes(DG_MXFP4, K));
+    return mx_choose(formatA == DG_MXFP4, false, M, N, K, row_bytes(formatA, K), row_bytes(DG_MXFP4, K));
 }
 
 const char *dg_gemm_mx_kernel_name(int kernel) { return kernel >= 0 && kernel < kNumMx ? kMx[kernel].name : nullptr; }

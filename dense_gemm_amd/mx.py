@@ -249,7 +249,10 @@ def gemm_mx(A: MxMatrix, B: MxMatrix, C=None, alpha=1.0, beta=0.0, bias=None, ac
     """C = act(alpha * A @ B^T + beta * C + bias): A [M, K] in mxfp4 or mxfp8,
     B [N, K] in mxfp4.  C (allocated with `out_dtype` when None, beta 0 then)
     is [M, N]; bias has N elements of C's dtype; activation is "none", "relu"
-    or "gelu"."""
+    or "gelu".  Sums are fp32; with an mxfp8 A, more than a few rows and a 16-bit
+    C, products far below their neighbours' largest are cut (1e-5 of the result by
+    norm, see include/dense_gemm.h), which an fp32 C avoids at up to twice the
+    time."""
     M, K, N = A.rows, A.cols, B.rows
     if B.cols != K:
         raise ValueError(f"inner dimensions differ: {K} vs {B.cols}")

@@ -631,3 +631,37 @@ def test_backward_bands_and_slices(rows, cols):
     # fp32 sums: below one rounding per row added
     bound = rows * 2.0 ** -24 * want.abs().sum(0)
     assert ((db.double() - want.sum(0)).abs() <= bound + 1e-30).all()
+
+
+@pytest.mark.parametrize("ty", list(T))
+@pytest.mark.parametrize("kernel", range(len(dg.mx_kernel_names())))
+def test_product_keeps_small_beside_large(kernel, ty):
+    """Each row of A holds one group of 8 neighbouring k with elements from 2^-9
+    to 2^7, in every other row with two of 128 that cancel.  Sums are multiples of
+    2^-10 below 8 * 128 * 6 < 2^13, so an fp32 sum is exact in any order: an fp32
+    C and the row kernels keep all of it.  The tiled kernels with a 16-bit C cut
+    each product to 2^-13 of the group's largest, 8 of them at most."""
+    rng = np.random.default_rng(24)
+    codes = np.flatnonzero(np.isfinite(mx_ref.FP8) & (np.abs(mx_ref.FP8) <= 128))
+    for M, N, K in ((1, 40, 2048), (5, 17, 64), (33, 65, 300), (130, 270, 1030)):
+        ca = np.zeros((M, mx_ref.groups(K) * 256), np.int64)
+        for m in range(M):
+            at = 8 * rng.integers(0, K // 8)
+            ca[m, at:at + 8] = codes[rng.integers(0, len(codes), 8)]
+            if m % 2 == 0:
+                ca[m, at:at + 2] = np.flatnonzero(mx_ref.FP8 == 128)[0], np.flatnonzero(mx_ref.FP8 == -128)[0]
+        cb = rng.integers(0, 16, (N, mx_ref.groups(K) * 256))
+        cb[:, 1::2] = cb[:, ::2]
+        cb[:, K:] = 0
+        qa, qb = mx_ref.pack(ca, "mxfp8"), mx_ref.pack(cb, "mxfp4")
+        sa, sb = (np.full((mx_ref.groups(K), n, 8), 127, np.uint8) for n in (M, N))
+        a, b = mx_ref.values(qa, sa, "mxfp8", K), mx_ref.values(qb, sb, "mxfp4", K)
+        A = dg.MxMatrix("mxfp8", M, K, torch.from_numpy(qa).to(DEV), torch.from_numpy(sa).to(DEV))
+        B = dg.MxMatrix("mxfp4", N, K, torch.from_numpy(qb).to(DEV), torch.from_numpy(sb).to(DEV))
+        got = dg.gemm_mx(A, B, out_dtype=T[ty], kernel=kernel)
+        want = a @ b.T
+        if ty == "f32" or dg.mx_kernel_names()[kernel].endswith("_rows"):
+            assert torch.equal(got.cpu(), torch.from_numpy(want).to(T[ty])), (M, N, K)
+        else:
+            cut = 8 * 2.0 ** -13 * np.stack([(np.abs(r) * np.abs(b)).max(1) for r in a])
+            assert (np.abs(np64(got) - want) <= cut * (1 + HALF[T[ty]]) + HALF[T[ty]] * np.abs(want) + TINY[T[ty]]).all(), (M, N, K)

@@ -264,16 +264,17 @@ __global__ __launch_bounds__(256) void act_checkpoint_kernel(MxParams p)
     }
 }
 
-// act'(z).  relu: 1 above zero, else 0 (NaN stays NaN).  gelu = z Phi(z):
-// Phi(z) + z phi(z), with phi the normal density and Phi by the same
+// d * act'(z).  relu chooses instead of multiplying: d above zero, else 0
+// whatever d is (an infinity or a NaN too), and NaN for a NaN z.  gelu = z Phi(z),
+// its slope Phi(z) + z phi(z), with phi the normal density and Phi by the same
 // approximation of erfc as the forward (Abramowitz & Stegun 7.1.26) on
 // q = erfc(|z| / sqrt 2): Phi = 1 - q/2 for z >= 0 and q/2 below (its constants
 // carry the 1/sqrt 2 and the 1/2).  exp(-z^2/2) serves both terms.  In z phi(z)
 // z is clamped to 14, where the density has underflowed, so that an infinity
 // gives 1 or 0 and not inf * 0 (a NaN comes through Phi).
-__device__ __forceinline__ float act_slope(int act, float z)
+__device__ __forceinline__ float act_gradient(int act, float z, float d)
 {
-    if (act == ACT_RELU) return z > 0.f ? 1.f : (z <= 0.f ? 0.f : z);
+    if (act == ACT_RELU) return z > 0.f ? d : (z <= 0.f ? 0.f : z);
     const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.3275911f * 0.70710678f, __builtin_fabsf(z), 1.f));
     float poly = __builtin_fmaf(t, 0.5f * 1.061405429f, 0.5f * -1.453152027f);
     poly = __builtin_fmaf(t, poly, 0.5f * 1.421413741f);
@@ -282,7 +283,7 @@ __device__ __forceinline__ float act_slope(int act, float z)
     const float ex = __builtin_amdgcn_exp2f(z * z * -0.72134752f);   // 2^(-z^2/2 * log2 e)
     const float hq = poly * t * ex;
     const float cdf = z >= 0.f ? 1.f - hq : hq;
-    return __builtin_fmaf(__builtin_amdgcn_fmed3f(z, -14.f, 14.f) * 0.3989422804014327f, ex, cdf);
+    return d * __builtin_fmaf(__builtin_amdgcn_fmed3f(z, -14.f, 14.f) * 0.3989422804014327f, ex, cdf);
 }
 
 // dZ = dH * act'(z8), and the column sums of dZ (before its rounding) into
@@ -313,7 +314,7 @@ __global__ __launch_bounds__(512) void act_backward_kernel(MxParams p)
                 load_codes<FORMAT>(p, row, col, z);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    d[i] *= act_slope(p.act, z[i]);
+                    d[i] = act_gradient(p.act, z[i], d[i]);
                     sum[i] += d[i];
                 }
                 store8<T>((T *)p.Y + row * p.ldy, col, p.cols, d);

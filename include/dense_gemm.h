@@ -385,7 +385,8 @@ int dg_act_checkpoint(int64_t rows, int64_t cols, const void *Z, int64_t ldz, vo
                       int64_t lds, void *stream);
 
 /* dZ = dH * act'(z) with z the values of (Q, S) (kept by dg_act_checkpoint or
- * dg_mx_quantize): relu'(z) = 1 for z > 0, else 0; gelu'(z) = Phi(z) + z phi(z).
+ * dg_mx_quantize).  relu: dH where z > 0, else 0 (an infinite or NaN dH too);
+ * gelu: dH times Phi(z) + z phi(z).  Where z is NaN, dZ is.
  * dZ may be dH itself (with ldz = ldh).  dbias (fp32, cols elements; NULL for
  * none) receives the column sums of dZ before its rounding, in a fixed order
  * of summation; it needs a workspace of dg_act_backward_workspace_size bytes

@@ -665,3 +665,21 @@ def test_product_keeps_small_beside_large(kernel, ty):
         else:
             cut = 8 * 2.0 ** -13 * np.stack([(np.abs(r) * np.abs(b)).max(1) for r in a])
             assert (np.abs(np64(got) - want) <= cut * (1 + HALF[T[ty]]) + HALF[T[ty]] * np.abs(want) + TINY[T[ty]]).all(), (M, N, K)
+
+
+@pytest.mark.parametrize("ty", list(T))
+def test_relu_gradient_of_infinities(ty):
+    """An overflowed gradient at a unit that relu switched off does not reach dZ
+    or the bias gradient; at one that is on it does; a NaN z gives NaN."""
+    z = torch.tensor([[-1.0, 0.0, -0.0, 2.0], [-3.0, -1e-30, 1.0, 2.0]], device=DEV).repeat(1, 8)
+    d = torch.tensor([[math.inf, -math.inf, math.nan, 1.0], [math.nan, math.inf, -math.inf, math.nan]], device=DEV, dtype=T[ty]).repeat(1, 8)
+    for fmt in ("mxfp8", "mxint8"):
+        m = dg.quantize_mx(z, format=fmt)
+        db = torch.empty(32, device=DEV)
+        got = np64(dg.act_backward(d, m, "relu", dbias=db))
+        want = np.tile([[0, 0, 0, 1], [0, 0, -math.inf, math.nan]], 8)
+        assert np.array_equal(got, want, equal_nan=True)
+        assert np.array_equal(np64(db), want.sum(0), equal_nan=True)
+        m.s[0, 0, 0] = 255
+        got = np64(dg.act_backward(d, m, "relu"))
+        assert np.isnan(got[0]).all() and np.array_equal(got[1], want[1], equal_nan=True)

@@ -19,7 +19,7 @@ LIB_PATH = os.path.join(_HERE, "libdense_gemm_amd.so")
 
 DG_OP_N, DG_OP_T = 0, 1
 DG_F32, DG_F16_F32ACC, DG_BF16_F32ACC, DG_F16_F32OUT, DG_BF16_F32OUT = 0, 1, 2, 3, 4
-DG_EPI_NONE, DG_EPI_RELU, DG_EPI_GELU = 0, 1, 2
+DG_EPI_NONE, DG_EPI_RELU, DG_EPI_GELU, DG_EPI_RELU_POSITIVE = 0, 1, 2, 4
 EPILOGUES = {"none": DG_EPI_NONE, "relu": DG_EPI_RELU, "gelu": DG_EPI_GELU}
 DG_OK, DG_ERR_UNSUPPORTED, DG_ERR_SCRATCH, DG_ERR_HIP = 0, -100, -101, -200
 DG_SCRATCH_BYTES = 16 * 1024 * 1024

@@ -251,7 +251,7 @@ int dg_act_checkpoint(int64_t rows, int64_t cols, const void *Z, int64_t ldz, vo
     if (ldz < (cols > 1 ? cols : 1)) return -4;
     if (any && (H == nullptr || !aligned(H, elem_size(type)))) return -5;
     if (ldh < (cols > 1 ? cols : 1) || (H == Z && any && ldh != ldz)) return -6;
-    if (activation != DG_EPI_RELU && activation != DG_EPI_GELU) return -8;
+    if (activation != DG_EPI_RELU && activation != DG_EPI_GELU && activation != DG_EPI_RELU_POSITIVE) return -8;
     if (format != DG_MXFP8 && format != DG_MXINT8) return -9;
     if (any && bad_q(Q)) return -10;
     if (bad_ldq(ldq, format, cols)) return -11;
@@ -271,7 +271,8 @@ int dg_act_checkpoint(int64_t rows, int64_t cols, const void *Z, int64_t ldz, vo
     p.cols = cols;
     p.type = type;
     p.format = format;
-    p.act = activation;
+    p.act = activation == DG_EPI_GELU ? DG_EPI_GELU : DG_EPI_RELU;
+    p.positive = activation == DG_EPI_RELU_POSITIVE;
     return dg::launch_status(dg::launch_act_checkpoint(p, (hipStream_t)stream));
 }
 

@@ -48,6 +48,7 @@ struct MxParams {
     int32_t type;         // ELEM_*
     int32_t format;       // MX_*
     int32_t act;          // ACT_RELU, ACT_GELU
+    int32_t positive;     // checkpoint: z above zero is kept above zero
     float *dbias;         // backward: column sums of dZ (NULL: none)
     float *ws;            // backward: partial column sums, [slices][cols]
     int32_t slices, band; // row slices of the backward's launch, rows of a band (8, 16 or 32)
@@ -86,7 +87,9 @@ __device__ __forceinline__ uint32_t mx_scale_byte(uint32_t amax, int format)
 
 // Eight consecutive elements of a block in the format's code, `byte` the
 // block's scale: 4 bytes (mxfp4, in o[0]) or 8.  NaN blocks store zeros.
-template <int FORMAT>
+// POSITIVE (8 bits): what lies above zero stays above it, as the least positive
+// element where it would round to zero.
+template <int FORMAT, bool POSITIVE = false>
 __device__ __forceinline__ u32x2 mx_encode8(const float (&v)[8], uint32_t byte)
 {
     u32x2 o = {0u, 0u};
@@ -106,8 +109,10 @@ __device__ __forceinline__ u32x2 mx_encode8(const float (&v)[8], uint32_t byte)
         const int e = 127 - (int)byte;
         float x[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < 8; ++i) {
             x[i] = __builtin_amdgcn_fmed3f(__builtin_amdgcn_ldexpf(v[i], e), -448.f, 448.f);
+            if (POSITIVE && v[i] > 0.f) x[i] = __builtin_fmaxf(x[i], 0x1p-9f);
+        }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             int w = 0;
@@ -119,7 +124,8 @@ __device__ __forceinline__ u32x2 mx_encode8(const float (&v)[8], uint32_t byte)
         const int e = 6 + 127 - (int)byte;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float x = __builtin_amdgcn_fmed3f(__builtin_rintf(__builtin_amdgcn_ldexpf(v[i], e)), -127.f, 127.f);
+            float x = __builtin_amdgcn_fmed3f(__builtin_rintf(__builtin_amdgcn_ldexpf(v[i], e)), -127.f, 127.f);
+            if (POSITIVE && v[i] > 0.f) x = __builtin_fmaxf(x, 1.f);
             o[i >> 2] |= ((uint32_t)(int)x & 255u) << (8 * (i & 3));
         }
     }

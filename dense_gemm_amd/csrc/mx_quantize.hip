@@ -75,11 +75,11 @@ __device__ __forceinline__ uint32_t block_amax(const float (&v)[8])
 }
 
 // Codes and scale of the 8 elements a lane holds, col a multiple of 8.
-template <int FORMAT>
+template <int FORMAT, bool POSITIVE = false>
 __device__ __forceinline__ void store_codes(const MxParams &p, int64_t row, int64_t col, const float (&v)[8])
 {
     const uint32_t byte = mx_scale_byte(block_amax(v), FORMAT);
-    const u32x2 q = mx_encode8<FORMAT>(v, byte);
+    const u32x2 q = mx_encode8<FORMAT, POSITIVE>(v, byte);
     uint8_t *qr = p.Q + row * p.ldq;
     if constexpr (FORMAT == MX_FP4) *(uint32_t *)(qr + col / 2) = q[0];
     else *(u32x2 *)(qr + col) = q;
@@ -247,8 +247,9 @@ __global__ __launch_bounds__(256) void mx_dequantize_kernel(MxParams p)
 }
 
 // h = act(z) and z in 8 bits, one read of z.  H may be Z itself: a lane
-// reads its elements before it writes them.
-template <typename T, int FORMAT>
+// reads its elements before it writes them.  POSITIVE: see mx_encode8 (32768 x
+// 5632 relu: mxfp8 157 us with and without, mxint8 161 and 158).
+template <typename T, int FORMAT, bool POSITIVE>
 __global__ __launch_bounds__(256) void act_checkpoint_kernel(MxParams p)
 {
     const int64_t n = row_items(p);
@@ -257,7 +258,7 @@ __global__ __launch_bounds__(256) void act_checkpoint_kernel(MxParams p)
         if (!place(p, b, row, col)) continue;
         float v[8];
         load8<T>((const T *)p.X + row * p.ldx, col, p.cols, v);
-        store_codes<FORMAT>(p, row, col, v);
+        store_codes<FORMAT, POSITIVE>(p, row, col, v);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = activate(p.act, v[i]);
         store8<T>((T *)p.Y + row * p.ldy, col, p.cols, v);
@@ -379,9 +380,9 @@ kernel_fn dequantize_fn(const MxParams &)
     return mx_dequantize_kernel<T, F>;
 }
 template <typename T, int F>
-kernel_fn checkpoint_fn(const MxParams &)
+kernel_fn checkpoint_fn(const MxParams &p)
 {
-    return act_checkpoint_kernel<T, F>;
+    return p.positive ? act_checkpoint_kernel<T, F, true> : act_checkpoint_kernel<T, F, false>;
 }
 template <typename T, int F>
 kernel_fn backward_fn(const MxParams &)

@@ -14,7 +14,7 @@ import ctypes
 
 import torch
 
-from . import DG_EPI_GELU, DG_EPI_RELU, DG_ERR_HIP, DG_KERNEL_AUTO, DG_OK, EPILOGUES, GemmError, _lib
+from . import DG_EPI_GELU, DG_EPI_RELU, DG_EPI_RELU_POSITIVE, DG_ERR_HIP, DG_KERNEL_AUTO, DG_OK, EPILOGUES, GemmError, _lib
 from . import dg_gemm_splitk_workspace_size, dg_last_hip_error, dg_status_string, hip_error_name
 
 DG_ELEM_F32, DG_ELEM_F16, DG_ELEM_BF16 = 0, 1, 2
@@ -306,15 +306,22 @@ def gemm_dq(A, B: MxMatrix, C=None, transA=False, alpha=1.0, beta=0.0, out_dtype
     return C
 
 
-def act_checkpoint(Z, activation="gelu", H=None, out=None, format="mxint8", stream=None):
+def act_checkpoint(Z, activation="gelu", H=None, out=None, format="mxint8", stream=None, keep_positive=False):
     """(H, kept): H = act(Z) ("relu" or "gelu") and Z in 8 bits ("mxfp8" or
     "mxint8") for act_backward, in one pass.  H may be Z itself; `out` (an
-    MxMatrix) sets the format when given."""
+    MxMatrix) sets the format when given.
+
+    With relu, a positive Z that rounds to zero loses its gradient (1.1% of the
+    positive elements of normal data in mxint8, 0.0005% in mxfp8).
+    `keep_positive` rounds those to the format's least positive element, so that
+    act_backward's mask is that of Z itself; nothing else changes."""
     if Z.dim() != 2:
         raise ValueError("Z must be 2-D")
     rows, cols = Z.shape
     if activation not in _ACTIVATIONS:
         raise ValueError(f"activation must be one of {sorted(_ACTIVATIONS)}")
+    if keep_positive and activation != "relu":
+        raise ValueError("keep_positive goes with relu")
     if H is None:
         H = _empty((rows, cols), Z.dtype, Z.device, stream)
     elif H.dtype != Z.dtype:
@@ -326,7 +333,8 @@ def act_checkpoint(Z, activation="gelu", H=None, out=None, format="mxint8", stre
     ldz, ldh = _plain(Z, "Z", rows, cols), _plain(H, "H", rows, cols)
     index, handle = _stream_of(stream, (Z, H, out.q, out.s))
     _call("dg_act_checkpoint", index, rows, cols, Z.data_ptr(), ldz, H.data_ptr(), ldh, _elem(Z, "Z"),
-          _ACTIVATIONS[activation], out.code, out.q.data_ptr(), out.ldq, out.s.data_ptr(), out.lds, handle)
+          DG_EPI_RELU_POSITIVE if keep_positive else _ACTIVATIONS[activation], out.code, out.q.data_ptr(), out.ldq,
+          out.s.data_ptr(), out.lds, handle)
     return H, out
 
 

@@ -683,3 +683,34 @@ def test_relu_gradient_of_infinities(ty):
         m.s[0, 0, 0] = 255
         got = np64(dg.act_backward(d, m, "relu"))
         assert np.isnan(got[0]).all() and np.array_equal(got[1], want[1], equal_nan=True)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxint8"])
+@pytest.mark.parametrize("ty", list(T))
+def test_relu_mask_is_kept(ty, fmt):
+    """keep_positive: the slope that act_backward finds is that of Z itself, down
+    to the type's least positive value beside its block's largest; only codes of
+    zero change, to 1; H, the scales and in-place use are as without."""
+    rng = np.random.default_rng(42)
+    for rows, cols, pad in ((1, 1, 0), (5, 33, 1), (70, 300, 0), (257, 1030, 3)):
+        x = rng.standard_normal((rows, cols)) * 10.0 ** rng.uniform(-6, 2, (rows, cols))
+        x[::2, ::5] = float(torch.finfo(T[ty]).smallest_normal * torch.finfo(T[ty]).eps)
+        x[::3, ::7] = 0.0
+        x[1::3, 3::7] = -0.0
+        x[rows // 2:, ::64] = 500.0
+        z = plain(rng, rows, cols, T[ty], pad)
+        z.copy_(torch.from_numpy(x).to(T[ty]))
+        h0, m0 = dg.act_checkpoint(z, "relu", format=fmt)
+        h, m = dg.act_checkpoint(z, "relu", format=fmt, keep_positive=True)
+        assert torch.equal(h, h0) and torch.equal(m.s, m0.s)
+        q0, q, v = m0.q[:, :cols], m.q[:, :cols], z.float()
+        assert torch.equal(q, torch.where((v > 0) & (q0 == 0), torch.ones_like(q0), q0)), (rows, cols)
+        assert not m.q[:, cols:].any()
+        d = torch.ones(rows, cols, dtype=T[ty], device=DEV)
+        assert torch.equal(dg.act_backward(d, m, "relu"), (v > 0).to(T[ty])), (rows, cols)
+        _, mi = dg.act_checkpoint(z, "relu", H=z, out=m0, keep_positive=True)
+        assert torch.equal(z, h) and torch.equal(mi.q, m.q) and torch.equal(mi.s, m.s)
+    z = torch.randn(4, 64, device=DEV, dtype=T[ty])      # a NaN block stays one
+    z[2, 40] = math.nan
+    _, m = dg.act_checkpoint(z, "relu", format=fmt, keep_positive=True)
+    assert m.s[0, 2, 1] == 255 and not m.q[2, 32:64].any()

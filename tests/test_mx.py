@@ -252,3 +252,12 @@ def test_torch_functions_refuse():
     ):
         with pytest.raises(TypeError):
             call()
+
+
+def test_keep_positive_goes_with_relu_in_the_checkpoint():
+    """The checkpoint's own activation value is refused everywhere else."""
+    assert dg.dg_act_backward(*dict(BWD, activation=dg.DG_EPI_RELU_POSITIVE).values()) == -13
+    assert dg.dg_gemm_mx(*dict(MX, epilogue=dg.DG_EPI_RELU_POSITIVE).values()) == -20
+    assert dg.dg_act_checkpoint(*dict(CKPT, activation=dg.DG_EPI_RELU_POSITIVE, Q=NULL).values()) == -10
+    with pytest.raises(ValueError, match="relu"):
+        dg.act_checkpoint(torch.zeros(4, 40), "gelu", keep_positive=True)

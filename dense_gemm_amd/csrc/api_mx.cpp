@@ -109,13 +109,18 @@ int mx_choose(bool a4, bool exact, int64_t M, int64_t N, int64_t K, int64_t lda,
 
 // ---- the kernels of dg_gemm_dq -------------------------------------------------
 struct DqTile {
+    const char *name;
     int bm, bn;
     double fixed, slab;      // us: the fixed part, and a slab of 64 k
     int resident;            // workgroups that fit a compute unit (LDS)
     double share;            // of a slab's time, for each of them
 };
-const DqTile kDq[] = {{32, 128, 3.0, 0.50, 4, 0.45}, {64, 128, 3.0, 0.60, 3, 0.58}, {128, 128, 4.0, 0.74, 2, 0.635},
-                      {256, 256, 10.0, 1.38, 1, 1.0}};
+const DqTile kDq[] = {
+    {"dq_32x128_tile", 32, 128, 3.0, 0.50, 4, 0.45},
+    {"dq_64x128_tile", 64, 128, 3.0, 0.60, 3, 0.58},
+    {"dq_128x128_tile", 128, 128, 4.0, 0.74, 2, 0.635},
+    {"dq_256x256_tile", 256, 256, 10.0, 1.38, 1, 1.0},   // A by direct loads only
+};
 constexpr int kNumDq = sizeof(kDq) / sizeof(kDq[0]);
 
 // K ranges of `splits` (each a multiple of 64 but the last).
@@ -418,9 +423,30 @@ int dg_gemm_dq_choose(int64_t M, int64_t N, int64_t K)
     return ranges;
 }
 
+int dg_gemm_dq_select(int64_t M, int64_t N, int64_t K)
+{
+    if (M < 0 || M > kMaxDim) return -1;
+    if (N < 0 || N > kMaxDim) return -2;
+    if (K < 0 || K > kMaxDim) return -3;
+    int tile = 0, ranges = 1;
+    if (M > 0 && N > 0 && K > 0) dq_choose(M, N, K, true, 0, &tile, &ranges);
+    return tile;
+}
+
+const char *dg_gemm_dq_kernel_name(int kernel) { return kernel >= 0 && kernel < kNumDq ? kDq[kernel].name : nullptr; }
+
 int dg_gemm_dq(dg_op_t transA, int64_t M, int64_t N, int64_t K, float alpha, const void *A, int64_t lda,
                dg_elem_t typeA, dg_mx_t formatB, const void *B, int64_t ldb, const void *SB, int64_t ldsb, float beta,
                void *C, int64_t ldc, dg_elem_t typeC, int splits, void *workspace, size_t workspace_bytes, void *stream)
+{
+    return dg_gemm_dq_with_kernel(transA, M, N, K, alpha, A, lda, typeA, formatB, B, ldb, SB, ldsb, beta, C, ldc, typeC,
+                                  splits, workspace, workspace_bytes, stream, DG_KERNEL_AUTO);
+}
+
+int dg_gemm_dq_with_kernel(dg_op_t transA, int64_t M, int64_t N, int64_t K, float alpha, const void *A, int64_t lda,
+                           dg_elem_t typeA, dg_mx_t formatB, const void *B, int64_t ldb, const void *SB, int64_t ldsb,
+                           float beta, void *C, int64_t ldc, dg_elem_t typeC, int splits, void *workspace,
+                           size_t workspace_bytes, void *stream, int kernel)
 {
     if (transA != DG_OP_N && transA != DG_OP_T) return -1;
     if (M < 0 || M > kMaxDim) return -2;
@@ -441,6 +467,7 @@ int dg_gemm_dq(dg_op_t transA, int64_t M, int64_t N, int64_t K, float alpha, con
     if (ldc < (N > 1 ? N : 1)) return -16;
     if (splits < 0 || splits > 4096) return -18;
     if (!out) return DG_OK;
+    if (kernel != DG_KERNEL_AUTO && (kernel < 0 || kernel >= kNumDq)) return DG_ERR_UNSUPPORTED;
 
     MxGemmParams p = {};
     p.g.A = A;
@@ -468,6 +495,8 @@ int dg_gemm_dq(dg_op_t transA, int64_t M, int64_t N, int64_t K, float alpha, con
     // (the choice of ranges is dg_gemm_dq_choose's, which knows no alignment)
     if (splits == 0) dq_choose(M, N, K, true, 0, &k, &splits);
     dq_choose(M, N, K, direct, splits, &k, &splits);
+    if (kernel != DG_KERNEL_AUTO) k = kernel;
+    if (k == 3 && !direct) return DG_ERR_UNSUPPORTED;
     const int64_t tm = ceil_div(M, kDq[k].bm), tn = ceil_div(N, kDq[k].bn), chunk = dq_chunk(K, splits);
     if (tm * tn * splits >= (1 << 22)) return DG_ERR_UNSUPPORTED;    // a launch of fewer than 2^31 threads
     if (splits > 1) {

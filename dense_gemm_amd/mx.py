@@ -27,6 +27,9 @@ GROUP = 256          # columns of a scale group
 _i64, _f32, _vp, _ci, _sz = ctypes.c_int64, ctypes.c_float, ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
 _MX = [_ci, _vp, _i64, _vp, _i64]                      # format, Q, ldq, S, lds
 _GEMM_MX = [_i64, _i64, _i64, _f32] + _MX + _MX + [_f32, _vp, _i64, _ci, _vp, _ci, _vp]
+_GEMM_DQ = [_ci, _i64, _i64, _i64, _f32, _vp, _i64, _ci] + _MX + [_f32, _vp, _i64, _ci, _ci, _vp, _sz, _vp]
+_GEMM_DQ_NAMES = ("transA M N K alpha A lda typeA formatB B ldb SB ldsb beta C ldc typeC splits workspace "
+                  "workspace_bytes stream")
 # name: (result, argument types, argument names in position order)
 _SIGNATURES = {
     "dg_mx_row_bytes": (_i64, [_ci, _i64], "format cols"),
@@ -41,9 +44,10 @@ _SIGNATURES = {
                                                       "ldc type bias epilogue stream kernel"),
     "dg_gemm_mx_select": (_ci, [_ci, _i64, _i64, _i64], "formatA M N K"),
     "dg_gemm_mx_kernel_name": (ctypes.c_char_p, [_ci], "kernel"),
-    "dg_gemm_dq": (_ci, [_ci, _i64, _i64, _i64, _f32, _vp, _i64, _ci] + _MX + [_f32, _vp, _i64, _ci, _ci, _vp, _sz, _vp],
-                   "transA M N K alpha A lda typeA formatB B ldb SB ldsb beta C ldc typeC splits workspace "
-                   "workspace_bytes stream"),
+    "dg_gemm_dq": (_ci, _GEMM_DQ, _GEMM_DQ_NAMES),
+    "dg_gemm_dq_with_kernel": (_ci, _GEMM_DQ + [_ci], _GEMM_DQ_NAMES + " kernel"),
+    "dg_gemm_dq_select": (_ci, [_i64, _i64, _i64], "M N K"),
+    "dg_gemm_dq_kernel_name": (ctypes.c_char_p, [_ci], "kernel"),
     "dg_gemm_dq_choose": (_ci, [_i64, _i64, _i64], "M N K"),
     "dg_act_checkpoint": (_ci, [_i64, _i64, _vp, _i64, _vp, _i64, _ci, _ci] + _MX + [_vp],
                           "rows cols Z ldz H ldh type activation format Q ldq S lds stream"),
@@ -55,7 +59,7 @@ _SIGNATURES = {
 EXPORTED = sorted(_SIGNATURES)
 __all__ = EXPORTED + ["MxMatrix", "MxError", "MX_FORMATS", "DG_ELEM_F32", "DG_ELEM_F16", "DG_ELEM_BF16", "DG_MXFP4",
                       "DG_MXFP8", "DG_MXINT8", "quantize_mx", "dequantize_mx", "gemm_mx", "gemm_dq", "act_checkpoint",
-                      "act_backward", "mx_kernel_names"]
+                      "act_backward", "mx_kernel_names", "dq_kernel_names"]
 _functions = {}
 for _name, (_res, _args, _) in _SIGNATURES.items():
     _f = getattr(_lib, _name)
@@ -63,12 +67,21 @@ for _name, (_res, _args, _) in _SIGNATURES.items():
     _functions[_name] = globals()[_name] = _f
 
 
-def mx_kernel_names() -> list[str]:
-    """The kernels of dg_gemm_mx, by index."""
+def _kernel_names(name_of) -> list[str]:
     names = []
-    while (n := dg_gemm_mx_kernel_name(len(names))) is not None:  # noqa: F821
+    while (n := name_of(len(names))) is not None:
         names.append(n.decode())
     return names
+
+
+def mx_kernel_names() -> list[str]:
+    """The kernels of dg_gemm_mx, by index."""
+    return _kernel_names(dg_gemm_mx_kernel_name)  # noqa: F821
+
+
+def dq_kernel_names() -> list[str]:
+    """The kernels of dg_gemm_dq, by index."""
+    return _kernel_names(dg_gemm_dq_kernel_name)  # noqa: F821
 
 
 class MxError(GemmError):
@@ -273,7 +286,7 @@ def gemm_mx(A: MxMatrix, B: MxMatrix, C=None, alpha=1.0, beta=0.0, bias=None, ac
 
 
 def gemm_dq(A, B: MxMatrix, C=None, transA=False, alpha=1.0, beta=0.0, out_dtype=None, splits=0, workspace=None,
-            stream=None):
+            stream=None, kernel=DG_KERNEL_AUTO):
     """C = alpha * op(A) @ B + beta * C: A float16 or bfloat16, [M, K] or (with
     transA) [K, M]; B [K, N] in any MX format.  C (allocated when None, with
     `out_dtype` or A's dtype) has A's dtype or float32.  `splits` cuts K into
@@ -301,8 +314,9 @@ def gemm_dq(A, B: MxMatrix, C=None, transA=False, alpha=1.0, beta=0.0, out_dtype
         workspace = _empty(dg_gemm_splitk_workspace_size(M, N, splits), torch.uint8, A.device, stream)
     ws, wsb = _workspace(workspace)
     index, handle = _stream_of(stream, (A, B.q, B.s, C, workspace))
-    _call("dg_gemm_dq", index, bool(transA), M, N, K, alpha, A.data_ptr(), lda, _ELEM[A.dtype], B.code, B.q.data_ptr(),
-          B.ldq, B.s.data_ptr(), B.lds, beta, C.data_ptr(), ldc, _ELEM[C.dtype], splits, ws, wsb, handle)
+    _call("dg_gemm_dq_with_kernel", index, bool(transA), M, N, K, alpha, A.data_ptr(), lda, _ELEM[A.dtype], B.code, B.q.data_ptr(),
+          B.ldq, B.s.data_ptr(), B.lds, beta, C.data_ptr(), ldc, _ELEM[C.dtype], splits, ws, wsb, handle,
+          kernel)
     return C
 
 

@@ -368,7 +368,8 @@ const char *dg_gemm_mx_kernel_name(int kernel);
  *   dg_gemm_dq_choose; the workspace holds splits * M * N fp32 partials, see
  *   dg_gemm_splitk_workspace_size, and is needed only when more than one
  *   range results).
- *   DG_ERR_UNSUPPORTED: an output of 2^22 tiles or more (about 2^34 elements).
+ *   DG_ERR_UNSUPPORTED: 2^22 tiles or more, times K ranges (an output of about
+ *   2^34 elements in one range).
  *   1 transA, 2 M, 3 N, 4 K, 5 alpha, 6 A, 7 lda, 8 typeA, 9 formatB, 10 B,
  *   11 ldb (bytes), 12 SB, 13 ldsb, 14 beta, 15 C, 16 ldc, 17 typeC,
  *   18 splits, 19 workspace (NULL or not 16-byte aligned), 20
@@ -380,6 +381,19 @@ int dg_gemm_dq(dg_op_t transA, int64_t M, int64_t N, int64_t K, float alpha, con
 
 /* The K ranges dg_gemm_dq uses with splits = 0, or -i (1 M, 2 N, 3 K). */
 int dg_gemm_dq_choose(int64_t M, int64_t N, int64_t K);
+
+/* dg_gemm_dq with a forced kernel (argument 22; DG_KERNEL_AUTO: the library's
+ * choice), for tests and measurement; DG_ERR_UNSUPPORTED when it cannot run the
+ * problem (the 256 x 256 tile: an A whose rows are not 4-byte aligned, whose lda
+ * is odd or, with transA, whose M is not a multiple of 8).  The choice for an
+ * aligned A with splits = 0 (or -i: 1 M, 2 N, 3 K), and the kernels' names (NULL
+ * when out of range). */
+int dg_gemm_dq_with_kernel(dg_op_t transA, int64_t M, int64_t N, int64_t K, float alpha, const void *A, int64_t lda,
+                           dg_elem_t typeA, dg_mx_t formatB, const void *B, int64_t ldb, const void *SB,
+                           int64_t ldsb, float beta, void *C, int64_t ldc, dg_elem_t typeC, int splits,
+                           void *workspace, size_t workspace_bytes, void *stream, int kernel);
+int dg_gemm_dq_select(int64_t M, int64_t N, int64_t K);
+const char *dg_gemm_dq_kernel_name(int kernel);
 
 /* H = act(Z) (relu or gelu, as the epilogues of dg_gemm_ex), and Z kept in 8
  * bits (DG_MXFP8 or DG_MXINT8) for dg_act_backward, in one pass.  H may be Z

@@ -714,3 +714,61 @@ def test_relu_mask_is_kept(ty, fmt):
     z[2, 40] = math.nan
     _, m = dg.act_checkpoint(z, "relu", format=fmt, keep_positive=True)
     assert m.s[0, 2, 1] == 255 and not m.q[2, 32:64].any()
+
+
+@pytest.mark.parametrize("transA", [False, True])
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("ty", ["f16", "bf16"])
+@pytest.mark.parametrize("kernel", range(len(dg.dq_kernel_names())))
+def test_dq_product_exact_on_every_tile(kernel, ty, fmt, transA):
+    """Every tile with sums that are exact in fp32 (as in test_dq_product_exact):
+    five and more slabs of 64 k in each K range, whole and ragged ends of M, N and
+    K, A by direct loads and (not on the 256 x 256 tile) through registers, one K
+    range and three."""
+    rng = np.random.default_rng(34)
+    for M, N, K, pads in ((304, 391, 1000, (0, 1)), (512, 256, 960, (2, 3)), (37, 545, 1985, (0,)), (8, 130, 1088, (8, 1))):
+        B, b = stored(rng, K, N, fmt, extra=16, lds=K + 1, spread=1, whole=True)
+        a = rng.integers(-8, 9, (M, K)).astype(np.float64)
+        want = a @ b
+        stored_a = torch.from_numpy(np.ascontiguousarray(a.T) if transA else a).to(T[ty])
+        r, c = stored_a.shape
+        for pad in pads:
+            A = torch.full((r, c + pad), math.nan, dtype=T[ty])
+            A[:, :c] = stored_a
+            A = A.to(DEV)[:, :c]
+            direct = (c + pad) % 2 == 0 and (not transA or M % 8 == 0)
+            for splits in (1, 3):
+                C = torch.full((M + 1, N + 1), math.nan, device=DEV)
+                if kernel == 3 and not direct:
+                    with pytest.raises(dg.MxError, match="support"):
+                        dg.gemm_dq(A, B, C=C[:M, :N], transA=transA, splits=splits, kernel=kernel)
+                    continue
+                dg.gemm_dq(A, B, C=C[:M, :N], transA=transA, splits=splits, kernel=kernel)
+                assert np.array_equal(np64(C[:M, :N]), want), (M, N, K, pad, splits)
+                assert torch.isnan(C[M:]).all() and torch.isnan(C[:, N:]).all()
+
+
+@pytest.mark.parametrize("ty", ["f16", "bf16"])
+@pytest.mark.parametrize("kernel", range(len(dg.dq_kernel_names())))
+def test_dq_product_epilogue_on_every_tile(kernel, ty):
+    """alpha, beta and 16-bit and fp32 outputs with even and odd row strides, in
+    one K range and joined from three: two fp32 operations, then half a step."""
+    rng = np.random.default_rng(35)
+    for M, N, K in ((300, 389, 704), (257, 640, 385)):
+        B, b = stored(rng, K, N, "mxfp4", spread=1, whole=True)
+        a = rng.integers(-4, 5, (M, K)).astype(np.float64)
+        A = torch.from_numpy(a).to(T[ty])
+        A = torch.cat([A, A[:, :K % 2]], 1).to(DEV)[:, :K]
+        s = a @ b
+        for to in (ty, "f32"):
+            for pad in (0, 1):
+                for splits in (1, 3):
+                    c0 = plain(rng, M, N, T[to], pad)
+                    base, full = np64(c0), c0.as_strided((M, N + pad), (N + pad, 1))
+                    dg.gemm_dq(A, B, C=c0, alpha=0.375, beta=-1.5, splits=splits, kernel=kernel)
+                    want = 0.375 * s - 1.5 * base
+                    tol = 2 * 2.0 ** -24 * (np.abs(0.375 * s) + np.abs(1.5 * base))
+                    tol = tol * (1 + HALF[T[to]]) + (HALF[T[to]] if to != "f32" else 0) * np.abs(want) + TINY[T[to]]
+                    assert (np.abs(np64(c0) - want) <= tol).all(), (M, N, to, pad, splits)
+                    if pad:
+                        assert torch.isnan(full[:, N:]).all()

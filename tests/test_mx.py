@@ -261,3 +261,22 @@ def test_keep_positive_goes_with_relu_in_the_checkpoint():
     assert dg.dg_act_checkpoint(*dict(CKPT, activation=dg.DG_EPI_RELU_POSITIVE, Q=NULL).values()) == -10
     with pytest.raises(ValueError, match="relu"):
         dg.act_checkpoint(torch.zeros(4, 40), "gelu", keep_positive=True)
+
+
+def test_dq_kernel_choice():
+    names = dg.dq_kernel_names()
+    assert len(names) == len(set(names)) and dg.dg_gemm_dq_kernel_name(-1) is None
+    pick = lambda *mnk: (names[dg.dg_gemm_dq_select(*mnk)], dg.dg_gemm_dq_choose(*mnk))  # noqa: E731
+    # each tile serves a shape: dW of an adapter, dX of a step and of a batch, large products
+    assert pick(32, 2048, 4096)[0] == "dq_32x128_tile" and pick(32, 2048, 4096)[1] > 1
+    assert pick(512, 2048, 5632) == ("dq_64x128_tile", 4)
+    assert pick(1024, 2048, 8192) == ("dq_128x128_tile", 3)
+    assert pick(4096, 4096, 4096) == ("dq_256x256_tile", 1)
+    assert pick(5632, 2048, 16384) == ("dq_256x256_tile", 1)
+    assert [dg.dg_gemm_dq_select(*a) for a in ((-1, 1, 1), (1, -1, 1), (1, 1, -1))] == [-1, -2, -3]
+    forced = lambda kernel, **kw: dg.dg_gemm_dq_with_kernel(*dict(DQ, **kw).values(), kernel)  # noqa: E731
+    assert forced(len(names)) == forced(-2) == dg.DG_ERR_UNSUPPORTED
+    # the 256 x 256 tile takes A by direct loads: 4-byte aligned rows, whole pieces of a transposed A
+    for kw in (dict(A=0x1002), dict(lda=65), dict(transA=1, lda=64), dict(lda=1 << 22)):
+        assert forced(3, **kw) == dg.DG_ERR_UNSUPPORTED, kw
+    assert forced(3, A=NULL) == -6

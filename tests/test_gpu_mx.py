@@ -772,3 +772,32 @@ def test_dq_product_epilogue_on_every_tile(kernel, ty):
                     assert (np.abs(np64(c0) - want) <= tol).all(), (M, N, to, pad, splits)
                     if pad:
                         assert torch.isnan(full[:, N:]).all()
+
+
+@pytest.mark.parametrize("ty", list(T))
+@pytest.mark.parametrize("fa", ["mxfp4", "mxfp8"])
+@pytest.mark.parametrize("kernel", range(len(dg.mx_kernel_names())))
+def test_product_epilogue_on_every_kernel(kernel, fa, ty):
+    """bias, activation, alpha and beta with even and odd row strides of C on each
+    kernel, on exact sums; the bound is test_product_epilogue's."""
+    rng = np.random.default_rng(25)
+    for M, N, K in ((5, 50, 256), (150, 389, 520), (257, 264, 300)):
+        A, a = stored(rng, M, K, fa, spread=1, whole=True)
+        B, b = stored(rng, N, K, "mxfp4", spread=1, whole=True)
+        s = a @ b.T
+        alpha, beta = 1.0 / 64, -0.5
+        for act in ("none", "relu", "gelu"):
+            for pad in (0, 1, 2):
+                c0 = plain(rng, M, N, T[ty], pad)
+                bias = plain(rng, 1, N, T[ty])[0]
+                base = np64(c0)
+                full = c0.as_strided((M, N + pad), (N + pad, 1))
+                dg.gemm_mx(A, B, C=c0, alpha=alpha, beta=beta, bias=bias, activation=act, kernel=kernel)
+                pre = alpha * s + beta * base + np64(bias)
+                mag = np.abs(alpha * s) + np.abs(beta * base) + np.abs(np64(bias))
+                want = act64(pre, act)
+                tol = 1.13 * 4 * 2.0 ** -24 * mag + (1e-6 * np.abs(pre) if act == "gelu" else 0)
+                tol = tol * (1 + HALF[T[ty]]) + HALF[T[ty]] * np.abs(want) + TINY[T[ty]]
+                assert (np.abs(np64(c0) - want) <= tol).all(), (M, N, act, pad)
+                if pad:
+                    assert torch.isnan(full[:, N:]).all()

@@ -280,3 +280,17 @@ def test_dq_kernel_choice():
     for kw in (dict(A=0x1002), dict(lda=65), dict(transA=1, lda=64), dict(lda=1 << 22)):
         assert forced(3, **kw) == dg.DG_ERR_UNSUPPORTED, kw
     assert forced(3, A=NULL) == -6
+
+
+@pytest.mark.parametrize("rows,cols", [(1, 1), (8, 9), (33, 8), (511, 5631), (512, 5632), (2048, 2048), (32768, 5632),
+                                       (32773, 24), (131072 + 37, 8), (2 ** 31 - 1, 1), (3, 2 ** 20), (40, 2 ** 31 - 1),
+                                       (2 ** 20, 2 ** 21)])
+def test_backward_workspace(rows, cols):
+    """One row of partial sums per slice: a band of rows each (32 rows where that
+    leaves 1024 workgroups of 512 columns, else 16 where that leaves 256, else 8), 4096
+    at most and no more than 2^22 workgroups."""
+    chunks = -(-cols // 512)
+    band = 32 if -(-rows // 32) * chunks >= 1024 else 16 if -(-rows // 16) * chunks >= 256 else 8
+    slices = max(1, min(-(-rows // band), 4096, 2 ** 22 // chunks))
+    assert dg.dg_act_backward_workspace_size(rows, cols) == slices * cols * 4
+    assert slices * chunks <= 2 ** 22

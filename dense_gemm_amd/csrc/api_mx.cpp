@@ -407,7 +407,8 @@ int dg_gemm_mx_select(dg_mx_t formatA, int64_t M, int64_t N, int64_t K)
     if (M < 0 || M > kMaxDim) return -2;
     if (N < 0 || N > kMaxDim) return -3;
     if (K < 0 || K > kMaxDim - dg::MX_GROUP) return -4;
-    return mx_choose(formatA == DG_MXFP4, false, M, N, K, row_bytes(formatA, K), row_bytes(DG_MXFP4, K));
+    const int k = mx_choose(formatA == DG_MXFP4, false, M, N, K, row_bytes(formatA, K), row_bytes(DG_MXFP4, K));
+    return k < 0 ? DG_ERR_UNSUPPORTED : k;
 }
 
 const char *dg_gemm_mx_kernel_name(int kernel) { return kernel >= 0 && kernel < kNumMx ? kMx[kernel].name : nullptr; }

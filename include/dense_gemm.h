@@ -334,8 +334,8 @@ int dg_mx_dequantize(int64_t rows, int64_t cols, dg_mx_t format, const void *Q, 
  * error; an fp32 C does not have it, at up to twice the time.
  *   M == 0 or N == 0: nothing is done; K == 0 or alpha == 0: A and B are not
  *   read, C = act(beta * C + bias); beta == 0: C is not read.
- *   DG_ERR_UNSUPPORTED: more tiles or rows than a launch holds (outputs of
- *   about 2^38 elements).
+ *   DG_ERR_UNSUPPORTED: more tiles than a launch holds (2^22 of 256 x 256, edge
+ *   tiles counted whole: from 2^30 rows of up to 256 columns or 2^19 x 2^19 on).
  *   1 M, 2 N, 3 K, 4 alpha, 5 formatA, 6 A, 7 lda (bytes), 8 SA, 9 ldsa,
  *   10 formatB, 11 B, 12 ldb (bytes), 13 SB, 14 ldsb, 15 beta, 16 C, 17 ldc,
  *   18 type, 19 bias, 20 epilogue, 21 stream. */
@@ -346,9 +346,9 @@ int dg_gemm_mx(int64_t M, int64_t N, int64_t K, float alpha, dg_mx_t formatA, co
 
 /* dg_gemm_mx with a forced kernel (argument 22; DG_KERNEL_AUTO: the
  * library's choice), for tests and measurement; DG_ERR_UNSUPPORTED when it
- * cannot run the problem.  The choice for packed operands and a 16-bit C (or
- * -i: 1 formatA, 2 M, 3 N, 4 K), and the kernels' names (NULL when out of
- * range). */
+ * cannot run the problem.  The choice for packed operands and a 16-bit C
+ * (DG_ERR_UNSUPPORTED when there is none; or -i: 1 formatA, 2 M, 3 N, 4 K), and
+ * the kernels' names (NULL when out of range). */
 int dg_gemm_mx_with_kernel(int64_t M, int64_t N, int64_t K, float alpha, dg_mx_t formatA, const void *A,
                            int64_t lda, const void *SA, int64_t ldsa, dg_mx_t formatB, const void *B, int64_t ldb,
                            const void *SB, int64_t ldsb, float beta, void *C, int64_t ldc, dg_elem_t type,

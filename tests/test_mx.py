@@ -294,3 +294,16 @@ def test_backward_workspace(rows, cols):
     slices = max(1, min(-(-rows // band), 4096, 2 ** 22 // chunks))
     assert dg.dg_act_backward_workspace_size(rows, cols) == slices * cols * 4
     assert slices * chunks <= 2 ** 22
+
+
+def test_select_names_what_no_kernel_runs():
+    """More tiles than a launch holds: the products' own status, not that of an
+    invalid argument."""
+    big = 2 ** 31 - 1
+    for fa in (dg.DG_MXFP4, dg.DG_MXFP8):
+        for M, N, K in ((big, big, 1), (big, 1, 1), (1, big, 1), (2 ** 21, 2 ** 21, 256)):
+            assert dg.dg_gemm_mx_select(fa, M, N, K) == dg.DG_ERR_UNSUPPORTED, (M, N, K)
+            args = dict(MX, M=M, N=N, K=K, formatA=fa, lda=256, ldb=256, ldsa=M, ldsb=N, ldc=N)
+            assert dg.dg_gemm_mx(*args.values()) == dg.DG_ERR_UNSUPPORTED
+        names = dg.mx_kernel_names()
+        assert names[dg.dg_gemm_mx_select(fa, 2 ** 30 - 256, 256, 256)] == "mx_256x256_tile"

@@ -756,6 +756,8 @@ int dg_kernel_tile_n(int kernel)
     return (kernel >= 0 && kernel < kNumKernels) ? kFamilies[kernel].bn : -1;
 }
 
+// (an invalid argument is named for the dense products; the MX calls number
+// their own, see include/dense_gemm.h)
 const char *dg_status_string(int status)
 {
     switch (status) {
@@ -763,21 +765,21 @@ const char *dg_status_string(int status)
     case DG_ERR_UNSUPPORTED: return "kernel does not support this problem";
     case DG_ERR_SCRATCH: return "split-K partials larger than the library's scratch (DG_SCRATCH_BYTES)";
     case DG_ERR_HIP: return "HIP error (see dg_last_hip_error)";
-    case -1: return "invalid argument 1 (transA)";
-    case -2: return "invalid argument 2 (transB)";
-    case -3: return "invalid argument 3 (M)";
-    case -4: return "invalid argument 4 (N)";
-    case -5: return "invalid argument 5 (K)";
-    case -6: return "invalid argument 6 (alpha)";
-    case -7: return "invalid argument 7 (A is NULL)";
-    case -8: return "invalid argument 8 (lda)";
-    case -9: return "invalid argument 9 (B is NULL; dg_gemm_ex: strideA)";
-    case -10: return "invalid argument 10 (ldb; dg_gemm_ex: B is NULL)";
-    case -11: return "invalid argument 11 (beta; dg_gemm_ex: ldb)";
-    case -12: return "invalid argument 12 (C is NULL; dg_gemm_ex: strideB)";
-    case -13: return "invalid argument 13 (ldc; dg_gemm_ex: beta)";
-    case -14: return "invalid argument 14 (dtype; dg_gemm_ex: C is NULL)";
-    case -15: return "invalid argument 15 (stream; dg_gemm_ex: ldc)";
+    case -1: return "invalid argument 1 (dg_gemm: transA)";
+    case -2: return "invalid argument 2 (dg_gemm: transB)";
+    case -3: return "invalid argument 3 (dg_gemm: M)";
+    case -4: return "invalid argument 4 (dg_gemm: N)";
+    case -5: return "invalid argument 5 (dg_gemm: K)";
+    case -6: return "invalid argument 6 (dg_gemm: alpha)";
+    case -7: return "invalid argument 7 (dg_gemm: A is NULL)";
+    case -8: return "invalid argument 8 (dg_gemm: lda)";
+    case -9: return "invalid argument 9 (dg_gemm: B is NULL; dg_gemm_ex: strideA)";
+    case -10: return "invalid argument 10 (dg_gemm: ldb; dg_gemm_ex: B is NULL)";
+    case -11: return "invalid argument 11 (dg_gemm: beta; dg_gemm_ex: ldb)";
+    case -12: return "invalid argument 12 (dg_gemm: C is NULL; dg_gemm_ex: strideB)";
+    case -13: return "invalid argument 13 (dg_gemm: ldc; dg_gemm_ex: beta)";
+    case -14: return "invalid argument 14 (dg_gemm: dtype; dg_gemm_ex: C is NULL)";
+    case -15: return "invalid argument 15 (dg_gemm: stream; dg_gemm_ex: ldc)";
     case -16: return "invalid argument 16 (dg_gemm_splitk: splits; dg_gemm_ex: strideC overlaps batches)";
     case -17: return "invalid argument 17 (dg_gemm_splitk: workspace NULL or not 16-byte aligned; "
                      "dg_gemm_ex: batch)";

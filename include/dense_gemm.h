@@ -436,7 +436,9 @@ const char *dg_kernel_name(int kernel);
 int dg_kernel_tile_m(int kernel);
 int dg_kernel_tile_n(int kernel);
 
-/* Static text for a status code. */
+/* Static text for a status code.  An invalid argument is given by its position
+ * and named for the dense products only; the lists above name those of the MX
+ * calls. */
 const char *dg_status_string(int status);
 
 /* hipError_t of the calling thread's last DG_ERR_HIP (0 if none). */

@@ -307,3 +307,13 @@ def test_select_names_what_no_kernel_runs():
             assert dg.dg_gemm_mx(*args.values()) == dg.DG_ERR_UNSUPPORTED
         names = dg.mx_kernel_names()
         assert names[dg.dg_gemm_mx_select(fa, 2 ** 30 - 256, 256, 256)] == "mx_256x256_tile"
+
+
+def test_status_texts_say_whose_argument_they_name():
+    """A position means another argument in every family of calls: a text that
+    names one says for which call."""
+    for i in range(1, 23):
+        text = dg.dg_status_string(-i)
+        assert text.startswith(f"invalid argument {i}")
+        names = text[len(f"invalid argument {i}"):].strip(" ()")
+        assert not names or all(n.strip().startswith("dg_gemm") for n in names.split(";")), text

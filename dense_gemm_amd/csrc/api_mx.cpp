@@ -72,17 +72,19 @@ bool mx_supports(int k, int64_t M, int64_t N, int64_t lda, int64_t ldb)
 
 // The kernel by its time (us) under a model of each: a fixed part, and a part
 // per slab (128 k, or 256 k of two mxfp4 operands) for as many rounds of tiles
-// as the compute units need (and C's way out at 4 TB/s for the 64 x 64 tile).  Fitted to back-to-back times at 32 shapes (M 1 to
-// 8192, N 1024 to 8192, K 512 to 8192); a 64 x 64 tile's units share about 270
-// tiles a round, a 128 x 128 one's 212 (two fit a unit, at less than twice the
-// speed), and a 256 x 256 one's 256, whose last round costs 0.82 when partly
-// filled.  The row kernels read B once per 16 (or 32) rows of A and their
+// as the compute units need (and C's way out at 4 TB/s for the 64 x 64 tile).
+// Fitted to back-to-back times; over 40 shapes with a bf16 C (M 1 to 8192, N 65 to
+// 8192, K 67 to 8192) the choice is 0.4% slower than the fastest kernel by
+// geometric mean, 14% at the worst (4138 x 901 x 291).  A 64 x 64 tile's units
+// share about 270 tiles a round, a 128 x 128 one's 212 (two fit a unit, at less
+// than twice the speed), and a 256 x 256 one's 256, whose last round costs 0.82
+// when partly filled.  The row kernels read B once per 16 (or 32) rows of A and their
 // own rows of A for every 16 columns.  Measured on both sides of the choice
-// (M x N x K, mxfp8 times mxfp4): 16 x 8192 x 8192 rows 15.3, tile 17.8 us;
-// 32 x 8192 x 8192 rows 22.9, tile 17.9; 64 x 2048 x 2048 rows 4.8, tile 6.8;
-// 512 x 5632 x 2048 64-tile 12.4, 128-tile 12.2; 1024 x 8192 x 8192 128-tile
-// 60.6, 256-tile 80.3; mxfp4 both, 2048 x 8192 x 4096 128-tile 46.8, 256-tile
-// 40.6.  `exact` (mxfp8 with an fp32 C) takes two matrix instructions for one on the
+// (M x N x K, mxfp8 times mxfp4): 16 x 8192 x 8192 rows 15.1, tile 17.9 us;
+// 32 x 8192 x 8192 rows 22.2, tile 18.0; 64 x 2048 x 2048 rows 5.1, tile 6.9;
+// 512 x 5632 x 2048 64-tile 13.0, 128-tile 13.4; 1024 x 8192 x 8192 128-tile
+// 58.9, 256-tile 80.1; mxfp4 both, 2048 x 8192 x 4096 128-tile 42.9, 256-tile
+// 37.7.  `exact` (mxfp8 with an fp32 C) takes two matrix instructions for one on the
 // tiled kernels: 32 x 8192 x 8192 rows 23, 64-tile 31; 512 x 5632 x 2048 64-tile
 // 17.4, 128-tile 19.7; 1024 x 8192 x 8192 128-tile 102, 64-tile 139; 4096^3 256-tile
 // 100, 128-tile 106.
@@ -130,12 +132,14 @@ int64_t dq_chunk(int64_t K, int splits) { return ceil_div(ceil_div(K, splits), 6
 // times of 21 shapes: a fixed part; a part per slab for as many rounds as the
 // workgroups need, a round longer once a compute unit's workgroups fill its
 // LDS bandwidth (`share` of a slab each); and for more than one range the
-// second launch and the partials' way to memory and back at 6 TB/s, or at 4
-// once they outgrow the caches.
-// `splits` > 0 fixes the ranges.  Measured on both sides (M x N x K, us):
-// 512 x 2048 x 5632 in 4 ranges 25.9, in one 54.1; 2048 x 1024 x 1024 in one
-// range 11.9, in two 23.6; 1024 x 2048 x 8192 128-tile in 4 ranges 51.6, 64-tile
-// in one 91; 4096^3 256-tile 109, 128-tile 134.
+// second launch and the partials' way to memory and back at a large copy's 5
+// TB/s.  `splits` > 0 fixes the ranges.  Over 32 shapes (M 8 to 8192, N 700 to
+// 6144, K 1024 to 16384) the choice is 3.4% slower than the fastest tile and
+// ranges by geometric mean, 25% at the worst (64 x 5632 x 2048).  Measured on both
+// sides (M x N x K, us): 512 x 2048 x 5632 in 4 ranges 26.5, in one 54.1; 1024^3 in one range
+// 11.8, in two 16; 4096 x 2048 x 16384 256-tile in two ranges 241, in one 345,
+// 128-tile in one 291; 5632 x 2048 x 16384 256-tile in one range 354, in two 416;
+// 4096^3 256-tile 108, 128-tile 130.
 void dq_choose(int64_t M, int64_t N, int64_t K, bool direct, int splits, int *tile, int *ranges)
 {
     double best = 1e300;
@@ -156,7 +160,7 @@ void dq_choose(int64_t M, int64_t N, int64_t K, bool direct, int splits, int *ti
             const double rounds = full * round(kDq[k].resident) + (rest > 0 ? (k == 3 && full > 0 ? 0.82 : round(rest)) : 0.);
             // (with every unit at work on the largest tile the clock drops)
             double t = kDq[k].fixed + (double)(chunk / 64) * kDq[k].slab * (direct ? 1. : 1.2) * rounds * (k == 3 && w > 0.9 ? 1.15 : 1.);
-            if (s > 1) t += 3.0 + (double)s * (0.4 + out * 8 / ((double)s * out * 4 < 64e6 ? 6e6 : 4e6));
+            if (s > 1) t += 3.0 + (double)s * (0.4 + out * 8 / 5e6);
             if (t < best) {
                 best = t;
                 *tile = k;

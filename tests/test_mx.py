@@ -317,3 +317,13 @@ def test_status_texts_say_whose_argument_they_name():
         assert text.startswith(f"invalid argument {i}")
         names = text[len(f"invalid argument {i}"):].strip(" ()")
         assert not names or all(n.strip().startswith("dg_gemm") for n in names.split(";")), text
+
+
+def test_dq_ranges_of_large_partials():
+    """Partials of 46 MB and more a range: two ranges where they fill the last
+    round of tiles, one where they would add a round."""
+    names = dg.dq_kernel_names()
+    for shape, tile, ranges in (((4096, 2048, 16384), "dq_256x256_tile", 2), ((5632, 4096, 16384), "dq_256x256_tile", 2),
+                                ((3584, 2048, 16384), "dq_256x256_tile", 2), ((5632, 2048, 16384), "dq_256x256_tile", 1),
+                                ((4608, 3584, 16384), "dq_256x256_tile", 1), ((256, 1024, 1024), "dq_32x128_tile", 1)):
+        assert (names[dg.dg_gemm_dq_select(*shape)], dg.dg_gemm_dq_choose(*shape)) == (tile, ranges), shape

@@ -157,9 +157,11 @@ void dq_choose(int64_t M, int64_t N, int64_t K, bool direct, int splits, int *ti
             const double w = tiles * (double)s / 256, full = (double)(int64_t)(w / kDq[k].resident);
             auto round = [&](double wgs) { return kDq[k].share * wgs > 1 ? kDq[k].share * wgs : 1.; };
             const double rest = w - full * kDq[k].resident;
-            const double rounds = full * round(kDq[k].resident) + (rest > 0 ? (k == 3 && full > 0 ? 0.82 : round(rest)) : 0.);
+            const double last = rest > 0 ? (k == 3 && full > 0 ? 0.82 : round(rest)) : 0.;
+            const double rounds = full * round(kDq[k].resident) + last;
             // (with every unit at work on the largest tile the clock drops)
-            double t = kDq[k].fixed + (double)(chunk / 64) * kDq[k].slab * (direct ? 1. : 1.2) * rounds * (k == 3 && w > 0.9 ? 1.15 : 1.);
+            const double slab = kDq[k].slab * (direct ? 1. : 1.2) * (k == 3 && w > 0.9 ? 1.15 : 1.);
+            double t = kDq[k].fixed + (double)(chunk / 64) * slab * rounds;
             if (s > 1) t += 3.0 + (double)s * (0.4 + out * 8 / 5e6);
             if (t < best) {
                 best = t;
@@ -376,7 +378,6 @@ int dg_gemm_mx_with_kernel(int64_t M, int64_t N, int64_t K, float alpha, dg_mx_t
     p.g.K = (int32_t)(dg::mx_groups(K) * dg::MX_GROUP);   // rows hold whole groups, zeros past K
     p.g.alpha = alpha;
     p.g.beta = beta;
-    p.g.c_vec = c_rows4(C, ldc, type);
     p.g.splits = 1;
     p.g.bias = bias;
     p.g.act = epilogue;

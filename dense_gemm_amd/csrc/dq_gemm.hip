@@ -17,16 +17,21 @@
 // B's 16-bit buffer is [64 k][BN], rows of BN * 2 bytes: the 64-byte quad q
 // (32 n) of row k sits at quad q ^ swz(k), and its 16-byte chunk c at chunk
 // c ^ (k & 3).  The fragment reads (ds_read_b64_tr_b16, four rows of a quad per
-// 16 lanes) see four distinct quads, and the 16 lanes of a write, which hold
-// the same chunk numbers of two or four rows, distinct chunks.
+// 16 lanes) see four distinct quads and have no bank conflicts.  The 16-byte
+// writes have: they are served 8 lanes at a time over 128 bytes of banks, and
+// those lanes' quads meet on each 16 bytes twice (8 conflict cycles a write; four
+// times and 24 for mxfp4 on the 256-wide tile, whose 8 lanes hold one chunk number of
+// 8 quads).  The counters agree to the cycle: 4096^3 on the 256 x 256 tile, 131072
+// slabs of a wave with 4 writes each, 1.26e7 cycles with mxfp4 and 4.2e6 with mxfp8,
+// and 5.2e5 of the epilogue's, of 3.1e7 and 2.2e7 that the LDS is at work.
 //
-// Measured: 4096^3 (mxfp4) 109 us, 1.26 PFLOP/s, the rate of a large bf16
+// Measured: 4096^3 (mxfp4) 108 us, 1.26 PFLOP/s, the rate of a large bf16
 // product of the library that ships with torch (1.24); 5632 x 2048 x 16384 (tn,
-// mxint8) 360 us, 1.05 PFLOP/s on the 176 compute units that have a tile, mxfp8
+// mxint8) 354-362 us, 1.05 PFLOP/s on the 176 compute units that have a tile, mxfp8
 // 335.  The matrix cores are busy at the clock they hold under load there.
 // Smaller outputs are bound by LDS bytes: a 128 x 128 tile moves 106 KB a slab
 // for a quarter of the work of the 256 x 256 tile's 256 KB, and converted
-// elements go in at about 48 bytes a clock.  Tried and left: B's codes through
+// elements go in at about 48 bytes a clock (conflicts and all).  Tried and left: B's codes through
 // an LDS ring, more slabs deep (no faster at 512 x 2048 x 5632, slower at
 // 2048^3); the 128 x 128 tile in two K groups of four waves (62 us against 68 in
 // one range there, 185 against 134 at 4096^3); a 192 x 256 tile (335 us at the tn
@@ -39,7 +44,7 @@ namespace {
 
 constexpr int DQ_BK = 64;
 
-// Two 16-bit values of T from the low or high half of codes q.
+// Values of T from codes and their block's scale.
 template <typename T, int FB>
 struct Decode {
     typedef T V8 __attribute__((ext_vector_type(8)));

@@ -19,8 +19,6 @@ namespace dg {
 
 namespace {
 
-
-
 // Eight elements of a row as one 16-byte access (two for fp32).  Rows need
 // only be aligned to their element: the GPU takes misaligned vector accesses
 // to global memory, so odd row strides go the same way as aligned ones.
@@ -34,7 +32,7 @@ template <typename T>
 __device__ __forceinline__ void load8(const T *row, int64_t col, int64_t n, float (&v)[8])
 {
     if (col + 8 <= n) {
-                const typename Eight<T>::V8 a = *(const typename Eight<T>::V8u *)(row + col);
+        const typename Eight<T>::V8 a = *(const typename Eight<T>::V8u *)(row + col);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = (float)a[i];
     } else {

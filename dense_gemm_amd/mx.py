@@ -104,7 +104,9 @@ class MxMatrix:
     """rows x cols values in an MX format: `q` (uint8 [rows, bytes], rows of
     whole 256-column groups) and `s` (uint8 [groups, rows, 8], the scale bytes
     of each row's group).  Both may be views: unit stride along the bytes, and
-    the rows of a group of `s` 8 bytes apart."""
+    the rows of a group of `s` 8 bytes apart.  Elements of the last group past
+    `cols` must be zero (every function here writes them so): a matrix of a
+    stored one's first columns ends at a multiple of 256."""
 
     __slots__ = ("format", "rows", "cols", "q", "s", "code", "ldq", "lds")
 

@@ -280,12 +280,17 @@ int dg_select_kernel(dg_op_t transA, dg_op_t transB, int64_t M, int64_t N, int64
  *   Q  elements, row r at byte r * ldq; mxfp4 two elements to a byte, the
  *      even one in the low 4 bits.  A row holds whole groups of 256 elements
  *      (128 bytes of mxfp4, 256 of the others; dg_mx_row_bytes); elements at
- *      or past cols are zero (the products rely on it).  Q is 16-byte
- *      aligned, ldq a multiple of 16.
+ *      or past cols are zero (dg_gemm_mx relies on it: a matrix of fewer
+ *      columns than were stored is one only if it ends at a multiple of 256).
+ *      Q is 16-byte aligned, ldq a multiple of 16.
  *   S  scales, one byte e + 127 each (255: NaN); the scale of block b of row
  *      r is byte ((b / 8) * lds + r) * 8 + b % 8, so the 8 scales of a row's
  *      group lie together and a group's rows one after the other.  S is
  *      8-byte aligned, lds >= rows (dg_mx_scale_bytes).
+ * A row takes the bytes of its whole groups: 136 (mxfp4) or 264 (8 bits) with
+ * the scales, per 256 columns begun.  Short rows save little or nothing: 32
+ * columns take 64 bytes in 16 bits, and 8-bit storage is the smaller from 133
+ * columns on (mxfp4 from 69).
  * Rows r0 .. of a matrix are the matrix at Q + r0 * ldq and S + r0 * 8 with
  * the same ldq and lds; columns from a multiple of 256 on, at Q + (128 or
  * 256) * g and S + g * lds * 8.  Nothing outside a matrix's own rows and
@@ -294,8 +299,8 @@ int dg_select_kernel(dg_op_t transA, dg_op_t transB, int64_t M, int64_t N, int64
  *
  * Pointers, streams, asynchrony and errors as dg_gemm: -i names an invalid
  * argument by its position (types and formats are checked before the pointers
- * whose alignment depends on them), and nothing is enqueued then.  Plain matrices are aligned to their element.  Sizes are at
- * most 2^31 - 1.  No call allocates memory, and no call keeps state: calls on
+ * whose alignment depends on them), and nothing is enqueued then.  Plain
+ * matrices are aligned to their element.  Sizes are at most 2^31 - 1.  No call allocates memory, and no call keeps state: calls on
  * different streams do not interfere unless they share a workspace or an
  * output. */
 
@@ -412,7 +417,9 @@ int dg_act_checkpoint(int64_t rows, int64_t cols, const void *Z, int64_t ldz, vo
 
 /* dZ = dH * act'(z) with z the values of (Q, S) (kept by dg_act_checkpoint or
  * dg_mx_quantize).  relu: dH where z > 0, else 0 (an infinite or NaN dH too);
- * gelu: dH times Phi(z) + z phi(z).  Where z is NaN, dZ is.
+ * gelu: dH times Phi(z) + z phi(z), off by at most 2e-6 of |dH| (the error
+ * function as in the forward, 1.5e-7; in every element type).  Where z is NaN, dZ
+ * is.
  * dZ may be dH itself (with ldz = ldh).  dbias (fp32, cols elements; NULL for
  * none) receives the column sums of dZ before its rounding, in a fixed order
  * of summation; it needs a workspace of dg_act_backward_workspace_size bytes

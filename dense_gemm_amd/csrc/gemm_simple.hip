@@ -126,14 +126,18 @@ __global__ __launch_bounds__(256) void scale_c_kernel(GemmParams p)
 // act(alpha * sum_s ws[s] + beta * C + bias), the splits summed in increasing
 // s (reduce_group4).  A thread takes 4 consecutive columns of one row; a row
 // has 2^tpr_log2 threads (enough to cover N / 4 groups, at most 256), a
-// workgroup 256 >> tpr_log2 rows, so the row and column come from shifts.
-template <typename T>
+// workgroup 256 >> tpr_log2 rows, so the row and column come from shifts.  MANY,
+// for more than 2^23 workgroups (a launch holds fewer than 2^32 threads): 2^23,
+// which walk on over the rows (a loop costs 0.4 us at 512 x 2048, 4 splits).
+template <typename T, bool MANY>
 __global__ __launch_bounds__(256) void splitk_reduce_kernel(GemmParams p, int tpr_log2)
 {
-    const int tpr = 1 << tpr_log2;
-    const int64_t row = (int64_t)blockIdx.x * (256 >> tpr_log2) + (threadIdx.x >> tpr_log2);
-    if (row >= p.M) return;
-    for (int c0 = (threadIdx.x & (tpr - 1)) * 4; c0 < p.N; c0 += tpr * 4) reduce_group4<T>(p, row, c0);
+    const int tpr = 1 << tpr_log2, rows = 256 >> tpr_log2;
+    for (int64_t row = (int64_t)blockIdx.x * rows + (threadIdx.x >> tpr_log2); row < p.M;
+         row += (int64_t)gridDim.x * rows) {
+        for (int c0 = (threadIdx.x & (tpr - 1)) * 4; c0 < p.N; c0 += tpr * 4) reduce_group4<T>(p, row, c0);
+        if (!MANY) break;
+    }
 }
 
 template <typename T>
@@ -143,12 +147,13 @@ hipError_t launch_splitk_reduce(const GemmParams &p, hipStream_t s)
     int tpr_log2 = 0;
     while (tpr_log2 < 8 && ((int64_t)1 << tpr_log2) < groups) ++tpr_log2;
     const int64_t rows_per_block = 256 >> tpr_log2;
-    const int64_t blocks = ((int64_t)p.M + rows_per_block - 1) / rows_per_block;
+    const int64_t blocks = ((int64_t)p.M + rows_per_block - 1) / rows_per_block, most = 1 << 23;
+    const bool many = blocks > most;
     GemmParams arg = p;
     int tl = tpr_log2;
     void *args[] = {&arg, &tl};
-    return hipLaunchKernel((const void *)&splitk_reduce_kernel<T>, dim3((unsigned)blocks), dim3(256),
-                           args, 0, s);
+    return hipLaunchKernel(many ? (const void *)&splitk_reduce_kernel<T, true> : (const void *)&splitk_reduce_kernel<T, false>,
+                           dim3((unsigned)(many ? most : blocks)), dim3(256), args, 0, s);
 }
 
 template <typename T, bool TA, bool TB, typename TC = T>

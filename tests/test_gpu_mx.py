@@ -801,3 +801,25 @@ def test_product_epilogue_on_every_kernel(kernel, fa, ty):
                 assert (np.abs(np64(c0) - want) <= tol).all(), (M, N, act, pad)
                 if pad:
                     assert torch.isnan(full[:, N:]).all()
+
+
+def test_ranges_joined_over_many_rows():
+    """The join of two K ranges over more rows than its launch holds workgroups of
+    256 threads (2^24 of one row each): equal to the product in one range, whose
+    sums are exact too."""
+    M, N, K = (1 << 24) + 3, 516, 128
+    if torch.cuda.mem_get_info()[0] < 150 << 30:
+        pytest.skip("needs 150 GiB of free GPU memory")
+    rng = np.random.default_rng(36)
+    B, b = stored(rng, K, N, "mxfp4", spread=1, whole=True)
+    g = torch.Generator(device=DEV).manual_seed(36)
+    A = torch.randint(-4, 5, (M, K), generator=g, device=DEV, dtype=torch.int8).to(torch.float16)
+    one = dg.gemm_dq(A, B, splits=1)
+    two = dg.gemm_dq(A, B, C=torch.full_like(one, math.nan), splits=2)
+    for i in range(0, M, 1 << 22):
+        assert torch.equal(one[i:i + (1 << 22)], two[i:i + (1 << 22)]), i
+    for r in (0, (1 << 23) - 1, 1 << 23, (1 << 24) - 1, M - 1):
+        want = torch.from_numpy(np64(A[r:r + 1]) @ b).to(torch.float16)
+        assert torch.equal(two[r:r + 1].cpu(), want), r
+    del A, one, two
+    torch.cuda.empty_cache()

@@ -823,3 +823,55 @@ def test_ranges_joined_over_many_rows():
         assert torch.equal(two[r:r + 1].cpu(), want), r
     del A, one, two
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("ty", ["f16", "bf16"])
+def test_dq_operand_values_under_every_scale(ty, fmt):
+    """One k and one block per scale byte, 2^-127 to 2^127: the product by 1 is B's
+    value rounded once to A's type (subnormals included, infinite past its range)."""
+    rng = np.random.default_rng(37)
+    n = 255 * 32
+    for kernel in range(len(dg.dq_kernel_names())):
+        q, s = mx_ref.random_stored(rng, 1, n, fmt)
+        s.reshape(-1)[:255] = np.arange(255)
+        B = dg.MxMatrix(fmt, 1, n, torch.from_numpy(q).to(DEV), torch.from_numpy(s).to(DEV))
+        A = torch.ones(8, 1, dtype=T[ty], device=DEV)
+        A = torch.cat([A, A], 1)[:, :1]
+        got = dg.gemm_dq(A, B, out_dtype=torch.float32, kernel=kernel)
+        want = torch.from_numpy(mx_ref.values(q, s, fmt, n)).to(T[ty]).float()
+        assert torch.equal(got.cpu(), want.expand(8, n)), kernel
+
+
+def test_captured_exact_product_and_mask():
+    """An fp32 C of an mxfp8 A (rows and tiles), relu with keep_positive and its
+    backward, captured once and replayed on other inputs with eager work between."""
+    rng = np.random.default_rng(55)
+    w, _ = stored(rng, 200, 512, "mxfp4")
+
+    def chain(x, d):
+        a = dg.quantize_mx(x, format="mxfp8")
+        z = dg.gemm_mx(a, w, out_dtype=torch.float32)
+        one = dg.gemm_mx(dg.quantize_mx(x[:1], format="mxfp8"), w)
+        h, kept = dg.act_checkpoint(z, "relu", keep_positive=True)
+        db = torch.empty(200, device=DEV)
+        dz = dg.act_backward(d, kept, "relu", dbias=db)
+        return [z, one, h, dz, db, dg.gemm_dq(dz.to(torch.bfloat16), w, splits=2)]
+
+    sets = [(plain(rng, 150, 512, torch.bfloat16), plain(rng, 150, 200, torch.float32)) for _ in range(3)]
+    x, d = (t.clone() for t in sets[0])
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        chain(x, d)
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = chain(x, d)
+    for k in (1, 2, 0, 1):
+        want = [t.clone() for t in chain(*sets[k])]
+        assert torch.equal(want[3], torch.where(want[0] > 0, sets[k][1], 0.0))
+        x.copy_(sets[k][0]), d.copy_(sets[k][1])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want)), k

@@ -875,3 +875,38 @@ def test_captured_exact_product_and_mask():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(outs, want)), k
+
+
+@pytest.mark.parametrize("ty", list(T))
+@pytest.mark.parametrize("kernel", range(len(dg.mx_kernel_names())))
+def test_product_bound_with_outlier_blocks(kernel, ty):
+    """Full-range mxfp8 elements under block scales 2^-6 to 2^6, every other row
+    with neighbours that cancel.  Each product of 8 neighbouring k is cut by less
+    than 2^-13 of the largest among them (tiled kernels with a 16-bit C; else not at
+    all); then at most one fp32 rounding per k, of a partial sum no larger than the
+    sum of magnitudes; then half a step of C."""
+    rng = np.random.default_rng(26)
+    codes = np.flatnonzero(np.isfinite(mx_ref.FP8))
+    for M, N, K in ((7, 33, 512), (131, 140, 520)):
+        G = mx_ref.groups(K)
+        ca = codes[rng.integers(0, len(codes), (M, G * 256))]
+        ca[::2, 1::2] = ca[::2, ::2] ^ 0x80
+        cb = rng.integers(0, 16, (N, G * 256))
+        cb[:, 1::2] = cb[:, ::2]
+        ca[:, K:], cb[:, K:] = 0, 0
+        qa, qb = mx_ref.pack(ca, "mxfp8"), mx_ref.pack(cb, "mxfp4")
+        sa, sb = (rng.integers(121, 134, (G, n, 8)).astype(np.uint8) for n in (M, N))
+        a, b = mx_ref.values(qa, sa, "mxfp8", K), mx_ref.values(qb, sb, "mxfp4", K)
+        A = dg.MxMatrix("mxfp8", M, K, torch.from_numpy(qa).to(DEV), torch.from_numpy(sa).to(DEV))
+        B = dg.MxMatrix("mxfp4", N, K, torch.from_numpy(qb).to(DEV), torch.from_numpy(sb).to(DEV))
+        got = np64(dg.gemm_mx(A, B, out_dtype=T[ty], kernel=kernel))
+        want, mag = a @ b.T, np.abs(a) @ np.abs(b).T
+        assert not want[::2].any() and want[1::2].any()
+        tol = K * 2.0 ** -24 * mag
+        if ty != "f32" and dg.mx_kernel_names()[kernel].endswith("_tile"):
+            for k in range(0, K, 8):
+                tol += 8 * 2.0 ** -13 * (np.abs(a[:, None, k:k + 8]) * np.abs(b[None, :, k:k + 8])).max(2)
+        big = torch.finfo(T[ty]).max
+        fits = np.abs(want) + tol < big
+        tol = tol * (1 + HALF[T[ty]]) + HALF[T[ty]] * np.abs(want) + TINY[T[ty]]
+        assert fits.mean() > 0.4 and (np.abs(got - want) <= tol)[fits].all(), (M, N, K)

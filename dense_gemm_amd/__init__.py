@@ -4,7 +4,9 @@ The functions named like the C ABI (include/dense_gemm.h) only marshal
 arguments: every step of the computation runs in the library's HIP kernels.
 `gemm()` is a convenience over torch tensors (torch is used for device memory
 and streams only); so are `quantize_mx`, `gemm_mx`, `gemm_dq`,
-`act_checkpoint` and their companions for block-scaled matrices (mx.py).
+`act_checkpoint` and their companions for block-scaled matrices (mx.py), and
+`gemm_fused`, `gemm_grouped`, `gemm_act_grad`, `gemm_grouped_act_grad` and
+`gemm_dw` for a layer's products (layer.py).
 
 The library must have been built (python dense_gemm_amd/build.py); importing
 this package fails loudly when it is missing.
@@ -269,3 +271,8 @@ def gemm(A, B, C=None, transA=False, transB=False, alpha=1.0, beta=0.0, bias=Non
 from . import mx as _mx  # noqa: E402
 from .mx import *  # noqa: E402,F401,F403
 EXPORTED += _mx.EXPORTED
+
+# ---- a layer's products, dense and grouped ----------------------------------------
+from . import layer as _layer  # noqa: E402
+from .layer import *  # noqa: E402,F401,F403
+EXPORTED += _layer.EXPORTED

@@ -1,0 +1,359 @@
+// Host side of a layer's products: argument checks, kernel choice and launches on
+// the caller's stream.  The C ABI is declared in include/dense_gemm.h.
+#include "../../include/dense_gemm.h"
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "layer_common.hpp"
+
+namespace dg {
+int launch_status(hipError_t err);
+const void *layer_kernel_f32(int config, int variant);
+const void *layer_kernel_f16(int config, int variant);
+const void *layer_kernel_bf16(int config, int variant);
+hipError_t launch_layer_join(const LayerParams &p, hipStream_t s);
+hipError_t launch_layer_colsum(const LayerParams &p, int type, hipStream_t s);
+}  // namespace dg
+
+namespace {
+
+using dg::LayerParams;
+
+// Row and column counts leave room for a tile past the end.
+constexpr int64_t kMaxDim = 0x7fffffff, kMaxTiled = kMaxDim - 1024;
+constexpr int kMaxGroups = 65535;      // a grid dimension
+
+bool is_dtype(int d) { return d >= DG_F32 && d <= DG_BF16_F32OUT; }
+// Operand and output elements: 0 fp32, 1 fp16, 2 bf16.
+int operand_type(int d) { return d == DG_F32 ? 0 : d == DG_F16_F32ACC || d == DG_F16_F32OUT ? 1 : 2; }
+int output_type(int d) { return d == DG_F16_F32ACC ? 1 : d == DG_BF16_F32ACC ? 2 : 0; }
+int64_t bytes_of(int type) { return type == 0 ? 4 : 2; }
+bool bad_ptr(const void *p, int64_t align) { return p == nullptr || (uintptr_t)p % (uintptr_t)align != 0; }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t max1(int64_t x) { return x > 1 ? x : 1; }
+
+struct LayerFamily {
+    const char *name;
+    int bm, bn, group_m, threads;
+};
+const LayerFamily kLayer[] = {
+    {"layer_64x64_staged", 64, 64, 4, 256},
+    {"layer_128x128_staged", 128, 128, 4, 256},
+};
+constexpr int kNumLayer = sizeof(kLayer) / sizeof(kLayer[0]);
+
+// What the choice of a kernel looks at.
+struct LayerShape {
+    int kind, type;
+    bool tb, ragged;
+    int64_t groups, M, N, K;      // as LayerParams
+};
+
+// The most tiles a launch can have: each group that has rows ends in a partial tile.
+int64_t most_tiles(const LayerShape &s, const LayerFamily &f)
+{
+    const int64_t tn = ceil_div(s.N, f.bn);
+    if (s.kind == dg::LAYER_WEIGHTS) return s.groups * ceil_div(s.M, f.bm) * tn;
+    const int64_t used = s.ragged && s.groups < s.M ? s.groups : s.ragged ? s.M : 1;
+    return (s.M + used * (f.bm - 1)) / f.bm * tn;
+}
+
+bool supports(int k, const LayerShape &s)
+{
+    const LayerFamily &f = kLayer[k];
+    if (s.M > kMaxTiled || s.N > kMaxTiled || s.K > kMaxTiled) return false;
+    // a launch holds fewer than 2^32 threads
+    return most_tiles(s, f) * f.threads < ((int64_t)1 << 32) && most_tiles(s, f) < kMaxDim;
+}
+
+int choose(const LayerShape &s)
+{
+    const int k = most_tiles(s, kLayer[1]) >= 256 ? 1 : 0;
+    return supports(k, s) ? k : supports(1, s) ? 1 : -1;
+}
+
+int resolve_splits(const LayerShape &s, int splits)
+{
+    if (s.kind != dg::LAYER_WEIGHTS && s.ragged) return 1;
+    return splits < 1 ? 1 : splits;
+}
+
+size_t workspace_bytes_of(int64_t groups, int64_t M, int64_t N, int splits)
+{
+    if (groups <= 0 || M <= 0 || N <= 0 || splits <= 1) return 0;
+    return (size_t)splits * (size_t)groups * (size_t)M * (size_t)N * 4;
+}
+
+int launch(LayerParams &p, const LayerShape &s, int dtype, int kernel, int splits, void *ws, size_t ws_bytes, int ws_arg,
+           hipStream_t stream)
+{
+    if (kernel == DG_KERNEL_AUTO) kernel = choose(s);
+    if (kernel < 0 || kernel >= kNumLayer || !supports(kernel, s)) return DG_ERR_UNSUPPORTED;
+    const LayerFamily &f = kLayer[kernel];
+    p.splits = resolve_splits(s, splits);
+    p.ws = (float *)ws;
+    if (p.splits > 1) {
+        if (bad_ptr(ws, 16)) return -ws_arg;
+        if (ws_bytes < workspace_bytes_of(p.groups, p.M, p.N, p.splits)) return -(ws_arg + 1);
+    }
+    p.tiles_m = (int32_t)ceil_div(p.M, f.bm);
+    p.tiles_n = (int32_t)ceil_div(p.N, f.bn);
+    p.group_m = f.group_m;
+    const int type = operand_type(dtype), variant = s.kind == dg::LAYER_WEIGHTS ? 2 : s.tb;
+    const void *k = type == 0 ? dg::layer_kernel_f32(kernel, variant)
+                              : type == 1 ? dg::layer_kernel_f16(kernel, variant) : dg::layer_kernel_bf16(kernel, variant);
+    LayerParams arg = p;
+    void *args[] = {&arg};
+    hipError_t err = hipLaunchKernel(k, dim3((unsigned)most_tiles(s, f), (unsigned)p.splits), dim3((unsigned)f.threads), args,
+                                     0, stream);
+    if (err == hipSuccess && p.splits > 1) err = dg::launch_layer_join(p, stream);
+    return dg::launch_status(err);
+}
+
+// The products over rows.  The arguments up to strideB (12) and from C (21) on stand
+// at the same places in dg_gemm_fused and dg_gemm_act_grad; `p` brings those
+// between them, checked by the caller from `between` on.
+struct RowsCall {
+    int transB;
+    int64_t groups;
+    const int32_t *offsets;
+    int64_t M, N, K;
+    float alpha;
+    const void *A;
+    int64_t lda;
+    const void *B;
+    int64_t ldb, strideB;
+    void *C;
+    int64_t ldc;
+    int dtype, splits;
+    void *workspace;
+    size_t workspace_bytes;
+    void *stream;
+    int kernel;
+    bool work() const { return M > 0 && N > 0 && groups > 0; }
+};
+
+// A matrix of rows that may be left out: -pos for its pointer, -(pos + 1) for its stride.
+int check_rows(const void *x, int64_t ld, int64_t N, int64_t bytes, int pos)
+{
+    if (x == nullptr) return 0;
+    return bad_ptr(x, bytes) ? -pos : ld < max1(N) ? -(pos + 1) : 0;
+}
+
+template <typename F>
+int rows_product(const RowsCall &c, LayerParams &p, F between)
+{
+    if (c.transB != DG_OP_N && c.transB != DG_OP_T) return -1;
+    if (c.groups < 0 || c.groups > kMaxGroups || (c.offsets == nullptr && c.groups != 1)) return -2;
+    if (c.offsets != nullptr && bad_ptr(c.offsets, 4)) return -3;
+    if (c.M < 0 || c.M > kMaxDim) return -4;
+    if (c.N < 0 || c.N > kMaxDim) return -5;
+    if (c.K < 0 || c.K > kMaxDim) return -6;
+    if (!is_dtype(c.dtype)) return -23;
+    const int64_t eb = bytes_of(operand_type(c.dtype)), cb = bytes_of(output_type(c.dtype));
+    const bool reads = c.work() && c.K > 0 && c.alpha != 0.f;
+    if (reads && bad_ptr(c.A, eb)) return -8;
+    if (c.lda < max1(c.K)) return -9;
+    if (reads && bad_ptr(c.B, eb)) return -10;
+    if (c.ldb < max1(c.transB == DG_OP_T ? c.K : c.N)) return -11;
+    if (c.strideB < 0) return -12;
+    const int rc = between(cb);
+    if (rc != 0) return rc;
+    if (c.work() && bad_ptr(c.C, cb)) return -21;
+    if (c.ldc < max1(c.N)) return -22;
+    if (c.splits < 0 || c.splits > 4096) return -24;
+    if (!c.work()) return DG_OK;
+    p.A = c.A;
+    p.B = c.B;
+    p.lda = c.lda;
+    p.ldb = c.ldb;
+    p.strideB = c.strideB;
+    p.M = (int32_t)c.M;
+    p.N = (int32_t)c.N;
+    p.K = reads ? (int32_t)c.K : 0;
+    p.alpha = c.alpha;
+    p.offsets = c.offsets;
+    p.groups = (int32_t)c.groups;
+    if (p.beta == 0.f) p.R = nullptr;
+    p.C = c.C;
+    p.ldc = c.ldc;
+    p.ctype = output_type(c.dtype);
+    const LayerShape s = {p.kind, operand_type(c.dtype), c.transB == DG_OP_T, c.offsets != nullptr, c.groups, c.M, c.N, p.K};
+    return launch(p, s, c.dtype, c.kernel, c.splits, c.workspace, c.workspace_bytes, 25, (hipStream_t)c.stream);
+}
+
+}  // namespace
+
+extern "C" {
+
+int dg_gemm_fused_with_kernel(dg_op_t transB, int64_t groups, const int32_t *offsets, int64_t M, int64_t N, int64_t K,
+                              float alpha, const void *A, int64_t lda, const void *B, int64_t ldb, int64_t strideB,
+                              const void *bias, int64_t strideBias, dg_epilogue_t epilogue, void *Z, int64_t ldz, float beta,
+                              const void *R, int64_t ldr, void *C, int64_t ldc, dg_dtype_t dtype, int splits,
+                              void *workspace, size_t workspace_bytes, void *stream, int kernel)
+{
+    const RowsCall c = {transB, groups, offsets, M, N, K, alpha, A, lda, B, ldb, strideB, C, ldc, dtype, splits, workspace,
+                        workspace_bytes, stream, kernel};
+    LayerParams p = {};
+    p.kind = dg::LAYER_FORWARD;
+    return rows_product(c, p, [&](int64_t cb) {
+        if (bias != nullptr && bad_ptr(bias, cb)) return -13;
+        if (strideBias < 0) return -14;
+        if (epilogue != DG_EPI_NONE && epilogue != DG_EPI_RELU && epilogue != DG_EPI_GELU) return -15;
+        if (int rc = check_rows(Z, ldz, N, cb, 16)) return rc;
+        if (int rc = check_rows(R, ldr, N, cb, 19)) return rc;
+        p.bias = bias;
+        p.stride_bias = strideBias;
+        p.act = epilogue;
+        p.keep = Z;
+        p.ldk = ldz;
+        p.beta = beta;
+        p.R = R;
+        p.ldr = ldr;
+        return 0;
+    });
+}
+
+int dg_gemm_fused(dg_op_t transB, int64_t groups, const int32_t *offsets, int64_t M, int64_t N, int64_t K, float alpha,
+                  const void *A, int64_t lda, const void *B, int64_t ldb, int64_t strideB, const void *bias,
+                  int64_t strideBias, dg_epilogue_t epilogue, void *Z, int64_t ldz, float beta, const void *R, int64_t ldr,
+                  void *C, int64_t ldc, dg_dtype_t dtype, int splits, void *workspace, size_t workspace_bytes, void *stream)
+{
+    return dg_gemm_fused_with_kernel(transB, groups, offsets, M, N, K, alpha, A, lda, B, ldb, strideB, bias, strideBias,
+                                     epilogue, Z, ldz, beta, R, ldr, C, ldc, dtype, splits, workspace, workspace_bytes,
+                                     stream, DG_KERNEL_AUTO);
+}
+
+int dg_gemm_act_grad_with_kernel(dg_op_t transB, int64_t groups, const int32_t *offsets, int64_t M, int64_t N, int64_t K,
+                                 float alpha, const void *A, int64_t lda, const void *B, int64_t ldb, int64_t strideB,
+                                 float beta, const void *R, int64_t ldr, void *H, int64_t ldh, dg_epilogue_t activation,
+                                 const void *Z, int64_t ldz, void *C, int64_t ldc, dg_dtype_t dtype, int splits,
+                                 void *workspace, size_t workspace_bytes, void *stream, int kernel)
+{
+    const RowsCall c = {transB, groups, offsets, M, N, K, alpha, A, lda, B, ldb, strideB, C, ldc, dtype, splits, workspace,
+                        workspace_bytes, stream, kernel};
+    LayerParams p = {};
+    p.kind = dg::LAYER_GRAD;
+    return rows_product(c, p, [&](int64_t cb) {
+        if (int rc = check_rows(R, ldr, N, cb, 14)) return rc;
+        if (int rc = check_rows(H, ldh, N, cb, 16)) return rc;
+        if (activation != DG_EPI_RELU && activation != DG_EPI_GELU) return -18;
+        if (c.work() && bad_ptr(Z, cb)) return -19;
+        if (ldz < max1(N)) return -20;
+        p.beta = beta;
+        p.R = R;
+        p.ldr = ldr;
+        p.keep = H;
+        p.ldk = ldh;
+        p.act = activation;
+        p.Z = Z;
+        p.ldz = ldz;
+        return 0;
+    });
+}
+
+int dg_gemm_act_grad(dg_op_t transB, int64_t groups, const int32_t *offsets, int64_t M, int64_t N, int64_t K, float alpha,
+                     const void *A, int64_t lda, const void *B, int64_t ldb, int64_t strideB, float beta, const void *R,
+                     int64_t ldr, void *H, int64_t ldh, dg_epilogue_t activation, const void *Z, int64_t ldz, void *C,
+                     int64_t ldc, dg_dtype_t dtype, int splits, void *workspace, size_t workspace_bytes, void *stream)
+{
+    return dg_gemm_act_grad_with_kernel(transB, groups, offsets, M, N, K, alpha, A, lda, B, ldb, strideB, beta, R, ldr, H,
+                                        ldh, activation, Z, ldz, C, ldc, dtype, splits, workspace, workspace_bytes, stream,
+                                        DG_KERNEL_AUTO);
+}
+
+int dg_gemm_dw_with_kernel(int64_t groups, const int32_t *offsets, int64_t rows, int64_t M, int64_t N, float alpha,
+                           const void *A, int64_t lda, const void *B, int64_t ldb, float beta, void *C, int64_t ldc,
+                           int64_t strideC, float *dbias, dg_dtype_t dtype, int splits, void *workspace,
+                           size_t workspace_bytes, void *stream, int kernel)
+{
+    if (groups < 0 || groups > kMaxGroups || (offsets == nullptr && groups != 1)) return -1;
+    if (offsets != nullptr && bad_ptr(offsets, 4)) return -2;
+    if (rows < 0 || rows > kMaxDim) return -3;
+    if (M < 0 || M > kMaxDim) return -4;
+    if (N < 0 || N > kMaxDim) return -5;
+    if (!is_dtype(dtype)) return -16;
+    const int64_t eb = bytes_of(operand_type(dtype)), cb = bytes_of(output_type(dtype));
+    const bool work = groups > 0 && M > 0 && N > 0, sums = dbias != nullptr && groups > 0 && M > 0;
+    const bool reads = work && rows > 0 && alpha != 0.f;
+    if ((reads || (sums && rows > 0)) && bad_ptr(A, eb)) return -7;
+    if (lda < max1(M)) return -8;
+    if (reads && bad_ptr(B, eb)) return -9;
+    if (ldb < max1(N)) return -10;
+    if (work && bad_ptr(C, cb)) return -12;
+    if (ldc < max1(N)) return -13;
+    if (strideC < 0 || (work && groups > 1 && strideC < (M - 1) * ldc + N)) return -14;
+    if (dbias != nullptr && bad_ptr(dbias, 4)) return -15;
+    if (splits < 0 || splits > 4096) return -17;
+    LayerParams p = {};
+    p.kind = dg::LAYER_WEIGHTS;
+    p.A = A;
+    p.B = B;
+    p.lda = lda;
+    p.ldb = ldb;
+    p.M = (int32_t)M;
+    p.N = (int32_t)N;
+    p.K = (int32_t)rows;
+    p.alpha = alpha;
+    p.beta = beta;
+    p.offsets = offsets;
+    p.groups = (int32_t)groups;
+    p.R = beta != 0.f ? C : nullptr;
+    p.ldr = ldc;
+    p.C = C;
+    p.ldc = ldc;
+    p.strideC = strideC;
+    p.ctype = output_type(dtype);
+    p.dbias = dbias;
+    if (sums && (M > kMaxTiled || rows > kMaxTiled)) return DG_ERR_UNSUPPORTED;
+    if (work) {
+        LayerParams q = p;
+        if (!reads) q.K = 0;
+        const LayerShape s = {p.kind, operand_type(dtype), false, offsets != nullptr, groups, M, N, q.K};
+        const int rc = launch(q, s, dtype, kernel, splits, workspace, workspace_bytes, 18, (hipStream_t)stream);
+        if (rc != DG_OK) return rc;
+    }
+    return sums ? dg::launch_status(dg::launch_layer_colsum(p, operand_type(dtype), (hipStream_t)stream)) : DG_OK;
+}
+
+int dg_gemm_dw(int64_t groups, const int32_t *offsets, int64_t rows, int64_t M, int64_t N, float alpha, const void *A,
+               int64_t lda, const void *B, int64_t ldb, float beta, void *C, int64_t ldc, int64_t strideC, float *dbias,
+               dg_dtype_t dtype, int splits, void *workspace, size_t workspace_bytes, void *stream)
+{
+    return dg_gemm_dw_with_kernel(groups, offsets, rows, M, N, alpha, A, lda, B, ldb, beta, C, ldc, strideC, dbias, dtype,
+                                  splits, workspace, workspace_bytes, stream, DG_KERNEL_AUTO);
+}
+
+int dg_gemm_fused_choose(int64_t M, int64_t N, int64_t K, dg_op_t transB, dg_dtype_t dtype)
+{
+    if (M < 0 || M > kMaxDim) return -1;
+    if (N < 0 || N > kMaxDim) return -2;
+    if (K < 0 || K > kMaxDim) return -3;
+    if (transB != DG_OP_N && transB != DG_OP_T) return -4;
+    if (!is_dtype(dtype)) return -5;
+    if (M == 0 || N == 0) return 1;
+    const LayerShape s = {dg::LAYER_FORWARD, operand_type(dtype), transB == DG_OP_T, false, 1, M, N, K};
+    return resolve_splits(s, 0);
+}
+
+int dg_gemm_dw_choose(int64_t groups, int64_t rows, int64_t M, int64_t N, dg_dtype_t dtype)
+{
+    if (groups < 0 || groups > kMaxGroups) return -1;
+    if (rows < 0 || rows > kMaxDim) return -2;
+    if (M < 0 || M > kMaxDim) return -3;
+    if (N < 0 || N > kMaxDim) return -4;
+    if (!is_dtype(dtype)) return -5;
+    if (groups == 0 || M == 0 || N == 0) return 1;
+    const LayerShape s = {dg::LAYER_WEIGHTS, operand_type(dtype), false, groups > 1, groups, M, N, rows};
+    return resolve_splits(s, 0);
+}
+
+size_t dg_layer_workspace_size(int64_t groups, int64_t M, int64_t N, int splits)
+{
+    return workspace_bytes_of(groups, M, N, splits);
+}
+
+const char *dg_layer_kernel_name(int kernel) { return kernel >= 0 && kernel < kNumLayer ? kLayer[kernel].name : nullptr; }
+
+}  // extern "C"

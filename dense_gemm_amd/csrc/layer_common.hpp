@@ -1,0 +1,370 @@
+// Shared by the kernels of a layer's products (fused epilogues, grouped by
+// expert, weight gradients): their parameters, the epilogue's arithmetic, and
+// which tile of which group a workgroup takes.
+//
+//   forward    z = alpha * acc + bias;        C = act(z) + beta * R
+//   gradient   h = alpha * acc + beta * R;    C = h * act'(Z)
+//   weights    C = alpha * acc + beta * C
+// z (forward) or h (gradient) is written to `keep` when that is given.  Sums and
+// the epilogue are fp32, with one rounding of each output.
+#pragma once
+
+#include "gemm_common.hpp"
+
+namespace dg {
+
+enum { LAYER_FORWARD = 0, LAYER_GRAD = 1, LAYER_WEIGHTS = 2 };
+
+struct LayerParams {
+    const void *A, *B;
+    int64_t lda, ldb, strideB;      // strideB: from a group's B to the next (elements)
+    // forward, gradient: A holds M rows, the groups' B is K x N (or N x K).
+    // weights: A and B hold K rows, a group's C is M x N.
+    int32_t M, N, K;
+    float alpha, beta;
+    int32_t kind, act;
+    const int32_t *offsets;         // groups + 1 row offsets on the device; NULL: one group of all rows
+    int32_t groups;
+    const void *bias;
+    int64_t stride_bias;
+    const void *Z;                  // gradient: the activation's input
+    int64_t ldz;
+    const void *R;                  // weights: C itself, or NULL for beta = 0
+    int64_t ldr;
+    void *keep;
+    int64_t ldk;
+    void *C;
+    int64_t ldc, strideC;           // strideC: weights, from a group's C to the next
+    int32_t ctype;                  // element of C, R, Z, keep and bias: 0 fp32, 1 fp16, 2 bf16
+    int32_t tiles_m, tiles_n, group_m;
+    int32_t splits;                 // K ranges, a grid dimension; with more than one the raw sums go to ws
+    float *ws;                      // [splits][groups][M][N]
+    float *dbias;                   // weights: [groups][M], or NULL
+};
+
+typedef hipError_t (*layer_launch_fn)(const LayerParams &p, hipStream_t s);
+
+#ifdef __HIPCC__
+
+// erfc(z), z >= 0, with gauss = exp(-z^2).  For 16-bit results erfc(z) exp(z^2) as a
+// polynomial in t = 1 / (1 + 0.44 z), fitted here to the least largest relative
+// error over 0 <= z <= 9: 5.2e-6, a thousandth of a bf16 step also far out on
+// gelu's negative side, for one step more than gelu()'s polynomial (whose
+// absolute error of 1.5e-7 is 4e-4 of gelu at -4).  For fp32 results the
+// device library's erfcf.
+template <bool EXACT>
+__device__ __forceinline__ float erfc_pos(float z, float gauss)
+{
+    if constexpr (EXACT) {
+        return erfcf(z);
+    } else {
+        const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.44f, z, 1.f));
+        float poly = __builtin_fmaf(t, -0.14608541f, 0.35058573f);
+        poly = __builtin_fmaf(t, poly, 0.040815864f);
+        poly = __builtin_fmaf(t, poly, 0.26353481f);
+        poly = __builtin_fmaf(t, poly, 0.24258447f);
+        poly = __builtin_fmaf(t, poly, 0.24855939f);
+        return poly * t * gauss;
+    }
+}
+
+// act(x) of the forward pass: gelu(x) = x Phi(x) with Phi(x) = 1 - q/2 (x >= 0) or
+// q/2, q = erfc(|x| / sqrt 2), so that the negative side keeps its relative accuracy.
+template <bool EXACT>
+__device__ __forceinline__ float layer_act(int act, float x)
+{
+    if (act == ACT_RELU) return x < 0.f ? 0.f : x;
+    if (act == ACT_GELU) {
+        const float z = __builtin_fabsf(x) * 0.70710678118654752f;
+        const float q = erfc_pos<EXACT>(z, EXACT ? 0.f : __expf(-z * z));
+        return x >= 0.f ? x * __builtin_fmaf(-0.5f, q, 1.f) : 0.5f * x * q;
+    }
+    return x;
+}
+
+// h * act'(x).  relu chooses h or 0 (an infinite or NaN h does not pass a unit
+// that is off; a NaN x gives NaN).  gelu' = Phi(x) + x phi(x); at |x| >= 16
+// phi underflows and x phi is 0, infinities included.
+template <bool EXACT>
+__device__ __forceinline__ float layer_act_grad(int act, float h, float x)
+{
+    if (act == ACT_RELU) return x > 0.f ? h : (x <= 0.f ? 0.f : x);
+    if (act == ACT_GELU) {
+        const float a = __builtin_fabsf(x), z = a * 0.70710678118654752f;
+        const float gauss = EXACT ? expf(-0.5f * x * x) : __expf(-z * z);
+        const float q = erfc_pos<EXACT>(z, gauss);
+        const float cdf = x >= 0.f ? __builtin_fmaf(-0.5f, q, 1.f) : 0.5f * q;
+        const float slope = a < 16.f ? __builtin_fmaf(x * 0.39894228040143268f, gauss, cdf) : cdf;
+        return h * slope;
+    }
+    return h;
+}
+
+// W consecutive elements of a row as fp32, by 16-byte accesses that need no more
+// than the element's alignment; `n` of them exist (the others are 0 and not read).
+template <typename T, int W>
+__device__ __forceinline__ void load_row(const T *x, int n, float (&v)[W])
+{
+    constexpr int PER = (int)(16 / sizeof(T)) < W ? (int)(16 / sizeof(T)) : W;
+    typedef T V __attribute__((ext_vector_type(PER)));
+    typedef V __attribute__((aligned(sizeof(T)))) Vu;
+    if (n >= W) {
+#pragma unroll
+        for (int c = 0; c < W / PER; ++c) {
+            const V y = *(const Vu *)(x + c * PER);
+#pragma unroll
+            for (int e = 0; e < PER; ++e) v[c * PER + e] = (float)y[e];
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < W; ++e) v[e] = e < n ? (float)x[e] : 0.f;
+    }
+}
+
+template <typename T, int W>
+__device__ __forceinline__ void store_row(T *x, int n, const float (&v)[W])
+{
+    constexpr int PER = (int)(16 / sizeof(T)) < W ? (int)(16 / sizeof(T)) : W;
+    typedef T V __attribute__((ext_vector_type(PER)));
+    typedef V __attribute__((aligned(sizeof(T)))) Vu;
+    if (n >= W) {
+#pragma unroll
+        for (int c = 0; c < W / PER; ++c) {
+            V y;
+#pragma unroll
+            for (int e = 0; e < PER; ++e) y[e] = (T)v[c * PER + e];
+            *(Vu *)(x + c * PER) = y;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < W; ++e)
+            if (e < n) x[e] = (T)v[e];
+    }
+}
+
+// The tile a workgroup works on, with its group's matrices.
+struct LayerTile {
+    int group;
+    int rows;            // rows of the group (forward, gradient) or of C (weights)
+    int m0, n0;
+    int64_t row0;        // first row of the group in the matrices of rows
+    int k0, k_len;       // this split's part of the sum
+};
+
+// What a row of C needs beside the sums, fetched ahead of them.
+template <typename TC, int W>
+struct LayerAux {
+    float r[W], z[W];
+    __device__ __forceinline__ void fetch(const LayerParams &p, const LayerTile &t, int row, int col, int n)
+    {
+        if (p.kind == LAYER_WEIGHTS) {
+            if (p.R) load_row<TC, W>((const TC *)p.R + t.group * p.strideC + (int64_t)row * p.ldr + col, n, r);
+            return;
+        }
+        if (p.R) load_row<TC, W>((const TC *)p.R + (t.row0 + row) * p.ldr + col, n, r);
+        if (p.kind == LAYER_GRAD) load_row<TC, W>((const TC *)p.Z + (t.row0 + row) * p.ldz + col, n, z);
+    }
+};
+
+// The epilogue of W columns col .. of row `row` (n of them exist): v holds the sums.
+template <typename TC, int W>
+__device__ __forceinline__ void layer_finish(const LayerParams &p, const LayerTile &t, int row, int col, int n,
+                                             float (&v)[W], const LayerAux<TC, W> &aux, const float (&bias)[W])
+{
+    constexpr bool EXACT = sizeof(TC) == 4;
+    int64_t at;
+    if (p.kind == LAYER_WEIGHTS) {
+        at = t.group * p.strideC + (int64_t)row * p.ldc + col;
+#pragma unroll
+        for (int e = 0; e < W; ++e) v[e] *= p.alpha;
+        if (p.R) {
+#pragma unroll
+            for (int e = 0; e < W; ++e) v[e] = __builtin_fmaf(p.beta, aux.r[e], v[e]);
+        }
+    } else {
+        const int64_t grow = t.row0 + row;
+        at = grow * p.ldc + col;
+        if (p.kind == LAYER_FORWARD) {
+#pragma unroll
+            for (int e = 0; e < W; ++e) v[e] = __builtin_fmaf(p.alpha, v[e], bias[e]);
+            if (p.keep) store_row<TC, W>((TC *)p.keep + grow * p.ldk + col, n, v);
+            if (p.act == ACT_GELU) {
+#pragma unroll
+                for (int e = 0; e < W; ++e) v[e] = layer_act<EXACT>(ACT_GELU, v[e]);
+            } else if (p.act == ACT_RELU) {
+#pragma unroll
+                for (int e = 0; e < W; ++e) v[e] = layer_act<EXACT>(ACT_RELU, v[e]);
+            }
+            if (p.R) {
+#pragma unroll
+                for (int e = 0; e < W; ++e) v[e] = __builtin_fmaf(p.beta, aux.r[e], v[e]);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < W; ++e) v[e] *= p.alpha;
+            if (p.R) {
+#pragma unroll
+                for (int e = 0; e < W; ++e) v[e] = __builtin_fmaf(p.beta, aux.r[e], v[e]);
+            }
+            if (p.keep) store_row<TC, W>((TC *)p.keep + grow * p.ldk + col, n, v);
+            if (p.act == ACT_GELU) {
+#pragma unroll
+                for (int e = 0; e < W; ++e) v[e] = layer_act_grad<EXACT>(ACT_GELU, v[e], aux.z[e]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < W; ++e) v[e] = layer_act_grad<EXACT>(ACT_RELU, v[e], aux.z[e]);
+            }
+        }
+    }
+    store_row<TC, W>((TC *)p.C + at, n, v);
+}
+
+// The bias of W columns of a group.
+template <typename TC, int W>
+__device__ __forceinline__ void layer_bias(const LayerParams &p, int group, int col, int n, float (&b)[W])
+{
+    if (p.kind == LAYER_FORWARD && p.bias) {
+        load_row<TC, W>((const TC *)p.bias + group * p.stride_bias + col, n > 0 ? n : 0, b);
+    } else {
+#pragma unroll
+        for (int e = 0; e < W; ++e) b[e] = 0.f;
+    }
+}
+
+// The raw sums of a split's W columns.
+template <int W>
+__device__ __forceinline__ void layer_partial(const LayerParams &p, const LayerTile &t, int row, int col, int n,
+                                              const float (&v)[W])
+{
+    float *w = p.ws + (((int64_t)blockIdx.y * p.groups + t.group) * p.M + row) * p.N + col;
+    store_row<float, W>(w, n, v);
+}
+
+// First row and rows of group g.  Offsets outside 0 .. total and descending ones
+// are brought back, so that no offset leads outside the matrices.
+__device__ __forceinline__ void group_rows(const LayerParams &p, int g, int total, int &begin, int &rows)
+{
+    int b = p.offsets[g], e = p.offsets[g + 1];
+    b = b < 0 ? 0 : (b > total ? total : b);
+    e = e < b ? b : (e > total ? total : e);
+    begin = b;
+    rows = e - b;
+}
+
+// Workgroup ids go to the 8 XCDs in turn; give each XCD a contiguous range of
+// the `nwg` tiles, so that the tiles resident on it share rows and columns.
+__device__ __forceinline__ int xcd_contiguous(int bid, int nwg)
+{
+    const int xcd = bid & 7, local = bid >> 3, per = nwg >> 3, rem = nwg & 7;
+    return xcd * per + (xcd < rem ? xcd : rem) + local;
+}
+
+// Tile `in` of a group with tiles_m x tiles_n: group_m tile rows are walked
+// together, column by column.
+__device__ __forceinline__ void walk_tiles(int in, int tiles_m, int tiles_n, int group_m, int &tm, int &tn)
+{
+    const int gsz = group_m * tiles_n, g = in / gsz, first = g * group_m;
+    const int rows = tiles_m - first < group_m ? tiles_m - first : group_m;
+    const int r = in - g * gsz;
+    tm = first + r % rows;
+    tn = r / rows;
+}
+
+// The tile of this workgroup, or false where the launch has more workgroups
+// than tiles.  The host does not know how many rows a group has: the launch
+// holds one workgroup for every tile there can be, and a wave counts the groups'
+// tiles (64 groups at a time, a lane each) to find its own.
+__device__ __forceinline__ bool layer_tile(const LayerParams &p, int bm, int bn, LayerTile &t)
+{
+    int id = blockIdx.x;
+    t.group = 0;
+    t.row0 = 0;
+    if (p.kind == LAYER_WEIGHTS) {
+        const int per = p.tiles_m * p.tiles_n;
+        id = xcd_contiguous(id, per * p.groups);
+        t.group = id / per;
+        int tm, tn;
+        walk_tiles(id - t.group * per, p.tiles_m, p.tiles_n, p.group_m, tm, tn);
+        t.m0 = tm * bm;
+        t.n0 = tn * bn;
+        t.rows = p.M;
+        int begin = 0, n = p.K;
+        if (p.offsets) group_rows(p, t.group, p.K, begin, n);
+        t.row0 = __builtin_amdgcn_readfirstlane(begin);
+        n = __builtin_amdgcn_readfirstlane(n);
+        t.k0 = 0;
+        t.k_len = n;
+        if (p.splits > 1) {
+            const int chunk = ((n + p.splits - 1) / p.splits + 63) & ~63;
+            const int64_t b = (int64_t)blockIdx.y * chunk;
+            t.k0 = b < n ? (int)b : n;
+            t.k_len = n - t.k0 < chunk ? n - t.k0 : chunk;
+        }
+        return true;
+    }
+    t.k0 = 0;
+    t.k_len = p.K;
+    int tiles_m, first = 0;                     // of the group, and its first tile row
+    if (p.offsets == nullptr) {
+        tiles_m = p.tiles_m;
+        t.rows = p.M;
+        id = xcd_contiguous(id, tiles_m * p.tiles_n);
+        if (p.splits > 1) {
+            const int chunk = ((p.K + p.splits - 1) / p.splits + 63) & ~63;
+            const int64_t b = (int64_t)blockIdx.y * chunk;
+            t.k0 = b < p.K ? (int)b : p.K;
+            t.k_len = p.K - t.k0 < chunk ? p.K - t.k0 : chunk;
+        }
+    } else {
+        const int lane = threadIdx.x & 63;
+        auto tiles_of = [&](int g) {
+            int b = 0, n = 0;
+            if (g < p.groups) group_rows(p, g, p.M, b, n);
+            return (n + bm - 1) / bm;
+        };
+        auto scan = [&](int x) {                // inclusive sums over the lanes
+#pragma unroll
+            for (int d = 1; d < 64; d <<= 1) {
+                const int y = __shfl_up(x, d);
+                if (lane >= d) x += y;
+            }
+            return x;
+        };
+        int sum = scan(tiles_of(lane)), total = __builtin_amdgcn_readlane(sum, 63);
+        const int sum0 = sum, total0 = total;
+        for (int base = 64; base < p.groups; base += 64) {
+            sum = scan(tiles_of(base + lane));
+            total += __builtin_amdgcn_readlane(sum, 63);
+        }
+        if (id >= total * p.tiles_n) return false;
+        id = xcd_contiguous(id, total * p.tiles_n);
+        const int row = id / p.tiles_n;         // tile row, counted over all groups
+        int base = 0, before = 0;
+        sum = sum0;
+        for (int upto = total0; row >= upto;) {
+            base += 64;
+            before = upto;
+            sum = scan(tiles_of(base + lane));
+            upto += __builtin_amdgcn_readlane(sum, 63);
+        }
+        const uint64_t past = __ballot(before + sum > row);
+        const int l = __ffsll((unsigned long long)past) - 1;
+        t.group = base + l;
+        const int upto = before + __builtin_amdgcn_readlane(sum, l);
+        first = l == 0 ? before : before + __builtin_amdgcn_readlane(sum, l - 1);
+        tiles_m = upto - first;
+        int begin, n;
+        group_rows(p, t.group, p.M, begin, n);
+        t.row0 = __builtin_amdgcn_readfirstlane(begin);
+        t.rows = __builtin_amdgcn_readfirstlane(n);
+    }
+    int tm, tn;
+    walk_tiles(id - first * p.tiles_n, tiles_m, p.tiles_n, p.group_m, tm, tn);
+    t.m0 = tm * bm;
+    t.n0 = tn * bn;
+    return true;
+}
+
+#endif
+
+}  // namespace dg

@@ -1,0 +1,106 @@
+// Passes beside a layer's products: the join of a split sum, and the column sums
+// of a weight gradient's bias.
+#include "layer_common.hpp"
+
+namespace dg {
+
+namespace {
+
+// The splits' raw sums (ws[split][group][M][N], fp32), added in their order, and the
+// epilogue: 8 columns of a row a thread.
+template <typename TC>
+__global__ __launch_bounds__(256) void layer_join_kernel(LayerParams p)
+{
+    const int per_row = (p.N + 7) / 8;
+    const int64_t total = (int64_t)p.groups * p.M * per_row, mn = (int64_t)p.groups * p.M * p.N;
+    for (int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x; at < total; at += (int64_t)gridDim.x * 256) {
+        const int64_t grow = at / per_row;
+        const int col = (int)(at - grow * per_row) * 8, n = p.N - col;
+        LayerTile t;
+        t.group = (int)(grow / p.M);
+        t.row0 = 0;
+        const int row = (int)(grow - (int64_t)t.group * p.M);
+        LayerAux<TC, 8> aux;
+        aux.fetch(p, t, row, col, n);
+        float v[8], bias[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = 0.f;
+        const float *w = p.ws + grow * p.N + col;
+        for (int s = 0; s < p.splits; s += 4) {
+            float x[4][8];
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (s + u < p.splits) load_row<float, 8>(w + (s + u) * mn, n, x[u]);
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (s + u < p.splits)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] += x[u][e];
+        }
+        layer_bias<TC, 8>(p, t.group, col, n, bias);
+        layer_finish<TC, 8>(p, t, row, col, n, v, aux, bias);
+    }
+}
+
+// dbias[g][m] = sum over group g's rows of A[r][m] (+ beta * dbias): a workgroup
+// takes 64 columns of a group, 64 rows at a time, 8 columns of a row a lane; the
+// 64 partial sums of a column are added in a fixed order.
+template <typename T>
+__global__ __launch_bounds__(512) void layer_colsum_kernel(LayerParams p)
+{
+    __shared__ float red[64][65];
+    const int g = blockIdx.y, lc = (threadIdx.x & 7) * 8, lr = threadIdx.x >> 3;
+    const int col = blockIdx.x * 64 + lc, n = p.M - col;
+    int begin = 0, rows = p.K;
+    if (p.offsets) group_rows(p, g, p.K, begin, rows);
+    const T *a = (const T *)p.A + (int64_t)begin * p.lda + col;
+    float s[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s[e] = 0.f;
+    for (int r = lr; r < rows; r += 256) {
+        float v[4][8];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            load_row<T, 8>(a + (int64_t)(r + 64 * u < rows ? r + 64 * u : r) * p.lda, r + 64 * u < rows ? n : 0, v[u]);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s[e] += v[u][e];
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) red[lr][lc + e] = s[e];
+    __syncthreads();
+    if (threadIdx.x < 64 && blockIdx.x * 64 + (int)threadIdx.x < p.M) {
+        float v = 0.f;
+#pragma unroll 8
+        for (int r = 0; r < 64; ++r) v += red[r][threadIdx.x];
+        float *d = p.dbias + (int64_t)g * p.M + blockIdx.x * 64 + threadIdx.x;
+        *d = p.beta != 0.f ? __builtin_fmaf(p.beta, *d, v) : v;
+    }
+}
+
+}  // namespace
+
+hipError_t launch_layer_join(const LayerParams &p, hipStream_t s)
+{
+    const int64_t total = (int64_t)p.groups * p.M * ((p.N + 7) / 8), blocks = (total + 255) / 256;
+    LayerParams arg = p;
+    void *args[] = {&arg};
+    const void *f = p.ctype == 0 ? (const void *)&layer_join_kernel<float>
+                                 : p.ctype == 1 ? (const void *)&layer_join_kernel<_Float16>
+                                                : (const void *)&layer_join_kernel<__bf16>;
+    return hipLaunchKernel(f, dim3((unsigned)(blocks < 65536 ? blocks : 65536)), dim3(256), args, 0, s);
+}
+
+// type: of the operands (0 fp32, 1 fp16, 2 bf16)
+hipError_t launch_layer_colsum(const LayerParams &p, int type, hipStream_t s)
+{
+    LayerParams arg = p;
+    void *args[] = {&arg};
+    const void *f = type == 0 ? (const void *)&layer_colsum_kernel<float>
+                              : type == 1 ? (const void *)&layer_colsum_kernel<_Float16>
+                                          : (const void *)&layer_colsum_kernel<__bf16>;
+    return hipLaunchKernel(f, dim3((unsigned)((p.M + 63) / 64), (unsigned)p.groups), dim3(512), args, 0, s);
+}
+
+}  // namespace dg

@@ -434,6 +434,107 @@ int dg_act_backward(int64_t rows, int64_t cols, const void *dH, int64_t ldh, dg_
                     void *stream);
 size_t dg_act_backward_workspace_size(int64_t rows, int64_t cols);
 
+/* ---- A layer's products ----------------------------------------------------------
+ *
+ * The products of a layer with its whole epilogue, forward and backward, with one
+ * matrix or with one for each group of rows (an expert's tokens).  Types, pointers,
+ * streams, asynchrony and errors as dg_gemm: -i names an invalid argument by its
+ * position (dtype is checked before the pointers whose alignment depends on it),
+ * nothing is enqueued then, no call allocates memory or keeps state, and calls
+ * on different streams do not interfere unless they share a workspace or an
+ * output.  Matrices are row-major and aligned to their element; any row stride
+ * from the row's length on will do.
+ *
+ * Groups.  With `offsets`, groups + 1 ascending int32 values in device memory, rows
+ * offsets[g] .. offsets[g + 1] - 1 of every matrix of rows belong to group g (0 ..
+ * groups - 1, at most 65535); a group may be empty.  Rows before offsets[0] and
+ * from offsets[groups] on belong to none: they are not read, and left as they were
+ * in every output.  The offsets are read by the kernels; values outside 0 .. the
+ * number of rows are taken as the nearest of these and a descending pair as an empty
+ * group, so no value reaches outside the matrices, but rows that two groups claim
+ * are unspecified.  offsets = NULL (with groups = 1): all rows, one matrix.
+ *
+ * Sums and the epilogue are fp32; each output is rounded once.  With gelu = x Phi(x)
+ * and gelu'(x) = Phi(x) + x phi(x), Phi is off by at most 6e-6 of its smaller
+ * tail for 16-bit outputs, and by a few fp32 roundings for fp32 ones. */
+
+/* Z = alpha * A op(B_g) + bias_g;  C = act(Z) + beta * R.
+ * A holds M rows of K, C (and R, Z) M rows of N; op(B) is K x N, group g's matrix
+ * at B + g * strideB (elements; 0: one matrix for every group), its bias of N
+ * elements at bias + g * strideBias.  bias, R and Z may be NULL: no bias, no R,
+ * Z not stored.  R may be C itself (ldr = ldc); otherwise outputs must not
+ * overlap anything else.  beta == 0: R is not read.  K == 0 or alpha == 0: A and
+ * B are not read.  M == 0 or N == 0 or groups == 0: nothing is done.
+ *   splits: K ranges, as dg_gemm_splitk (0: the library's choice,
+ *   dg_gemm_fused_choose; always one with offsets); their fp32 sums go to the
+ *   workspace of dg_layer_workspace_size(1, M, N, splits) bytes.
+ *   DG_ERR_UNSUPPORTED: M, N or K above 2^31 - 1025, or more tiles than a launch
+ *   holds (2^32 / 256 of 64 x 64).
+ *   1 transB, 2 groups, 3 offsets, 4 M, 5 N, 6 K, 7 alpha, 8 A, 9 lda, 10 B, 11 ldb,
+ *   12 strideB, 13 bias, 14 strideBias, 15 epilogue, 16 Z, 17 ldz, 18 beta, 19 R,
+ *   20 ldr, 21 C, 22 ldc, 23 dtype, 24 splits (below 0 or above 4096), 25
+ *   workspace (NULL or not 16-byte aligned), 26 workspace_bytes (too few), 27 stream. */
+int dg_gemm_fused(dg_op_t transB, int64_t groups, const int32_t *offsets, int64_t M, int64_t N, int64_t K, float alpha,
+                  const void *A, int64_t lda, const void *B, int64_t ldb, int64_t strideB, const void *bias,
+                  int64_t strideBias, dg_epilogue_t epilogue, void *Z, int64_t ldz, float beta, const void *R, int64_t ldr,
+                  void *C, int64_t ldc, dg_dtype_t dtype, int splits, void *workspace, size_t workspace_bytes, void *stream);
+
+/* H = alpha * A op(B_g) + beta * R;  C = H * act'(Z), the gradient that a layer hands
+ * to the activation below it: A the gradient of the layer's output, op(B) its
+ * weights, R a gradient that joins (a residual's; NULL for none), Z the
+ * activation's input as dg_gemm_fused stores it, activation DG_EPI_RELU or
+ * DG_EPI_GELU.  H (NULL: not stored) receives the sum before act'.  relu
+ * chooses H where z > 0 and 0 elsewhere (an infinite or NaN H too); where z is
+ * NaN, C is.  R may be C or H itself, H may not be C.  The rest as dg_gemm_fused.
+ *   1 .. 12 as dg_gemm_fused, 13 beta, 14 R, 15 ldr, 16 H, 17 ldh, 18 activation,
+ *   19 Z, 20 ldz, 21 .. 27 as dg_gemm_fused. */
+int dg_gemm_act_grad(dg_op_t transB, int64_t groups, const int32_t *offsets, int64_t M, int64_t N, int64_t K, float alpha,
+                     const void *A, int64_t lda, const void *B, int64_t ldb, int64_t strideB, float beta, const void *R,
+                     int64_t ldr, void *H, int64_t ldh, dg_epilogue_t activation, const void *Z, int64_t ldz, void *C,
+                     int64_t ldc, dg_dtype_t dtype, int splits, void *workspace, size_t workspace_bytes, void *stream);
+
+/* C_g = alpha * A_g^T B_g + beta * C_g, a layer's weight gradient: A holds `rows` rows
+ * of M (the gradient of the layer's output), B rows of N (its input), A_g and B_g
+ * are group g's rows of them, and C_g, M x N, lies at C + g * strideC
+ * (strideC >= (M - 1) * ldc + N with more than one group).  dbias (fp32, M elements
+ * for each group, contiguous; NULL for none) receives the column sums of A_g, +
+ * beta * dbias_g, unscaled by alpha.  A group without rows: beta * C_g and beta *
+ * dbias_g.  beta == 0: C and dbias are not read; alpha == 0: B is not read.
+ *   splits: ranges of each group's rows (0: the library's choice,
+ *   dg_gemm_dw_choose), their fp32 sums in the workspace of
+ *   dg_layer_workspace_size(groups, M, N, splits) bytes.
+ *   DG_ERR_UNSUPPORTED as dg_gemm_fused.
+ *   1 groups, 2 offsets, 3 rows, 4 M, 5 N, 6 alpha, 7 A, 8 lda, 9 B, 10 ldb, 11 beta,
+ *   12 C, 13 ldc, 14 strideC, 15 dbias, 16 dtype, 17 splits, 18 workspace, 19
+ *   workspace_bytes, 20 stream. */
+int dg_gemm_dw(int64_t groups, const int32_t *offsets, int64_t rows, int64_t M, int64_t N, float alpha, const void *A,
+               int64_t lda, const void *B, int64_t ldb, float beta, void *C, int64_t ldc, int64_t strideC, float *dbias,
+               dg_dtype_t dtype, int splits, void *workspace, size_t workspace_bytes, void *stream);
+
+/* The same with a forced kernel (the last argument; DG_KERNEL_AUTO: the library's
+ * choice), for tests and measurement; DG_ERR_UNSUPPORTED when it cannot run the
+ * problem.  The kernels' names (NULL when out of range), the ranges that splits = 0
+ * gives (or -i: 1 M, 2 N, 3 K, 4 transB, 5 dtype; 1 groups, 2 rows, 3 M, 4 N, 5
+ * dtype), and the workspace's bytes (0 for one range). */
+int dg_gemm_fused_with_kernel(dg_op_t transB, int64_t groups, const int32_t *offsets, int64_t M, int64_t N, int64_t K,
+                              float alpha, const void *A, int64_t lda, const void *B, int64_t ldb, int64_t strideB,
+                              const void *bias, int64_t strideBias, dg_epilogue_t epilogue, void *Z, int64_t ldz, float beta,
+                              const void *R, int64_t ldr, void *C, int64_t ldc, dg_dtype_t dtype, int splits,
+                              void *workspace, size_t workspace_bytes, void *stream, int kernel);
+int dg_gemm_act_grad_with_kernel(dg_op_t transB, int64_t groups, const int32_t *offsets, int64_t M, int64_t N, int64_t K,
+                                 float alpha, const void *A, int64_t lda, const void *B, int64_t ldb, int64_t strideB,
+                                 float beta, const void *R, int64_t ldr, void *H, int64_t ldh, dg_epilogue_t activation,
+                                 const void *Z, int64_t ldz, void *C, int64_t ldc, dg_dtype_t dtype, int splits,
+                                 void *workspace, size_t workspace_bytes, void *stream, int kernel);
+int dg_gemm_dw_with_kernel(int64_t groups, const int32_t *offsets, int64_t rows, int64_t M, int64_t N, float alpha,
+                           const void *A, int64_t lda, const void *B, int64_t ldb, float beta, void *C, int64_t ldc,
+                           int64_t strideC, float *dbias, dg_dtype_t dtype, int splits, void *workspace,
+                           size_t workspace_bytes, void *stream, int kernel);
+int dg_gemm_fused_choose(int64_t M, int64_t N, int64_t K, dg_op_t transB, dg_dtype_t dtype);
+int dg_gemm_dw_choose(int64_t groups, int64_t rows, int64_t M, int64_t N, dg_dtype_t dtype);
+size_t dg_layer_workspace_size(int64_t groups, int64_t M, int64_t N, int splits);
+const char *dg_layer_kernel_name(int kernel);
+
 /* Number of kernels in the table, and a static name for kernel i (NULL when
  * i is out of range).  Names read "<dtype>_<tiles>_<variant>". */
 int dg_kernel_count(void);
@@ -445,7 +546,7 @@ int dg_kernel_tile_n(int kernel);
 
 /* Static text for a status code.  An invalid argument is given by its position
  * and named for the dense products only; the lists above name those of the MX
- * calls. */
+ * calls and of a layer's products. */
 const char *dg_status_string(int status);
 
 /* hipError_t of the calling thread's last DG_ERR_HIP (0 if none). */

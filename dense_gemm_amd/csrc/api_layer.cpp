@@ -33,22 +33,41 @@ bool bad_ptr(const void *p, int64_t align) { return p == nullptr || (uintptr_t)p
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t max1(int64_t x) { return x > 1 ? x : 1; }
 
+enum Loads { STAGED, DIRECT };
 struct LayerFamily {
     const char *name;
     int bm, bn, group_m, threads;
+    Loads loads;
 };
 const LayerFamily kLayer[] = {
-    {"layer_64x64_staged", 64, 64, 4, 256},
-    {"layer_128x128_staged", 128, 128, 4, 256},
+    {"layer_64x64_staged", 64, 64, 4, 256, STAGED},
+    {"layer_128x128_staged", 128, 128, 4, 256, STAGED},
+    {"layer_64x64_pipe", 64, 64, 4, 256, DIRECT},
+    {"layer_128x128_pipe", 128, 128, 4, 256, DIRECT},
+    {"layer_256x256_pipe", 256, 256, 4, 512, DIRECT},
 };
 constexpr int kNumLayer = sizeof(kLayer) / sizeof(kLayer[0]);
+enum { K_STAGED_64, K_STAGED_128, K_PIPE_64, K_PIPE_128, K_PIPE_256 };
 
 // What the choice of a kernel looks at.
 struct LayerShape {
     int kind, type;
     bool tb, ragged;
     int64_t groups, M, N, K;      // as LayerParams
+    bool direct;                  // the direct loads take the operands
 };
+
+// The direct loads' 16-byte pieces lie at whole multiples of 16 bytes from a row's
+// start, which has to be 4-byte aligned; 256 rows lie within 32-bit byte
+// offsets; and a row that runs across the summed index is at least a piece long.
+bool direct_ok(const LayerParams &p, int type, bool tb)
+{
+    const int64_t eb = bytes_of(type), per = 16 / eb, lim = (int64_t)1 << 31;
+    const bool dw = p.kind == dg::LAYER_WEIGHTS;
+    return ((uintptr_t)p.A & 3) == 0 && ((uintptr_t)p.B & 3) == 0 && p.lda * eb % 4 == 0 && p.ldb * eb % 4 == 0 &&
+           p.strideB * eb % 4 == 0 && 256 * p.lda * eb < lim && 256 * p.ldb * eb < lim && (!dw || p.M >= per) &&
+           ((tb && !dw) || p.N >= per);
+}
 
 // The most tiles a launch can have: each group that has rows ends in a partial tile.
 int64_t most_tiles(const LayerShape &s, const LayerFamily &f)
@@ -63,14 +82,18 @@ bool supports(int k, const LayerShape &s)
 {
     const LayerFamily &f = kLayer[k];
     if (s.M > kMaxTiled || s.N > kMaxTiled || s.K > kMaxTiled) return false;
+    if (f.loads == DIRECT && !s.direct) return false;
+    if (k == K_PIPE_256 && s.type == 0) return false;
     // a launch holds fewer than 2^32 threads
     return most_tiles(s, f) * f.threads < ((int64_t)1 << 32) && most_tiles(s, f) < kMaxDim;
 }
 
 int choose(const LayerShape &s)
 {
-    const int k = most_tiles(s, kLayer[1]) >= 256 ? 1 : 0;
-    return supports(k, s) ? k : supports(1, s) ? 1 : -1;
+    int k = s.direct ? K_PIPE_64 : K_STAGED_64;
+    if (most_tiles(s, kLayer[K_PIPE_128]) >= 256) k = s.direct ? K_PIPE_128 : K_STAGED_128;
+    if (s.direct && s.type != 0 && most_tiles(s, kLayer[K_PIPE_256]) >= 256) k = K_PIPE_256;
+    return supports(k, s) ? k : supports(K_STAGED_128, s) ? K_STAGED_128 : -1;
 }
 
 int resolve_splits(const LayerShape &s, int splits)
@@ -179,7 +202,8 @@ int rows_product(const RowsCall &c, LayerParams &p, F between)
     p.C = c.C;
     p.ldc = c.ldc;
     p.ctype = output_type(c.dtype);
-    const LayerShape s = {p.kind, operand_type(c.dtype), c.transB == DG_OP_T, c.offsets != nullptr, c.groups, c.M, c.N, p.K};
+    const LayerShape s = {p.kind, operand_type(c.dtype), c.transB == DG_OP_T, c.offsets != nullptr, c.groups, c.M, c.N, p.K,
+                          direct_ok(p, operand_type(c.dtype), c.transB == DG_OP_T)};
     return launch(p, s, c.dtype, c.kernel, c.splits, c.workspace, c.workspace_bytes, 25, (hipStream_t)c.stream);
 }
 
@@ -310,7 +334,8 @@ int dg_gemm_dw_with_kernel(int64_t groups, const int32_t *offsets, int64_t rows,
     if (work) {
         LayerParams q = p;
         if (!reads) q.K = 0;
-        const LayerShape s = {p.kind, operand_type(dtype), false, offsets != nullptr, groups, M, N, q.K};
+        const LayerShape s = {p.kind, operand_type(dtype), false, offsets != nullptr, groups, M, N, q.K,
+                              direct_ok(q, operand_type(dtype), false)};
         const int rc = launch(q, s, dtype, kernel, splits, workspace, workspace_bytes, 18, (hipStream_t)stream);
         if (rc != DG_OK) return rc;
     }
@@ -333,7 +358,7 @@ int dg_gemm_fused_choose(int64_t M, int64_t N, int64_t K, dg_op_t transB, dg_dty
     if (transB != DG_OP_N && transB != DG_OP_T) return -4;
     if (!is_dtype(dtype)) return -5;
     if (M == 0 || N == 0) return 1;
-    const LayerShape s = {dg::LAYER_FORWARD, operand_type(dtype), transB == DG_OP_T, false, 1, M, N, K};
+    const LayerShape s = {dg::LAYER_FORWARD, operand_type(dtype), transB == DG_OP_T, false, 1, M, N, K, true};
     return resolve_splits(s, 0);
 }
 
@@ -345,7 +370,7 @@ int dg_gemm_dw_choose(int64_t groups, int64_t rows, int64_t M, int64_t N, dg_dty
     if (N < 0 || N > kMaxDim) return -4;
     if (!is_dtype(dtype)) return -5;
     if (groups == 0 || M == 0 || N == 0) return 1;
-    const LayerShape s = {dg::LAYER_WEIGHTS, operand_type(dtype), false, groups > 1, groups, M, N, rows};
+    const LayerShape s = {dg::LAYER_WEIGHTS, operand_type(dtype), false, groups > 1, groups, M, N, rows, true};
     return resolve_splits(s, 0);
 }
 

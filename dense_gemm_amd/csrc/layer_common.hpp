@@ -34,7 +34,7 @@ struct LayerParams {
     void *keep;
     int64_t ldk;
     void *C;
-    int64_t ldc, strideC;           // strideC: weights, from a group's C to the next
+    int64_t ldc, strideC;           // strideC: weights, from a group's C to the next (else 0)
     int32_t ctype;                  // element of C, R, Z, keep and bias: 0 fp32, 1 fp16, 2 bf16
     int32_t tiles_m, tiles_n, group_m;
     int32_t splits;                 // K ranges, a grid dimension; with more than one the raw sums go to ws
@@ -100,45 +100,45 @@ __device__ __forceinline__ float layer_act_grad(int act, float h, float x)
     return h;
 }
 
-// W consecutive elements of a row as fp32, by 16-byte accesses that need no more
-// than the element's alignment; `n` of them exist (the others are 0 and not read).
+// W consecutive elements of a row as fp32 and back, by 16-byte accesses that need
+// no more than the element's alignment (the GPU takes misaligned vectors).
 template <typename T, int W>
-__device__ __forceinline__ void load_row(const T *x, int n, float (&v)[W])
+__device__ __forceinline__ auto load_raw(const T *x)
 {
     constexpr int PER = (int)(16 / sizeof(T)) < W ? (int)(16 / sizeof(T)) : W;
     typedef T V __attribute__((ext_vector_type(PER)));
     typedef V __attribute__((aligned(sizeof(T)))) Vu;
-    if (n >= W) {
+    typedef T VW __attribute__((ext_vector_type(W)));
+    VW v;
 #pragma unroll
-        for (int c = 0; c < W / PER; ++c) {
-            const V y = *(const Vu *)(x + c * PER);
+    for (int c = 0; c < W / PER; ++c) {
+        const V y = *(const Vu *)(x + c * PER);
 #pragma unroll
-            for (int e = 0; e < PER; ++e) v[c * PER + e] = (float)y[e];
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < W; ++e) v[e] = e < n ? (float)x[e] : 0.f;
+        for (int e = 0; e < PER; ++e) v[c * PER + e] = y[e];
     }
+    return v;
 }
 
 template <typename T, int W>
-__device__ __forceinline__ void store_row(T *x, int n, const float (&v)[W])
+__device__ __forceinline__ void load_row(const T *x, float (&v)[W])
+{
+    const auto y = load_raw<T, W>(x);
+#pragma unroll
+    for (int e = 0; e < W; ++e) v[e] = (float)y[e];
+}
+
+template <typename T, int W>
+__device__ __forceinline__ void store_row(T *x, const float (&v)[W])
 {
     constexpr int PER = (int)(16 / sizeof(T)) < W ? (int)(16 / sizeof(T)) : W;
     typedef T V __attribute__((ext_vector_type(PER)));
     typedef V __attribute__((aligned(sizeof(T)))) Vu;
-    if (n >= W) {
 #pragma unroll
-        for (int c = 0; c < W / PER; ++c) {
-            V y;
+    for (int c = 0; c < W / PER; ++c) {
+        V y;
 #pragma unroll
-            for (int e = 0; e < PER; ++e) y[e] = (T)v[c * PER + e];
-            *(Vu *)(x + c * PER) = y;
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < W; ++e)
-            if (e < n) x[e] = (T)v[e];
+        for (int e = 0; e < PER; ++e) y[e] = (T)v[c * PER + e];
+        *(Vu *)(x + c * PER) = y;
     }
 }
 
@@ -148,83 +148,78 @@ struct LayerTile {
     int rows;            // rows of the group (forward, gradient) or of C (weights)
     int m0, n0;
     int64_t row0;        // first row of the group in the matrices of rows
+    int64_t out0;        // the same for C's rows (weights: 0, a group's C stands by itself)
     int k0, k_len;       // this split's part of the sum
 };
 
-// What a row of C needs beside the sums, fetched ahead of them.
+// What W columns of a row of C need beside the sums, fetched ahead of them and kept
+// in C's type: Z of the gradient, else R.  (A gradient's R is read when it is
+// needed: both ahead take more registers than the largest tile leaves.)
 template <typename TC, int W>
 struct LayerAux {
-    float r[W], z[W];
-    __device__ __forceinline__ void fetch(const LayerParams &p, const LayerTile &t, int row, int col, int n)
+    typedef TC V __attribute__((ext_vector_type(W)));
+    V x;
+    __device__ __forceinline__ static V residual(const LayerParams &p, const LayerTile &t, int row, int col)
     {
-        if (p.kind == LAYER_WEIGHTS) {
-            if (p.R) load_row<TC, W>((const TC *)p.R + t.group * p.strideC + (int64_t)row * p.ldr + col, n, r);
-            return;
-        }
-        if (p.R) load_row<TC, W>((const TC *)p.R + (t.row0 + row) * p.ldr + col, n, r);
-        if (p.kind == LAYER_GRAD) load_row<TC, W>((const TC *)p.Z + (t.row0 + row) * p.ldz + col, n, z);
+        return load_raw<TC, W>((const TC *)p.R + t.group * p.strideC + (t.out0 + row) * p.ldr + col);
+    }
+    __device__ __forceinline__ void fetch(const LayerParams &p, const LayerTile &t, int row, int col)
+    {
+        x = (V)(TC)0.f;
+        if (p.Z) x = load_raw<TC, W>((const TC *)p.Z + (t.out0 + row) * p.ldz + col);
+        else if (p.R) x = residual(p, t, row, col);
     }
 };
 
-// The epilogue of W columns col .. of row `row` (n of them exist): v holds the sums.
+// The epilogue of W columns col .. of row `row`: v holds the sums.
 template <typename TC, int W>
-__device__ __forceinline__ void layer_finish(const LayerParams &p, const LayerTile &t, int row, int col, int n,
+__device__ __forceinline__ void layer_finish(const LayerParams &p, const LayerTile &t, int row, int col,
                                              float (&v)[W], const LayerAux<TC, W> &aux, const float (&bias)[W])
 {
     constexpr bool EXACT = sizeof(TC) == 4;
-    int64_t at;
-    if (p.kind == LAYER_WEIGHTS) {
-        at = t.group * p.strideC + (int64_t)row * p.ldc + col;
+    const int64_t out = t.out0 + row;
 #pragma unroll
-        for (int e = 0; e < W; ++e) v[e] *= p.alpha;
-        if (p.R) {
+    for (int e = 0; e < W; ++e) v[e] = __builtin_fmaf(p.alpha, v[e], bias[e]);
+    if (p.kind == LAYER_GRAD && p.R) {
+        const auto r = LayerAux<TC, W>::residual(p, t, row, col);
 #pragma unroll
-            for (int e = 0; e < W; ++e) v[e] = __builtin_fmaf(p.beta, aux.r[e], v[e]);
-        }
-    } else {
-        const int64_t grow = t.row0 + row;
-        at = grow * p.ldc + col;
-        if (p.kind == LAYER_FORWARD) {
+        for (int e = 0; e < W; ++e) v[e] = __builtin_fmaf(p.beta, (float)r[e], v[e]);
+    }
+    if (p.keep) store_row<TC, W>((TC *)p.keep + out * p.ldk + col, v);
+    if (p.kind == LAYER_GRAD) {
+        if (p.act == ACT_GELU) {
 #pragma unroll
-            for (int e = 0; e < W; ++e) v[e] = __builtin_fmaf(p.alpha, v[e], bias[e]);
-            if (p.keep) store_row<TC, W>((TC *)p.keep + grow * p.ldk + col, n, v);
-            if (p.act == ACT_GELU) {
-#pragma unroll
-                for (int e = 0; e < W; ++e) v[e] = layer_act<EXACT>(ACT_GELU, v[e]);
-            } else if (p.act == ACT_RELU) {
-#pragma unroll
-                for (int e = 0; e < W; ++e) v[e] = layer_act<EXACT>(ACT_RELU, v[e]);
-            }
-            if (p.R) {
-#pragma unroll
-                for (int e = 0; e < W; ++e) v[e] = __builtin_fmaf(p.beta, aux.r[e], v[e]);
+            for (int e = 0; e < W; ++e) {
+                v[e] = layer_act_grad<EXACT>(ACT_GELU, v[e], (float)aux.x[e]);
+                if (EXACT) __builtin_amdgcn_sched_barrier(0);    // erfcf's registers one at a time
             }
         } else {
 #pragma unroll
-            for (int e = 0; e < W; ++e) v[e] *= p.alpha;
-            if (p.R) {
-#pragma unroll
-                for (int e = 0; e < W; ++e) v[e] = __builtin_fmaf(p.beta, aux.r[e], v[e]);
-            }
-            if (p.keep) store_row<TC, W>((TC *)p.keep + grow * p.ldk + col, n, v);
-            if (p.act == ACT_GELU) {
-#pragma unroll
-                for (int e = 0; e < W; ++e) v[e] = layer_act_grad<EXACT>(ACT_GELU, v[e], aux.z[e]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < W; ++e) v[e] = layer_act_grad<EXACT>(ACT_RELU, v[e], aux.z[e]);
-            }
+            for (int e = 0; e < W; ++e) v[e] = layer_act_grad<EXACT>(ACT_RELU, v[e], (float)aux.x[e]);
         }
+    } else if (p.act == ACT_GELU) {
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+            v[e] = layer_act<EXACT>(ACT_GELU, v[e]);
+            if (EXACT) __builtin_amdgcn_sched_barrier(0);
+        }
+    } else if (p.act == ACT_RELU) {
+#pragma unroll
+        for (int e = 0; e < W; ++e) v[e] = layer_act<EXACT>(ACT_RELU, v[e]);
     }
-    store_row<TC, W>((TC *)p.C + at, n, v);
+    if (p.kind != LAYER_GRAD && p.R) {
+#pragma unroll
+        for (int e = 0; e < W; ++e) v[e] = __builtin_fmaf(p.beta, (float)aux.x[e], v[e]);
+    }
+    store_row<TC, W>((TC *)p.C + t.group * p.strideC + out * p.ldc + col, v);
 }
 
 // The bias of W columns of a group.
 template <typename TC, int W>
-__device__ __forceinline__ void layer_bias(const LayerParams &p, int group, int col, int n, float (&b)[W])
+__device__ __forceinline__ void layer_bias(const LayerParams &p, int group, int col, float (&b)[W])
 {
-    if (p.kind == LAYER_FORWARD && p.bias) {
-        load_row<TC, W>((const TC *)p.bias + group * p.stride_bias + col, n > 0 ? n : 0, b);
+    if (p.bias) {
+        load_row<TC, W>((const TC *)p.bias + group * p.stride_bias + col, b);
     } else {
 #pragma unroll
         for (int e = 0; e < W; ++e) b[e] = 0.f;
@@ -233,11 +228,11 @@ __device__ __forceinline__ void layer_bias(const LayerParams &p, int group, int 
 
 // The raw sums of a split's W columns.
 template <int W>
-__device__ __forceinline__ void layer_partial(const LayerParams &p, const LayerTile &t, int row, int col, int n,
+__device__ __forceinline__ void layer_partial(const LayerParams &p, const LayerTile &t, int row, int col,
                                               const float (&v)[W])
 {
     float *w = p.ws + (((int64_t)blockIdx.y * p.groups + t.group) * p.M + row) * p.N + col;
-    store_row<float, W>(w, n, v);
+    store_row<float, W>(w, v);
 }
 
 // First row and rows of group g.  Offsets outside 0 .. total and descending ones
@@ -288,6 +283,7 @@ __device__ __forceinline__ bool layer_tile(const LayerParams &p, int bm, int bn,
         t.m0 = tm * bm;
         t.n0 = tn * bn;
         t.rows = p.M;
+        t.out0 = 0;
         int begin = 0, n = p.K;
         if (p.offsets) group_rows(p, t.group, p.K, begin, n);
         t.row0 = __builtin_amdgcn_readfirstlane(begin);
@@ -302,6 +298,7 @@ __device__ __forceinline__ bool layer_tile(const LayerParams &p, int bm, int bn,
         }
         return true;
     }
+    t.out0 = t.row0;
     t.k0 = 0;
     t.k_len = p.K;
     int tiles_m, first = 0;                     // of the group, and its first tile row
@@ -355,7 +352,7 @@ __device__ __forceinline__ bool layer_tile(const LayerParams &p, int bm, int bn,
         tiles_m = upto - first;
         int begin, n;
         group_rows(p, t.group, p.M, begin, n);
-        t.row0 = __builtin_amdgcn_readfirstlane(begin);
+        t.row0 = t.out0 = __builtin_amdgcn_readfirstlane(begin);
         t.rows = __builtin_amdgcn_readfirstlane(n);
     }
     int tm, tn;

@@ -6,39 +6,52 @@ namespace dg {
 
 namespace {
 
-// The splits' raw sums (ws[split][group][M][N], fp32), added in their order, and the
-// epilogue: 8 columns of a row a thread.
+// The sums of W columns of row `grow` (counted over the groups): the splits' raw sums
+// (ws[split][group][M][N], fp32) added in their order, then the epilogue.
+template <typename TC, int W>
+__device__ __forceinline__ void join(const LayerParams &p, int64_t grow, int col)
+{
+    LayerTile t;
+    t.group = (int)(grow / p.M);
+    t.row0 = t.out0 = 0;
+    const int row = (int)(grow - (int64_t)t.group * p.M);
+    LayerAux<TC, W> aux;
+    aux.fetch(p, t, row, col);
+    float v[W], bias[W];
+#pragma unroll
+    for (int e = 0; e < W; ++e) v[e] = 0.f;
+    const float *w = p.ws + grow * p.N + col;
+    const int64_t mn = (int64_t)p.groups * p.M * p.N;
+    for (int s = 0; s < p.splits; s += 4) {
+        float x[4][W];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (s + u < p.splits) load_row<float, W>(w + (s + u) * mn, x[u]);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (s + u < p.splits)
+#pragma unroll
+                for (int e = 0; e < W; ++e) v[e] += x[u][e];
+    }
+    layer_bias<TC, W>(p, t.group, col, bias);
+    layer_finish<TC, W>(p, t, row, col, v, aux, bias);
+}
+
+// 8 columns of a row a thread; the last columns one by one.
 template <typename TC>
 __global__ __launch_bounds__(256) void layer_join_kernel(LayerParams p)
 {
     const int per_row = (p.N + 7) / 8;
-    const int64_t total = (int64_t)p.groups * p.M * per_row, mn = (int64_t)p.groups * p.M * p.N;
+    const int64_t total = (int64_t)p.groups * p.M * per_row;
     for (int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x; at < total; at += (int64_t)gridDim.x * 256) {
         const int64_t grow = at / per_row;
-        const int col = (int)(at - grow * per_row) * 8, n = p.N - col;
-        LayerTile t;
-        t.group = (int)(grow / p.M);
-        t.row0 = 0;
-        const int row = (int)(grow - (int64_t)t.group * p.M);
-        LayerAux<TC, 8> aux;
-        aux.fetch(p, t, row, col, n);
-        float v[8], bias[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = 0.f;
-        const float *w = p.ws + grow * p.N + col;
-        for (int s = 0; s < p.splits; s += 4) {
-            float x[4][8];
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-                if (s + u < p.splits) load_row<float, 8>(w + (s + u) * mn, n, x[u]);
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-                if (s + u < p.splits)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] += x[u][e];
+        const int col = (int)(at - grow * per_row) * 8;
+        if (col + 8 <= p.N) {
+            join<TC, 8>(p, grow, col);
+        } else {
+#pragma unroll 1
+            for (int c = col; c < p.N; ++c) join<TC, 1>(p, grow, c);
         }
-        layer_bias<TC, 8>(p, t.group, col, n, bias);
-        layer_finish<TC, 8>(p, t, row, col, n, v, aux, bias);
     }
 }
 
@@ -57,15 +70,23 @@ __global__ __launch_bounds__(512) void layer_colsum_kernel(LayerParams p)
     float s[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) s[e] = 0.f;
-    for (int r = lr; r < rows; r += 256) {
-        float v[4][8];
+    if (n >= 8) {
+        for (int r = lr; r < rows; r += 256) {
+            float v[4][8];
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-            load_row<T, 8>(a + (int64_t)(r + 64 * u < rows ? r + 64 * u : r) * p.lda, r + 64 * u < rows ? n : 0, v[u]);
+            for (int u = 0; u < 4; ++u)
+                if (r + 64 * u < rows) load_row<T, 8>(a + (int64_t)(r + 64 * u) * p.lda, v[u]);
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
+            for (int u = 0; u < 4; ++u)
+                if (r + 64 * u < rows)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) s[e] += v[u][e];
+                    for (int e = 0; e < 8; ++e) s[e] += v[u][e];
+        }
+    } else if (n > 0) {
+        for (int r = lr; r < rows; r += 64)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (e < n) s[e] += (float)a[(int64_t)r * p.lda + e];
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) red[lr][lc + e] = s[e];

@@ -33,46 +33,56 @@ bool bad_ptr(const void *p, int64_t align) { return p == nullptr || (uintptr_t)p
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t max1(int64_t x) { return x > 1 ? x : 1; }
 
-enum Loads { STAGED, DIRECT };
+// How a kernel loads its operands.  ANY: the operands that the direct loads do not
+// take through registers (three entries of the kernel tables, A, B or both).
+// ROWS, STREAM: few rows (bn is that of a B stored N x K); STREAM with direct loads.
+enum Loads { ANY, DIRECT, ROWS, STREAM };
 struct LayerFamily {
     const char *name;
+    int config;          // in the kernel tables
     int bm, bn, group_m, threads;
     Loads loads;
 };
 const LayerFamily kLayer[] = {
-    {"layer_64x64_staged", 64, 64, 4, 256, STAGED},
-    {"layer_128x128_staged", 128, 128, 4, 256, STAGED},
-    {"layer_64x64_pipe", 64, 64, 4, 256, DIRECT},
-    {"layer_128x128_pipe", 128, 128, 4, 256, DIRECT},
-    {"layer_256x256_pipe", 256, 256, 4, 512, DIRECT},
+    {"layer_64x64_any", 0, 64, 64, 4, 256, ANY},
+    {"layer_128x128_any", 3, 128, 128, 4, 256, ANY},
+    {"layer_64x64_pipe", 6, 64, 64, 4, 256, DIRECT},
+    {"layer_128x128_pipe", 7, 128, 128, 4, 256, DIRECT},
+    {"layer_256x256_pipe", 8, 256, 256, 4, 512, DIRECT},
+    {"layer_256x128_pipe", 9, 256, 128, 4, 256, DIRECT},
+    {"layer_256x256_k32_pipe", 10, 256, 256, 4, 512, DIRECT},
+    {"layer_16_rows", 11, 16, 16, 1, 512, ROWS},
+    {"layer_32_rows", 12, 32, 16, 1, 512, ROWS},
+    {"layer_16_rows_stream", 13, 16, 16, 1, 512, STREAM},
+    {"layer_32_rows_stream", 14, 32, 16, 1, 512, STREAM},
+    {"layer_16_rows_stream_w16", 15, 16, 16, 1, 1024, STREAM},
+    {"layer_32_rows_stream_w16", 16, 32, 16, 1, 1024, STREAM},
 };
 constexpr int kNumLayer = sizeof(kLayer) / sizeof(kLayer[0]);
-enum { K_STAGED_64, K_STAGED_128, K_PIPE_64, K_PIPE_128, K_PIPE_256 };
+enum { K_ANY_64, K_ANY_128, K_PIPE_64, K_PIPE_128, K_PIPE_256 };
 
 // What the choice of a kernel looks at.
 struct LayerShape {
     int kind, type;
     bool tb, ragged;
     int64_t groups, M, N, K;      // as LayerParams
-    bool direct;                  // the direct loads take the operands
+    bool direct_a, direct_b;      // the direct loads take the operand
+    bool direct() const { return direct_a && direct_b; }
 };
 
 // The direct loads' 16-byte pieces lie at whole multiples of 16 bytes from a row's
-// start, which has to be 4-byte aligned; 256 rows lie within 32-bit byte
-// offsets; and a row that runs across the summed index is at least a piece long.
-bool direct_ok(const LayerParams &p, int type, bool tb)
+// start, which has to be 4-byte aligned, and 256 rows lie within 32-bit byte offsets.
+bool direct_ok(const void *x, int64_t ld, int64_t stride, int64_t bytes)
 {
-    const int64_t eb = bytes_of(type), per = 16 / eb, lim = (int64_t)1 << 31;
-    const bool dw = p.kind == dg::LAYER_WEIGHTS;
-    return ((uintptr_t)p.A & 3) == 0 && ((uintptr_t)p.B & 3) == 0 && p.lda * eb % 4 == 0 && p.ldb * eb % 4 == 0 &&
-           p.strideB * eb % 4 == 0 && 256 * p.lda * eb < lim && 256 * p.ldb * eb < lim && (!dw || p.M >= per) &&
-           ((tb && !dw) || p.N >= per);
+    return ((uintptr_t)x & 3) == 0 && ld * bytes % 4 == 0 && stride * bytes % 4 == 0 && 256 * ld * bytes < ((int64_t)1 << 31);
 }
+
+int bn_of(const LayerFamily &f, const LayerShape &s) { return f.loads == ROWS && !s.tb ? 64 : f.bn; }
 
 // The most tiles a launch can have: each group that has rows ends in a partial tile.
 int64_t most_tiles(const LayerShape &s, const LayerFamily &f)
 {
-    const int64_t tn = ceil_div(s.N, f.bn);
+    const int64_t tn = ceil_div(s.N, bn_of(f, s));
     if (s.kind == dg::LAYER_WEIGHTS) return s.groups * ceil_div(s.M, f.bm) * tn;
     const int64_t used = s.ragged && s.groups < s.M ? s.groups : s.ragged ? s.M : 1;
     return (s.M + used * (f.bm - 1)) / f.bm * tn;
@@ -82,18 +92,21 @@ bool supports(int k, const LayerShape &s)
 {
     const LayerFamily &f = kLayer[k];
     if (s.M > kMaxTiled || s.N > kMaxTiled || s.K > kMaxTiled) return false;
-    if (f.loads == DIRECT && !s.direct) return false;
-    if (k == K_PIPE_256 && s.type == 0) return false;
+    if ((f.loads == DIRECT || f.loads == STREAM) && !s.direct()) return false;
+    if (f.loads == STREAM && (s.kind == dg::LAYER_WEIGHTS || !s.tb)) return false;
+    if (k >= K_PIPE_256 && f.loads == DIRECT && s.type == 0) return false;
+    // the row kernels' columns of a B stored K x N go four together
+    if (f.loads == ROWS && (s.kind == dg::LAYER_WEIGHTS || (!s.tb && s.N < 4))) return false;
     // a launch holds fewer than 2^32 threads
     return most_tiles(s, f) * f.threads < ((int64_t)1 << 32) && most_tiles(s, f) < kMaxDim;
 }
 
 int choose(const LayerShape &s)
 {
-    int k = s.direct ? K_PIPE_64 : K_STAGED_64;
-    if (most_tiles(s, kLayer[K_PIPE_128]) >= 256) k = s.direct ? K_PIPE_128 : K_STAGED_128;
-    if (s.direct && s.type != 0 && most_tiles(s, kLayer[K_PIPE_256]) >= 256) k = K_PIPE_256;
-    return supports(k, s) ? k : supports(K_STAGED_128, s) ? K_STAGED_128 : -1;
+    int k = s.direct() ? K_PIPE_64 : K_ANY_64;
+    if (most_tiles(s, kLayer[K_PIPE_128]) >= 256) k = s.direct() ? K_PIPE_128 : K_ANY_128;
+    if (s.direct() && s.type != 0 && most_tiles(s, kLayer[K_PIPE_256]) >= 256) k = K_PIPE_256;
+    return supports(k, s) ? k : supports(K_ANY_128, s) ? K_ANY_128 : -1;
 }
 
 int resolve_splits(const LayerShape &s, int splits)
@@ -121,11 +134,13 @@ int launch(LayerParams &p, const LayerShape &s, int dtype, int kernel, int split
         if (ws_bytes < workspace_bytes_of(p.groups, p.M, p.N, p.splits)) return -(ws_arg + 1);
     }
     p.tiles_m = (int32_t)ceil_div(p.M, f.bm);
-    p.tiles_n = (int32_t)ceil_div(p.N, f.bn);
+    p.tiles_n = (int32_t)ceil_div(p.N, bn_of(f, s));
     p.group_m = f.group_m;
     const int type = operand_type(dtype), variant = s.kind == dg::LAYER_WEIGHTS ? 2 : s.tb;
-    const void *k = type == 0 ? dg::layer_kernel_f32(kernel, variant)
-                              : type == 1 ? dg::layer_kernel_f16(kernel, variant) : dg::layer_kernel_bf16(kernel, variant);
+    // (an ANY kernel forced on operands that both could load directly takes both through registers)
+    const int config = f.config + (f.loads != ANY || (!s.direct_a && s.direct_b) ? 0 : s.direct_a && !s.direct_b ? 1 : 2);
+    const void *k = type == 0 ? dg::layer_kernel_f32(config, variant)
+                              : type == 1 ? dg::layer_kernel_f16(config, variant) : dg::layer_kernel_bf16(config, variant);
     LayerParams arg = p;
     void *args[] = {&arg};
     hipError_t err = hipLaunchKernel(k, dim3((unsigned)most_tiles(s, f), (unsigned)p.splits), dim3((unsigned)f.threads), args,
@@ -203,7 +218,7 @@ int rows_product(const RowsCall &c, LayerParams &p, F between)
     p.ldc = c.ldc;
     p.ctype = output_type(c.dtype);
     const LayerShape s = {p.kind, operand_type(c.dtype), c.transB == DG_OP_T, c.offsets != nullptr, c.groups, c.M, c.N, p.K,
-                          direct_ok(p, operand_type(c.dtype), c.transB == DG_OP_T)};
+                          direct_ok(c.A, c.lda, 0, eb), direct_ok(c.B, c.ldb, c.strideB, eb)};
     return launch(p, s, c.dtype, c.kernel, c.splits, c.workspace, c.workspace_bytes, 25, (hipStream_t)c.stream);
 }
 
@@ -335,7 +350,7 @@ int dg_gemm_dw_with_kernel(int64_t groups, const int32_t *offsets, int64_t rows,
         LayerParams q = p;
         if (!reads) q.K = 0;
         const LayerShape s = {p.kind, operand_type(dtype), false, offsets != nullptr, groups, M, N, q.K,
-                              direct_ok(q, operand_type(dtype), false)};
+                              direct_ok(A, lda, 0, eb), direct_ok(B, ldb, 0, eb)};
         const int rc = launch(q, s, dtype, kernel, splits, workspace, workspace_bytes, 18, (hipStream_t)stream);
         if (rc != DG_OK) return rc;
     }
@@ -358,7 +373,7 @@ int dg_gemm_fused_choose(int64_t M, int64_t N, int64_t K, dg_op_t transB, dg_dty
     if (transB != DG_OP_N && transB != DG_OP_T) return -4;
     if (!is_dtype(dtype)) return -5;
     if (M == 0 || N == 0) return 1;
-    const LayerShape s = {dg::LAYER_FORWARD, operand_type(dtype), transB == DG_OP_T, false, 1, M, N, K, true};
+    const LayerShape s = {dg::LAYER_FORWARD, operand_type(dtype), transB == DG_OP_T, false, 1, M, N, K, true, true};
     return resolve_splits(s, 0);
 }
 
@@ -370,7 +385,7 @@ int dg_gemm_dw_choose(int64_t groups, int64_t rows, int64_t M, int64_t N, dg_dty
     if (N < 0 || N > kMaxDim) return -4;
     if (!is_dtype(dtype)) return -5;
     if (groups == 0 || M == 0 || N == 0) return 1;
-    const LayerShape s = {dg::LAYER_WEIGHTS, operand_type(dtype), false, groups > 1, groups, M, N, rows, true};
+    const LayerShape s = {dg::LAYER_WEIGHTS, operand_type(dtype), false, groups > 1, groups, M, N, rows, true, true};
     return resolve_splits(s, 0);
 }
 

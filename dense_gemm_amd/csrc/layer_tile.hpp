@@ -8,13 +8,10 @@
 // the end are fetched from valid places and never stored, summed indices past the
 // end are zero.
 //
-// layer_staged_kernel  any strides and alignment: operands through registers;
-// layer_pipe_kernel    4-byte aligned rows: a ring of slabs in LDS filled by direct loads.
 #pragma once
 
 #include <type_traits>
 
-#include "gemm_mfma.hpp"
 #include "gemm_pipe.hpp"
 #include "layer_common.hpp"
 
@@ -120,213 +117,153 @@ __device__ __forceinline__ void layer_store(const LayerParams &p, const LayerTil
     else layer_store_as<float>(p, t, stg, acc, row0, col0, lane, false);
 }
 
-// ---- any strides and alignment ----------------------------------------------------
-// Operands go through registers into a double-buffered LDS slab, in 16-byte loads
-// that need only the element's alignment (the GPU takes misaligned vectors).
-template <typename T, int BMN, int BK, bool KCONT>
-struct StagedOperand : Operand<T, BMN, BK, KCONT, true> {
-    typedef Operand<T, BMN, BK, KCONT, true> Base;
-    typedef typename Base::vec vec;
-    typedef vec __attribute__((aligned(sizeof(T)))) vecu;
-    static constexpr int V = Base::V;
+// ---- operands -------------------------------------------------------------------------
+// A 16-bit operand's slab of BK summed indices in LDS, as PipeOperandH lays it out (for
+// a BK of its own).  KCONT (rows of BK): the 16-byte chunk c of row r sits at chunk c
+// ^ swz(r), so that the 16 rows which a quarter wave reads together hit 16 distinct bank
+// groups.  Else (BK rows of BMN): the 64-byte quad q of row k sits at q ^ swz(k), and
+// fragments come from the transposing read.
+template <typename T, int BMN, bool KCONT, int NW, int BK_>
+struct SlabOperandH {
+    typedef T V8 __attribute__((ext_vector_type(8)));
+    typedef __attribute__((address_space(3))) V8 lds_v8_t;
+    static constexpr int BK = BK_, BYTES = BMN * BK * 2, SPAN = 1024, LOADS = BYTES / (NW * SPAN);
+    static constexpr int ROW_BYTES = KCONT ? BK * 2 : BMN * 2;
+    static_assert(BK == 32 || BK == 64, "slabs of 32 or 64");
+    static_assert(LOADS * NW * SPAN == BYTES, "whole loads");
+    static_assert(KCONT || BMN == 64 || BMN % 128 == 0, "two quads, or four and more");
 
-    __device__ __forceinline__ static vec load_piece(const T *p, int valid)
+    const char *base;            // the current slab's tile origin (wave-uniform)
+    uint32_t off[LOADS];         // a lane's byte offsets from it
+    int64_t step;                // bytes from a slab to the next
+
+    __device__ static __forceinline__ int swz(int r)
     {
-        vec v;
-        if (valid >= V) {
-            v = *(const vecu *)p;
-        } else {
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                T x = (T)0.f;
-                if (e < valid) x = p[e];
-                v[e] = x;
-            }
-        }
-        return v;
+        if constexpr (KCONT) return BK == 64 ? (r >> 1) & 7 : (r >> 2) & 3;
+        else return BMN == 64 ? (r >> 1) & 1 : r & 3;
     }
-
-    // the slab at (mn0, k0) of a matrix of ext rows (or columns) and K summed indices
-    __device__ __forceinline__ void load(const T *g, int64_t ld, int mn0, int k0, int ext, int K, int tid)
+    // row and first column of the piece at byte b of a stage
+    __device__ static __forceinline__ void place(int b, int &r, int &c)
+    {
+        r = b / ROW_BYTES;
+        const int p = (b % ROW_BYTES) >> 4;
+        c = KCONT ? (p ^ swz(r)) * 8 : (((p >> 2) ^ swz(r)) << 5) + (p & 3) * 8;
+    }
+    __device__ __forceinline__ void advance() { base += step; }
+    __device__ __forceinline__ void issue_one(lds_char_t *lds, int wave, int i)
+    {
+        load_lds16(off[i], buffer_rsrc(base), (unsigned)(uintptr_t)(lds + (i * NW + wave) * SPAN));
+    }
+    // the operand of 32 rows from b0 on, for step kk of 16 summed indices
+    __device__ __forceinline__ V8 frag(const lds_char_t *lds, int b0, int kk, int lane) const
     {
         if constexpr (KCONT) {
-            const int rr = tid / Base::LPR, c = (tid % Base::LPR) * V;
-#pragma unroll
-            for (int q = 0; q < Base::NV; ++q) {
-                const int mn = mn0 + q * Base::RPP + rr, k = k0 + c;
-                this->r[q] = load_piece(g + (int64_t)mn * ld + k, mn < ext ? K - k : 0);
-            }
+            const int r = b0 + (lane & 31);
+            return *(const lds_v8_t *)(lds + r * ROW_BYTES + (((2 * kk + (lane >> 5)) ^ swz(r)) << 4));
         } else {
-            // consecutive k rows per thread where the store transposes them (16 bits)
-            const int kg = tid / Base::LPK, c = (tid % Base::LPK) * V;
-#pragma unroll
-            for (int q = 0; q < Base::NV; ++q) {
-                const int k = k0 + (Base::F16 ? kg * Base::KV + q : q * Base::KG + kg), mn = mn0 + c;
-                this->r[q] = load_piece(g + (int64_t)k * ld + mn, k < K ? ext - mn : 0);
-            }
+            const int g = lane >> 4, t = (lane & 15) >> 2, s = lane & 3;
+            const int colb = (16 * (g & 1) + 4 * s) * 2, k0 = 16 * kk + 8 * (g >> 1) + t;
+            const lds_char_t *p0 = lds + k0 * ROW_BYTES + (((b0 >> 5) ^ swz(k0)) << 6) + colb;
+            const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t *)p0);
+            const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t *)(p0 + 4 * ROW_BYTES));
+            typedef short i16x8 __attribute__((ext_vector_type(8)));
+            const i16x8 v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+            return __builtin_bit_cast(V8, v);
         }
     }
 };
 
-template <typename T, int BM, int BN, int BK, int WM, int WN, bool DW, bool TB, int MINW>
-__global__ __launch_bounds__(256, MINW) void layer_staged_kernel(LayerParams p)
-{
-    constexpr int WAVES_N = BN / WN, TM = WM / 32, TN = WN / 32;
-    static_assert((BM / WM) * WAVES_N == 4, "4 waves per workgroup");
-    typedef StagedOperand<T, BM, BK, !DW> OpA;
-    typedef StagedOperand<T, BN, BK, TB && !DW> OpB;
-    constexpr int STAGE = OpA::ELEMS + OpB::ELEMS;
-    constexpr int RING = 2 * STAGE * (int)sizeof(T), STRIPS = 4 * kStripBytes<WN>;
-    __shared__ __attribute__((aligned(16))) char smem_raw[RING > STRIPS ? RING : STRIPS];
-    T *smem = (T *)smem_raw;
-
-    LayerTile t;
-    if (!layer_tile(p, BM, BN, t)) return;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int wm0 = (wave / WAVES_N) * WM, wn0 = (wave % WAVES_N) * WN;
-    const T *A = (const T *)p.A + (DW ? (t.row0 + t.k0) * p.lda : t.row0 * p.lda + t.k0);
-    const T *B = (const T *)p.B + (DW ? (t.row0 + t.k0) * p.ldb
-                                      : t.group * p.strideB + (TB ? (int64_t)t.k0 : t.k0 * p.ldb));
-    const int K = t.k_len, nk = (K + BK - 1) / BK;
-
-    f32x16 acc[TM][TN];
-#pragma unroll
-    for (int i = 0; i < TM; ++i)
-#pragma unroll
-        for (int j = 0; j < TN; ++j)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
-
-    OpA ga;
-    OpB gb;
-    if (nk > 0) {
-        ga.load(A, p.lda, t.m0, 0, t.rows, K, tid);
-        gb.load(B, p.ldb, t.n0, 0, p.N, K, tid);
-        ga.store(smem, tid);
-        gb.store(smem + OpA::ELEMS, tid);
-    }
-    __syncthreads();
-    const int lrow = lane & 31, khalf = (lane >> 5) * (BK / 2);
-    for (int kt = 0; kt < nk; ++kt) {
-        const T *sA = smem + (kt & 1) * STAGE;
-        const T *sB = sA + OpA::ELEMS;
-        const bool more = kt + 1 < nk;
-        if (more) {
-            ga.load(A, p.lda, t.m0, (kt + 1) * BK, t.rows, K, tid);
-            gb.load(B, p.ldb, t.n0, (kt + 1) * BK, p.N, K, tid);
-        }
-        if constexpr (sizeof(T) == 4) {
-            // 32x32x2 steps, four at a time; lane half h takes k of the slab's half h
-#pragma unroll
-            for (int c = 0; c < BK / 8; ++c) {
-                float a[TM][4], b[TN][4];
-#pragma unroll
-                for (int i = 0; i < TM; ++i)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        a[i][e] = OpA::LDS_KMAJOR ? sA[(wm0 + 32 * i + lrow) * OpA::LD + khalf + 4 * c + e]
-                                                  : sA[(khalf + 4 * c + e) * OpA::LD + wm0 + 32 * i + lrow];
-#pragma unroll
-                for (int j = 0; j < TN; ++j)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        b[j][e] = OpB::LDS_KMAJOR ? sB[(wn0 + 32 * j + lrow) * OpB::LD + khalf + 4 * c + e]
-                                                  : sB[(khalf + 4 * c + e) * OpB::LD + wn0 + 32 * j + lrow];
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-#pragma unroll
-                    for (int i = 0; i < TM; ++i)
-#pragma unroll
-                        for (int j = 0; j < TN; ++j)
-                            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(a[i][e], b[j][e], acc[i][j], 0, 0, 0);
-            }
-        } else {
-            // 32x32x16 steps, 8 k a lane
-            typedef typename ElemTraits<T>::vec v8;
-#pragma unroll
-            for (int c = 0; c < BK / 16; ++c) {
-                v8 a[TM], b[TN];
-#pragma unroll
-                for (int i = 0; i < TM; ++i) a[i] = *(const v8 *)(sA + (wm0 + 32 * i + lrow) * OpA::LD + khalf + 8 * c);
-#pragma unroll
-                for (int j = 0; j < TN; ++j) b[j] = *(const v8 *)(sB + (wn0 + 32 * j + lrow) * OpB::LD + khalf + 8 * c);
-#pragma unroll
-                for (int i = 0; i < TM; ++i)
-#pragma unroll
-                    for (int j = 0; j < TN; ++j) acc[i][j] = mfma_32x32x16(a[i], b[j], acc[i][j]);
-            }
-        }
-        if (more) {
-            T *s = smem + ((kt + 1) & 1) * STAGE;
-            ga.store(s, tid);
-            gb.store(s + OpA::ELEMS, tid);
-        }
-        __syncthreads();
-    }
-    lds_char_t *stg = (lds_char_t *)smem_raw + wave * kStripBytes<WN>;
-    layer_store<T>(p, t, stg, acc, t.m0 + wm0, t.n0 + wn0, lane);
-}
-
-
-// ---- 4-byte aligned rows -------------------------------------------------------------
-// The operands of the direct loads (gemm_pipe.hpp), for any extents: a piece of a
-// row that is no whole number of pieces long reaches past the row's end, into the
-// next row (rows are at least a piece long), and the last slab, which has no next
-// row, goes through registers element by element (`tail`), as does a last slab of
-// fewer summed indices than a slab has.  What lies past a row's end only feeds
-// outputs that are never stored.
-template <typename T, int BMN, bool KCONT, int NW, int BKS>
-struct LayerOperand : std::conditional<sizeof(T) == 2, PipeOperandH<T, BMN, KCONT, NW, 16>,
-                                       PipeOperandS<BMN, KCONT, NW, 16, BKS>>::type {
-    typedef typename std::conditional<sizeof(T) == 2, PipeOperandH<T, BMN, KCONT, NW, 16>,
-                                      PipeOperandS<BMN, KCONT, NW, 16, BKS>>::type Base;
-    static constexpr bool H = sizeof(T) == 2;
-    static constexpr int PER = 16 / (int)sizeof(T);       // elements of a piece, which a lane loads
-
-    // Row (KCONT) or summed index, and first column, of the piece at byte b of a stage.
+// An fp32 operand's (PipeOperandS).
+template <int BMN, bool KCONT, int NW, int BK_>
+struct SlabOperandS : PipeOperandS<BMN, KCONT, NW, 16, BK_> {
+    typedef PipeOperandS<BMN, KCONT, NW, 16, BK_> Base;
     __device__ static __forceinline__ void place(int b, int &r, int &c)
     {
         r = b / Base::ROW_BYTES;
         const int p = (b % Base::ROW_BYTES) >> 4;
-        if constexpr (H) {
-            c = KCONT ? (p ^ ((r >> 1) & 7)) * 8 : (((p >> 2) ^ Base::swz(r)) << 5) + (p & 3) * 8;
-        } else if constexpr (KCONT) {
+        if constexpr (KCONT) {
             c = (p ^ Base::swz(r)) * 4;
         } else {
             r = Base::krow(r);
             c = (((p >> 3) ^ Base::hsw(r)) << 5) + (p & 7) * 4;
         }
     }
+};
+
+// An operand of any extents.  A piece of a row that is no whole number of pieces long
+// reaches past the row's end, into the next row; the last slab, which has no next row,
+// goes element by element (`tail`), as does a last slab of fewer summed indices than a
+// slab has, and every slab of rows shorter than a piece.  What lies past a row's end
+// only feeds outputs that are never stored.
+//   REG = false: direct loads into LDS, of rows that are 4-byte aligned, 256 of which
+//     lie within 32-bit byte offsets.
+//   REG = true: any strides and alignment, through registers: fetch() loads a slab
+//     (the GPU takes misaligned vectors), commit() writes it to its stage.
+template <typename T, int BMN, bool KCONT, int NW, int BK_, bool REG>
+struct LayerOperand : std::conditional<sizeof(T) == 2, SlabOperandH<T, BMN, KCONT, NW, BK_>,
+                                       SlabOperandS<BMN, KCONT, NW, BK_>>::type {
+    typedef typename std::conditional<sizeof(T) == 2, SlabOperandH<T, BMN, KCONT, NW, BK_>,
+                                      SlabOperandS<BMN, KCONT, NW, BK_>>::type Base;
+    static constexpr int PER = 16 / (int)sizeof(T);       // elements of a piece, which a lane loads
+    typedef T V __attribute__((ext_vector_type(PER)));
+    typedef V __attribute__((aligned(sizeof(T)))) Vu;
+    typedef __attribute__((address_space(3))) V lds_v_t;
+    int64_t row_step;                                     // bytes from a stored row to the next
+    int64_t far[REG ? Base::LOADS : 1];
+    V held[REG ? Base::LOADS : 1];
 
     __device__ __forceinline__ void init(const T *g, int64_t ld, int mn0, int ext, int wave, int lane)
     {
         this->base = (const char *)(KCONT ? g + (int64_t)mn0 * ld : g + mn0);
+        row_step = ld * (int)sizeof(T);
 #pragma unroll
         for (int i = 0; i < Base::LOADS; ++i) {
             int r, c;
-            place((i * NW + wave) * Base::SPAN + lane * 16, r, c);
+            Base::place((i * NW + wave) * Base::SPAN + lane * 16, r, c);
             if constexpr (KCONT) {
                 if (mn0 + r >= ext) r = ext - 1 - mn0;
             } else {
                 if (mn0 + c >= ext) c = ((ext - 1) / PER) * PER - mn0;
             }
-            this->off[i] = (uint32_t)(((int64_t)r * ld + c) * (int)sizeof(T));
+            const int64_t at = ((int64_t)r * ld + c) * (int)sizeof(T);
+            if constexpr (REG) far[i] = at;
+            else this->off[i] = (uint32_t)at;
         }
         this->step = (KCONT ? Base::BK : Base::BK * ld) * (int)sizeof(T);
     }
 
-    // the last slab, with krem summed indices left
+    // the last slab is not whole, or not made of whole pieces
+    __device__ static __forceinline__ bool ragged(int krem, int ext) { return krem < Base::BK || (!KCONT && ext % PER != 0); }
+    __device__ static __forceinline__ bool narrow(int ext) { return !KCONT && ext < PER; }
+
+    __device__ __forceinline__ void issue(lds_char_t *lds, int wave)
+    {
+        static_assert(!REG, "direct loads");
+#pragma unroll
+        for (int i = 0; i < Base::LOADS; ++i) this->issue_one(lds, wave, i);
+        this->advance();
+    }
+    __device__ __forceinline__ void fetch()
+    {
+        static_assert(REG, "loads into registers");
+#pragma unroll
+        for (int i = 0; i < Base::LOADS; ++i) held[i] = *(const Vu *)(this->base + far[i]);
+        this->advance();
+    }
+    __device__ __forceinline__ void commit(lds_char_t *lds, int wave, int lane) const
+    {
+#pragma unroll
+        for (int i = 0; i < Base::LOADS; ++i) *(lds_v_t *)(lds + (i * NW + wave) * Base::SPAN + lane * 16) = held[i];
+    }
+
+    // a slab with krem summed indices left, straight to its stage
     __device__ __forceinline__ void tail(lds_char_t *lds, int wave, int lane, int krem, int mn0, int ext)
     {
-        typedef T V __attribute__((ext_vector_type(PER)));
-        typedef V __attribute__((aligned(sizeof(T)))) Vu;
-        typedef __attribute__((address_space(3))) V lds_v_t;
 #pragma unroll 1
         for (int i = 0; i < Base::LOADS; ++i) {
             const int b = (i * NW + wave) * Base::SPAN + lane * 16;
-            int r, c;
-            place(b, r, c);
-            int valid;
+            int r, c, valid;
+            Base::place(b, r, c);
             if constexpr (KCONT) {
                 valid = mn0 + r < ext ? krem - c : 0;
             } else {
@@ -344,30 +281,33 @@ struct LayerOperand : std::conditional<sizeof(T) == 2, PipeOperandH<T, BMN, KCON
         }
         this->advance();
     }
-
-    int64_t row_step;                                     // bytes from a stored row to the next
 };
 
 // BM x BN tile, waves of WM x WN, a ring of STAGES slabs of BK summed indices.
 //
-// 16 bits (slabs of 64): fragments are double-buffered per step of 16 k.  The
-// barrier of a slab sits before its last step, which runs from registers while the
-// next slab's first fragments are read and the slab STAGES ahead is loaded into the
-// stage just finished (A's loads there, B's during the following step), so that
-// no fragment read waits at a barrier and loads and reads lie between MFMAs.
-// fp32 (slabs of BKS): one barrier at a slab's start, the loads of slab kt + STAGES -
-// 1 spread over its MFMAs.
-template <typename T, int BM, int BN, int WM, int WN, bool DW, bool TB, int STAGES, int BKS>
+// 16 bits: fragments are double-buffered per step of 16 k.  The barrier of a slab sits
+// before its last step, which runs from registers while the next slab's first
+// fragments are read and the slab STAGES ahead is loaded into the stage just finished
+// (A's loads there, B's during the following step), so that no fragment read waits at
+// a barrier and loads and reads lie between MFMAs.  An operand through registers
+// (RA, RB; two stages) is fetched in a slab's last step and written to its stage before
+// the next slab's barrier.
+// fp32: one barrier at a slab's start, the loads of slab kt + STAGES - 1 spread over its
+// MFMAs (or fetched before them and written after them).
+template <typename T, int BM, int BN, int WM, int WN, bool DW, bool TB, int STAGES, int BK, bool RA, bool RB>
 __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), 2) void layer_pipe_kernel(LayerParams p)
 {
     constexpr bool H = sizeof(T) == 2;
     constexpr int WAVES_N = BN / WN, NW = (BM / WM) * WAVES_N, TM = WM / 32, TN = WN / 32, NM = TM * TN;
-    typedef LayerOperand<T, BM, !DW, NW, BKS> OpA;
-    typedef LayerOperand<T, BN, TB && !DW, NW, BKS> OpB;
-    constexpr int BK = OpA::BK, LOADS = OpA::LOADS + OpB::LOADS, STAGE = OpA::BYTES + OpB::BYTES;
+    typedef LayerOperand<T, BM, !DW, NW, BK, RA> OpA;
+    typedef LayerOperand<T, BN, TB && !DW, NW, BK, RB> OpB;
+    static_assert(!(RA || RB) || STAGES == 2, "an operand through registers: two stages");
+    // direct loads of a slab, by operand
+    constexpr int LA = RA ? 0 : OpA::LOADS, LBN = RB ? 0 : OpB::LOADS, LOADS = LA + LBN, STAGE = OpA::BYTES + OpB::BYTES;
+    constexpr int PA = LA ? LA : 1, PB = LBN ? LBN : 1, PL = LOADS ? LOADS : 1;     // divisors
     constexpr int RING = STAGES * STAGE, STRIPS = NW * kStripBytes<WN>;
     static_assert((RING > STRIPS ? RING : STRIPS) <= 160 * 1024, "the ring and the strips fit the LDS");
-    static_assert((STAGES - 2) * LOADS + OpA::LOADS < 64, "the loads in flight can be counted");
+    static_assert((STAGES - 2) * LOADS + LA < 64, "the loads in flight can be counted");
     __shared__ __attribute__((aligned(1024))) char smem_raw[RING > STRIPS ? RING : STRIPS];
     lds_char_t *smem = (lds_char_t *)smem_raw;
 
@@ -380,19 +320,17 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), 2) void layer_pipe_kern
     const T *B = (const T *)p.B + (DW ? (t.row0 + t.k0) * p.ldb
                                       : t.group * p.strideB + (TB ? (int64_t)t.k0 : t.k0 * p.ldb));
     const int nk = (t.k_len + BK - 1) / BK, krem = t.k_len - (nk - 1) * BK;
-    // the last slab through registers: it ends early, or its rows in part of a piece
-    const bool tail = krem < BK || (DW && t.rows % OpA::PER != 0) || (!(TB && !DW) && p.N % OpB::PER != 0);
-    const int nfull = tail ? nk - 1 : nk;
+    int nfull = OpA::ragged(krem, t.rows) || OpB::ragged(krem, p.N) ? nk - 1 : nk;
+    if (OpA::narrow(t.rows) || OpB::narrow(p.N)) nfull = 0;
 
     OpA ga;
     OpB gb;
     ga.init(A, p.lda, t.m0, t.rows, wave, lane);
     gb.init(B, p.ldb, t.n0, p.N, wave, lane);
-    ga.row_step = p.lda * (int)sizeof(T);
-    gb.row_step = p.ldb * (int)sizeof(T);
-    auto slab_tail = [&](lds_char_t *st) {
-        ga.tail(st, wave, lane, krem, t.m0, t.rows);
-        gb.tail(st + OpA::BYTES, wave, lane, krem, t.n0, p.N);
+    auto slab_tail = [&](lds_char_t *st, int slab) {
+        const int left = slab == nk - 1 ? krem : BK;
+        ga.tail(st, wave, lane, left, t.m0, t.rows);
+        gb.tail(st + OpA::BYTES, wave, lane, left, t.n0, p.N);
     };
 
     f32x16 acc[TM][TN];
@@ -409,18 +347,29 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), 2) void layer_pipe_kern
         V8 fa[2][TM], fb[2][TN];
         auto read_a = [&](const lds_char_t *st, int i, int s) { return ga.frag(st, wm0 + 32 * i, s, lane); };
         auto read_b = [&](const lds_char_t *st, int j, int s) { return gb.frag(st + OpA::BYTES, wn0 + 32 * j, s, lane); };
-        // the ring, but for B of its last stage, which the first step loads
+        // the ring, but for B of its last stage, which the first step loads (and
+        // for an operand through registers, which holds its second slab)
 #pragma unroll
         for (int s = 0; s < STAGES; ++s) {
             lds_char_t *st = smem + s * STAGE;
             if (s < nfull) {
-                ga.issue(st, wave);
-                if (s < STAGES - 1) gb.issue(st + OpA::BYTES, wave);
+                if constexpr (RA) {
+                    ga.fetch();
+                    if (s == 0) ga.commit(st, wave, lane);
+                } else {
+                    ga.issue(st, wave);
+                }
+                if constexpr (RB) {
+                    gb.fetch();
+                    if (s == 0) gb.commit(st + OpA::BYTES, wave, lane);
+                } else {
+                    if (s < STAGES - 1) gb.issue(st + OpA::BYTES, wave);
+                }
             } else if (s < nk) {
-                slab_tail(st);
+                slab_tail(st, s);
             }
         }
-        if (nfull >= STAGES) wait_vmcnt<(STAGES - 2) * LOADS + OpA::LOADS>();
+        if (!(RA || RB) && nfull >= STAGES) wait_vmcnt<(STAGES - 2) * LOADS + LA>();
         else wait_vmcnt<0>();
         __syncthreads();
 #pragma unroll
@@ -445,8 +394,8 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), 2) void layer_pipe_kern
                         const int m = i * TN + j;
                         if (s == 0) {
 #pragma unroll
-                            for (int l = 0; l < OpB::LOADS; ++l)
-                                if (l * NM / OpB::LOADS == m && pend) gb.issue_one(prev + OpA::BYTES, wave, l);
+                            for (int l = 0; l < LBN; ++l)
+                                if (l * NM / PB == m && pend) gb.issue_one(prev + OpA::BYTES, wave, l);
                         }
 #pragma unroll
                         for (int f = 0; f < TM + TN; ++f)
@@ -457,7 +406,13 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), 2) void layer_pipe_kern
                         acc[i][j] = mfma_32x32x16(fa[cur][i], fb[cur][j], acc[i][j]);
                         __builtin_amdgcn_sched_barrier(0);
                     }
-                if (s == 0 && pend) gb.advance();
+                if (s == 0 && pend && !RB) gb.advance();
+            }
+            if constexpr (RA) {
+                if (pend) ga.commit(prev, wave, lane);
+            }
+            if constexpr (RB) {
+                if (pend) gb.commit(prev + OpA::BYTES, wave, lane);
             }
             // slab kt + 1 has landed in every wave's part, and every wave holds
             // its last fragments of slab kt
@@ -468,7 +423,13 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), 2) void layer_pipe_kern
             const lds_char_t *nst = smem + stage * STAGE;
             const bool more = FAST || kt + STAGES < nfull;
             if constexpr (!FAST) {
-                if (!more && kt + STAGES < nk) slab_tail(st);
+                if (!more && kt + STAGES < nk) slab_tail(st, kt + STAGES);
+            }
+            if constexpr (RA) {
+                if (more) ga.fetch();
+            }
+            if constexpr (RB) {
+                if (more) gb.fetch();
             }
             constexpr int cur = (KPW - 1) & 1, nxt = cur ^ 1;
             // (after the last slab these reads fetch a stale stage, never used)
@@ -478,8 +439,8 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), 2) void layer_pipe_kern
                 for (int j = 0; j < TN; ++j) {
                     const int m = i * TN + j;
 #pragma unroll
-                    for (int l = 0; l < OpA::LOADS; ++l)
-                        if (l * NM / OpA::LOADS == m && more) ga.issue_one(st, wave, l);
+                    for (int l = 0; l < LA; ++l)
+                        if (l * NM / PA == m && more) ga.issue_one(st, wave, l);
 #pragma unroll
                     for (int f = 0; f < TM + TN; ++f)
                         if (f * NM / (TM + TN) == m) {
@@ -489,7 +450,7 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), 2) void layer_pipe_kern
                     acc[i][j] = mfma_32x32x16(fa[cur][i], fb[cur][j], acc[i][j]);
                     __builtin_amdgcn_sched_barrier(0);
                 }
-            if (more) ga.advance();
+            if (more && !RA) ga.advance();
         };
         int kt = 0;
         for (; kt + STAGES < nfull; ++kt) slab(std::true_type(), kt);
@@ -499,10 +460,20 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), 2) void layer_pipe_kern
         for (int s = 0; s < STAGES - 1; ++s) {
             lds_char_t *st = smem + s * STAGE;
             if (s < nfull) {
-                ga.issue(st, wave);
-                gb.issue(st + OpA::BYTES, wave);
+                if constexpr (RA) {
+                    ga.fetch();
+                    ga.commit(st, wave, lane);
+                } else {
+                    ga.issue(st, wave);
+                }
+                if constexpr (RB) {
+                    gb.fetch();
+                    gb.commit(st + OpA::BYTES, wave, lane);
+                } else {
+                    gb.issue(st + OpA::BYTES, wave);
+                }
             } else if (s < nk) {
-                slab_tail(st);
+                slab_tail(st, s);
             }
         }
         int stage = 0;
@@ -516,7 +487,13 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), 2) void layer_pipe_kern
             lds_char_t *dst = smem + ((stage == 0 ? STAGES : stage) - 1) * STAGE;
             const bool more = FAST || ns < nfull;
             if constexpr (!FAST) {
-                if (!more && ns < nk) slab_tail(dst);
+                if (!more && ns < nk) slab_tail(dst, ns);
+            }
+            if constexpr (RA) {
+                if (more) ga.fetch();
+            }
+            if constexpr (RB) {
+                if (more) gb.fetch();
             }
             const lds_char_t *sA = smem + stage * STAGE;
             const lds_char_t *sB = sA + OpA::BYTES;
@@ -537,16 +514,18 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), 2) void layer_pipe_kern
                             const int m = ((c2 * 4 + e) * TM + i) * TN + j;
 #pragma unroll
                             for (int l = 0; l < LOADS; ++l)
-                                if (l * TOTAL / LOADS == m && more) {
-                                    if (l < OpA::LOADS) ga.issue_one(dst, wave, l);
-                                    else gb.issue_one(dst + OpA::BYTES, wave, l - OpA::LOADS);
+                                if (l * TOTAL / PL == m && more) {
+                                    if (l < LA) ga.issue_one(dst, wave, l);
+                                    else gb.issue_one(dst + OpA::BYTES, wave, l - LA);
                                 }
                             acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(a[i][e], b[j][e], acc[i][j], 0, 0, 0);
                         }
             }
             if (more) {
-                ga.advance();
-                gb.advance();
+                if constexpr (RA) ga.commit(dst, wave, lane);
+                else ga.advance();
+                if constexpr (RB) gb.commit(dst + OpA::BYTES, wave, lane);
+                else gb.advance();
             }
             stage = stage + 1 == STAGES ? 0 : stage + 1;
         };

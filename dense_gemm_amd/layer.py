@@ -17,7 +17,8 @@ import ctypes
 
 import torch
 
-from . import DG_EPI_GELU, DG_EPI_RELU, DG_ERR_HIP, DG_KERNEL_AUTO, DG_OK, EPILOGUES, GemmError, _dtype_code, _lib
+from . import DG_BF16_F32ACC, DG_BF16_F32OUT, DG_EPI_GELU, DG_EPI_RELU, DG_ERR_HIP, DG_F16_F32ACC, DG_F16_F32OUT, DG_F32
+from . import DG_KERNEL_AUTO, DG_OK, EPILOGUES, GemmError, _dtype_code, _lib
 from . import dg_last_hip_error, dg_status_string, hip_error_name
 from .mx import _current_device, _empty, _kernel_names, _plain, _stream_of, _workspace
 
@@ -78,7 +79,7 @@ class LayerError(GemmError):
         self.status = status
 
 
-def _call(function, index, *args):
+def _run(function, index, args):
     """One library call with device `index` current."""
     f = _functions[function]
     if index == _current_device():
@@ -90,6 +91,12 @@ def _call(function, index, *args):
         raise LayerError(function, rc)
 
 
+# (operand, output) -> the library's dtype
+_DTYPES = {(torch.float32, torch.float32): DG_F32, (torch.float16, torch.float16): DG_F16_F32ACC,
+           (torch.bfloat16, torch.bfloat16): DG_BF16_F32ACC, (torch.float16, torch.float32): DG_F16_F32OUT,
+           (torch.bfloat16, torch.float32): DG_BF16_F32OUT}
+
+
 def _groups(offsets):
     """(groups, address) of a tensor of row offsets."""
     if offsets.dtype != torch.int32:
@@ -99,19 +106,15 @@ def _groups(offsets):
     return offsets.shape[0] - 1, offsets.data_ptr()
 
 
-def _rows(t, name, M, N, dtype):
-    """(address, row stride) of a matrix of rows, (None, N) where it is not given."""
-    if t is None:
-        return None, max(N, 1)
+def _rows(t, name, shape, dtype):
+    """(address, row stride) of a matrix of rows."""
     if t.dtype != dtype:
         raise TypeError(f"{name} must have C's dtype")
-    return t.data_ptr(), _plain(t, name, M, N)
+    return t.data_ptr(), _plain(t, name, *shape)
 
 
 def _matrices(B, groups, rows, cols, name="B"):
-    """(row stride, stride between the matrices) of B: [rows, cols], or [groups, rows, cols]."""
-    if groups is None:
-        return _plain(B, name, rows, cols), 0
+    """(row stride, stride between the matrices) of [groups, rows, cols]."""
     if B.shape != (groups, rows, cols):
         raise ValueError(f"{name} must be [{groups}, {rows}, {cols}]")
     if groups == 0:
@@ -119,71 +122,75 @@ def _matrices(B, groups, rows, cols, name="B"):
     return _plain(B[0], name, rows, cols), B.stride(0) if groups > 1 else 0
 
 
-def _product(function, A, B, offsets, C, transB, alpha, out_dtype, splits, workspace, stream, kernel, tensors, middle):
-    """One product over rows: the checks and arguments that both kinds share.
-    `middle(M, N, dtype)` gives the arguments between strideB and C."""
-    if A.dim() != 2:
+def _product(grad, A, B, offsets, C, transB, alpha, bias, activation, Z, R, beta, keep, out_dtype, splits, workspace, kernel,
+             stream):
+    """One product over rows.  `keep`: what the epilogue stores beside C (Z of the
+    forward, H of the gradient); Z: the gradient's."""
+    sb = B.shape
+    if len(A.shape) != 2:
         raise ValueError("A must be 2-D")
     if B.dtype != A.dtype:
         raise TypeError("A and B must share one dtype")
     M, K = A.shape
-    if B.dim() != (2 if offsets is None else 3):
+    if len(sb) != (2 if offsets is None else 3):
         raise ValueError("B must be 2-D" if offsets is None else "B must be 3-D, a matrix for each group")
-    N = B.shape[-2] if transB else B.shape[-1]
-    groups, address = (None, None) if offsets is None else _groups(offsets)
-    if (B.shape[-1] if transB else B.shape[-2]) != K:
-        raise ValueError(f"inner dimensions differ: {K} vs {B.shape[-1] if transB else B.shape[-2]}")
-    ldb, strideB = _matrices(B, groups, B.shape[-2], B.shape[-1])
+    N, inner = (sb[-2], sb[-1]) if transB else (sb[-1], sb[-2])
+    if inner != K:
+        raise ValueError(f"inner dimensions differ: {K} vs {inner}")
+    if offsets is None:
+        groups, address, ldb, strideB = 1, None, _plain(B, "B", *sb), 0
+    else:
+        groups, address = _groups(offsets)
+        ldb, strideB = _matrices(B, groups, sb[-2], sb[-1])
+    shape = (M, N)
     if C is None:
-        C = _empty((M, N), out_dtype or A.dtype, A.device, stream)
-    dtype = _dtype_code(A.dtype, C.dtype)
+        C = _empty(shape, out_dtype or A.dtype, A.device, stream)
+    cd = C.dtype
+    dtype = _DTYPES.get((A.dtype, cd))
+    if dtype is None:
+        raise TypeError(f"unsupported operand/output dtypes {A.dtype}/{cd} (float32, float16 or bfloat16 operands; an "
+                        "output of the operand dtype, or float32)")
     lda, ldc = _plain(A, "A", M, K), _plain(C, "C", M, N)
-    args = middle(M, N, C.dtype, groups)
+    k, ldk = (None, N or 1) if keep is None else _rows(keep, "H" if grad else "Z", shape, cd)
+    r, ldr = (None, N or 1) if R is None else _rows(R, "R", shape, cd)
     if offsets is not None:
         splits = 1
     elif splits == 0:
-        splits = max(dg_gemm_fused_choose(M, N, K, transB, dtype), 1)  # noqa: F821
+        splits = dg_gemm_fused_choose(M, N, K, transB, dtype)  # noqa: F821
     if splits > 1 and workspace is None:
         workspace = _empty(dg_layer_workspace_size(1, M, N, splits), torch.uint8, A.device, stream)  # noqa: F821
-    ws, wsb = _workspace(workspace)
-    index, handle = _stream_of(stream, (A, B, C, offsets, workspace, *tensors))
-    _call(function, index, transB, 1 if groups is None else groups, address, M, N, K, alpha, A.data_ptr(), lda, B.data_ptr(),
-          ldb, strideB, *args, C.data_ptr(), ldc, dtype, splits, ws, wsb, handle, kernel)
+    ws, wsb = (None, 0) if workspace is None else _workspace(workspace)
+    if grad:
+        z, ldz = _rows(Z, "Z", shape, cd)
+    b, stride_bias = None, 0
+    if bias is not None:
+        if bias.dtype != cd:
+            raise TypeError("bias must have C's dtype")
+        if offsets is None:
+            if bias.shape != (N,) or (N > 1 and bias.stride(0) != 1):
+                raise ValueError(f"bias must be [{N}], contiguous")
+        else:
+            if bias.shape != (groups, N) or (N > 1 and bias.stride(1) != 1):
+                raise ValueError(f"bias must be [{groups}, {N}], its rows contiguous")
+            stride_bias = bias.stride(0) if groups > 1 else 0
+        b = bias.data_ptr()
+    index, handle = _stream_of(stream, (A, B, C, offsets, workspace, bias, Z, R, keep))
+    if grad:
+        _run("dg_gemm_act_grad_with_kernel", index,
+             (transB, groups, address, M, N, K, alpha, A.data_ptr(), lda, B.data_ptr(), ldb, strideB, beta, r, ldr, k, ldk,
+              activation, z, ldz, C.data_ptr(), ldc, dtype, splits, ws, wsb, handle, kernel))
+        return C
+    _run("dg_gemm_fused_with_kernel", index,
+         (transB, groups, address, M, N, K, alpha, A.data_ptr(), lda, B.data_ptr(), ldb, strideB, b, stride_bias, activation,
+          k, ldk, beta, r, ldr, C.data_ptr(), ldc, dtype, splits, ws, wsb, handle, kernel))
     return C
 
 
-def _fused(A, B, offsets, C, transB, alpha, bias, activation, R, beta, Z, out_dtype, splits, workspace, kernel, stream):
-    if activation not in EPILOGUES:
-        raise ValueError(f"activation must be one of {sorted(EPILOGUES)}")
-
-    def middle(M, N, dtype, groups):
-        b, stride_bias = None, 0
-        if bias is not None:
-            if bias.dtype != dtype:
-                raise TypeError("bias must have C's dtype")
-            if bias.shape != ((N,) if groups is None else (groups, N)) or (N > 1 and bias.stride(-1) != 1):
-                raise ValueError(f"bias must be [{N}]" if groups is None else f"bias must be [{groups}, {N}], its rows contiguous")
-            b, stride_bias = bias.data_ptr(), bias.stride(0) if groups is not None and groups > 1 else 0
-        z, ldz = _rows(Z, "Z", M, N, dtype)
-        r, ldr = _rows(R, "R", M, N, dtype)
-        return b, stride_bias, EPILOGUES[activation], z, ldz, beta, r, ldr
-
-    return _product("dg_gemm_fused_with_kernel", A, B, offsets, C, transB, alpha, out_dtype, splits, workspace, stream,
-                    kernel, (bias, Z, R), middle)
-
-
-def _act_grad(A, B, offsets, Z, C, transB, alpha, activation, R, beta, H, out_dtype, splits, workspace, kernel, stream):
-    if activation not in _ACT_GRADS:
-        raise ValueError(f"activation must be one of {sorted(_ACT_GRADS)}")
-
-    def middle(M, N, dtype, groups):
-        r, ldr = _rows(R, "R", M, N, dtype)
-        h, ldh = _rows(H, "H", M, N, dtype)
-        z, ldz = _rows(Z, "Z", M, N, dtype)
-        return beta, r, ldr, h, ldh, _ACT_GRADS[activation], z, ldz
-
-    return _product("dg_gemm_act_grad_with_kernel", A, B, offsets, C, transB, alpha, out_dtype or Z.dtype, splits, workspace,
-                    stream, kernel, (Z, R, H), middle)
+def _activation(codes, name):
+    code = codes.get(name)
+    if code is None:
+        raise ValueError(f"activation must be one of {sorted(codes)}")
+    return code
 
 
 def gemm_fused(A, B, C=None, transB=False, alpha=1.0, bias=None, activation="none", R=None, beta=1.0, Z=None, out_dtype=None,
@@ -200,7 +207,8 @@ def gemm_fused(A, B, C=None, transB=False, alpha=1.0, bias=None, activation="non
     `splits` cuts K into ranges (0: the library's choice) whose fp32 sums go to
     `workspace`, a 16-byte aligned tensor of dg_layer_workspace_size(1, M, N,
     splits) bytes, or to one allocated here."""
-    return _fused(A, B, None, C, transB, alpha, bias, activation, R, beta, Z, out_dtype, splits, workspace, kernel, stream)
+    return _product(False, A, B, None, C, transB, alpha, bias, _activation(EPILOGUES, activation), None, R, beta, Z, out_dtype,
+                    splits, workspace, kernel, stream)
 
 
 def gemm_grouped(A, B, offsets, C=None, transB=False, alpha=1.0, bias=None, activation="none", R=None, beta=1.0, Z=None,
@@ -212,7 +220,8 @@ def gemm_grouped(A, B, offsets, C=None, transB=False, alpha=1.0, bias=None, acti
     group may be empty); B is [groups, K, N] or (transB) [groups, N, K]; bias is
     [groups, N].  Rows before offsets[0] and from offsets[-1] on are left as
     they were, in every output."""
-    return _fused(A, B, offsets, C, transB, alpha, bias, activation, R, beta, Z, out_dtype, 1, None, kernel, stream)
+    return _product(False, A, B, offsets, C, transB, alpha, bias, _activation(EPILOGUES, activation), None, R, beta, Z,
+                    out_dtype, 1, None, kernel, stream)
 
 
 def gemm_act_grad(A, B, Z, C=None, transB=False, alpha=1.0, activation="gelu", R=None, beta=1.0, H=None, out_dtype=None,
@@ -224,13 +233,15 @@ def gemm_act_grad(A, B, Z, C=None, transB=False, alpha=1.0, activation="gelu", R
     (a residual's), and H, where given, receives the sum before act'.  All are
     [M, N] of C's dtype (C: allocated when None, with Z's dtype).  relu chooses H
     or 0; activation is "relu" or "gelu".  The rest as gemm_fused."""
-    return _act_grad(A, B, None, Z, C, transB, alpha, activation, R, beta, H, out_dtype, splits, workspace, kernel, stream)
+    return _product(True, A, B, None, C, transB, alpha, None, _activation(_ACT_GRADS, activation), Z, R, beta, H,
+                    out_dtype or Z.dtype, splits, workspace, kernel, stream)
 
 
 def gemm_grouped_act_grad(A, B, offsets, Z, C=None, transB=False, alpha=1.0, activation="gelu", R=None, beta=1.0, H=None,
                           out_dtype=None, kernel=DG_KERNEL_AUTO, stream=None):
     """gemm_act_grad with a matrix for each group of rows, as gemm_grouped."""
-    return _act_grad(A, B, offsets, Z, C, transB, alpha, activation, R, beta, H, out_dtype, 1, None, kernel, stream)
+    return _product(True, A, B, offsets, C, transB, alpha, None, _activation(_ACT_GRADS, activation), Z, R, beta, H,
+                    out_dtype or Z.dtype, 1, None, kernel, stream)
 
 
 def gemm_dw(A, B, C=None, offsets=None, alpha=1.0, beta=0.0, dbias=None, out_dtype=None, splits=0, workspace=None,
@@ -262,17 +273,18 @@ def gemm_dw(A, B, C=None, offsets=None, alpha=1.0, beta=0.0, dbias=None, out_dty
             raise ValueError("beta != 0 needs C")
         C = _empty((M, N) if groups is None else (groups, M, N), out_dtype or A.dtype, A.device, stream)
     dtype = _dtype_code(A.dtype, C.dtype)
-    ldc, strideC = _matrices(C, groups, M, N, "C")
+    ldc, strideC = (_plain(C, "C", M, N), 0) if groups is None else _matrices(C, groups, M, N, "C")
     if dbias is not None and (dbias.dtype != torch.float32 or dbias.shape != ((M,) if groups is None else (groups, M))
                               or not dbias.is_contiguous()):
         raise ValueError("dbias must be a contiguous float32 tensor of " + (f"[{M}]" if groups is None else f"[{groups}, {M}]"))
     lda, ldb = _plain(A, "A", rows, M), _plain(B, "B", rows, N)
     if splits == 0:
-        splits = max(dg_gemm_dw_choose(count, rows, M, N, dtype), 1)  # noqa: F821
+        splits = dg_gemm_dw_choose(count, rows, M, N, dtype)  # noqa: F821
     if splits > 1 and workspace is None:
         workspace = _empty(dg_layer_workspace_size(count, M, N, splits), torch.uint8, A.device, stream)  # noqa: F821
-    ws, wsb = _workspace(workspace)
+    ws, wsb = (None, 0) if workspace is None else _workspace(workspace)
     index, handle = _stream_of(stream, (A, B, C, offsets, dbias, workspace))
-    _call("dg_gemm_dw_with_kernel", index, count, address, rows, M, N, alpha, A.data_ptr(), lda, B.data_ptr(), ldb, beta,
-          C.data_ptr(), ldc, strideC, None if dbias is None else dbias.data_ptr(), dtype, splits, ws, wsb, handle, kernel)
+    _run("dg_gemm_dw_with_kernel", index,
+         (count, address, rows, M, N, alpha, A.data_ptr(), lda, B.data_ptr(), ldb, beta, C.data_ptr(), ldc, strideC,
+          None if dbias is None else dbias.data_ptr(), dtype, splits, ws, wsb, handle, kernel))
     return C

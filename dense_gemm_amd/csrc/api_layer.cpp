@@ -57,6 +57,11 @@ const LayerFamily kLayer[] = {
     {"layer_32_rows_stream", 14, 32, 16, 1, 512, STREAM},
     {"layer_16_rows_stream_w16", 15, 16, 16, 1, 1024, STREAM},
     {"layer_32_rows_stream_w16", 16, 32, 16, 1, 1024, STREAM},
+    {"x_64_k2_s4", 17, 64, 64, 4, 256, DIRECT},
+    {"x_64_k2_s2", 18, 64, 64, 4, 256, DIRECT},
+    {"x_64_k2_s3", 19, 64, 64, 4, 256, DIRECT},
+    {"x_128_k2_s4", 20, 128, 128, 4, 512, DIRECT},
+    {"x_64x128_k2", 21, 64, 128, 4, 256, DIRECT},
 };
 constexpr int kNumLayer = sizeof(kLayer) / sizeof(kLayer[0]);
 enum { K_ANY_64, K_ANY_128, K_PIPE_64, K_PIPE_128, K_PIPE_256 };
@@ -94,7 +99,7 @@ bool supports(int k, const LayerShape &s)
     if (s.M > kMaxTiled || s.N > kMaxTiled || s.K > kMaxTiled) return false;
     if ((f.loads == DIRECT || f.loads == STREAM) && !s.direct()) return false;
     if (f.loads == STREAM && (s.kind == dg::LAYER_WEIGHTS || !s.tb)) return false;
-    if (k >= K_PIPE_256 && f.loads == DIRECT && s.type == 0) return false;
+    if (((k >= K_PIPE_256 && k < 10) || k>13) && f.loads == DIRECT && s.type == 0) return false;
     // the row kernels' columns of a B stored K x N go four together
     if (f.loads == ROWS && (s.kind == dg::LAYER_WEIGHTS || (!s.tb && s.N < 4))) return false;
     // a launch holds fewer than 2^32 threads
@@ -118,7 +123,7 @@ int resolve_splits(const LayerShape &s, int splits)
 size_t workspace_bytes_of(int64_t groups, int64_t M, int64_t N, int splits)
 {
     if (groups <= 0 || M <= 0 || N <= 0 || splits <= 1) return 0;
-    return (size_t)splits * (size_t)groups * (size_t)M * (size_t)N * 4;
+    return (size_t)splits * (size_t)groups * (size_t)M * (size_t)(N + 1) * 4;     // and a bias's gradient
 }
 
 int launch(LayerParams &p, const LayerShape &s, int dtype, int kernel, int splits, void *ws, size_t ws_bytes, int ws_arg,
@@ -346,15 +351,18 @@ int dg_gemm_dw_with_kernel(int64_t groups, const int32_t *offsets, int64_t rows,
     p.ctype = output_type(dtype);
     p.dbias = dbias;
     if (sums && (M > kMaxTiled || rows > kMaxTiled)) return DG_ERR_UNSUPPORTED;
+    // the bias's gradient comes with the product, or by a pass of its own without one
+    const bool alone = sums && rows > 0 && !reads;
     if (work) {
         LayerParams q = p;
         if (!reads) q.K = 0;
+        if (alone) q.dbias = nullptr;
         const LayerShape s = {p.kind, operand_type(dtype), false, offsets != nullptr, groups, M, N, q.K,
                               direct_ok(A, lda, 0, eb), direct_ok(B, ldb, 0, eb)};
         const int rc = launch(q, s, dtype, kernel, splits, workspace, workspace_bytes, 18, (hipStream_t)stream);
         if (rc != DG_OK) return rc;
     }
-    return sums ? dg::launch_status(dg::launch_layer_colsum(p, operand_type(dtype), (hipStream_t)stream)) : DG_OK;
+    return alone || (sums && !work) ? dg::launch_status(dg::launch_layer_colsum(p, operand_type(dtype), (hipStream_t)stream)) : DG_OK;
 }
 
 int dg_gemm_dw(int64_t groups, const int32_t *offsets, int64_t rows, int64_t M, int64_t N, float alpha, const void *A,

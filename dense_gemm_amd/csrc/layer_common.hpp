@@ -38,7 +38,7 @@ struct LayerParams {
     int32_t ctype;                  // element of C, R, Z, keep and bias: 0 fp32, 1 fp16, 2 bf16
     int32_t tiles_m, tiles_n, group_m;
     int32_t splits;                 // K ranges, a grid dimension; with more than one the raw sums go to ws
-    float *ws;                      // [splits][groups][M][N]
+    float *ws;                      // [splits][groups][M][N], and weights: [splits][groups][M] behind them
     float *dbias;                   // weights: [groups][M], or NULL
 };
 
@@ -233,6 +233,19 @@ __device__ __forceinline__ void layer_partial(const LayerParams &p, const LayerT
 {
     float *w = p.ws + (((int64_t)blockIdx.y * p.groups + t.group) * p.M + row) * p.N + col;
     store_row<float, W>(w, v);
+}
+
+// One column's sum for the bias's gradient: a split's goes behind the splits' sums of
+// the product, [splits][groups][M].
+__device__ __forceinline__ void layer_dbias(const LayerParams &p, int group, int m, float v)
+{
+    const int64_t at = (int64_t)group * p.M + m, gm = (int64_t)p.groups * p.M;
+    if (p.splits > 1) {
+        p.ws[p.splits * gm * p.N + blockIdx.y * gm + at] = v;
+        return;
+    }
+    if (p.beta != 0.f) v = __builtin_fmaf(p.beta, p.dbias[at], v);
+    p.dbias[at] = v;
 }
 
 // First row and rows of group g.  Offsets outside 0 .. total and descending ones

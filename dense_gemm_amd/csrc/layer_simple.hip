@@ -37,7 +37,8 @@ __device__ __forceinline__ void join(const LayerParams &p, int64_t grow, int col
     layer_finish<TC, W>(p, t, row, col, v, aux, bias);
 }
 
-// 8 columns of a row a thread; the last columns one by one.
+// 8 columns of a row a thread; the last columns one by one, the bias's gradient with
+// the first.
 template <typename TC>
 __global__ __launch_bounds__(256) void layer_join_kernel(LayerParams p)
 {
@@ -46,6 +47,13 @@ __global__ __launch_bounds__(256) void layer_join_kernel(LayerParams p)
     for (int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x; at < total; at += (int64_t)gridDim.x * 256) {
         const int64_t grow = at / per_row;
         const int col = (int)(at - grow * per_row) * 8;
+        if (p.dbias && col == 0) {
+            const int64_t gm = (int64_t)p.groups * p.M;
+            const float *w = p.ws + p.splits * gm * p.N + grow;
+            float v = 0.f;
+            for (int s = 0; s < p.splits; ++s) v += w[s * gm];
+            p.dbias[grow] = p.beta != 0.f ? __builtin_fmaf(p.beta, p.dbias[grow], v) : v;
+        }
         if (col + 8 <= p.N) {
             join<TC, 8>(p, grow, col);
         } else {
@@ -55,7 +63,8 @@ __global__ __launch_bounds__(256) void layer_join_kernel(LayerParams p)
     }
 }
 
-// dbias[g][m] = sum over group g's rows of A[r][m] (+ beta * dbias): a workgroup
+// dbias where there is no product to compute it with (no column in B, or alpha = 0):
+// dbias[g][m] = sum over group g's rows of A[r][m] (+ beta * dbias).  A workgroup
 // takes 64 columns of a group, 64 rows at a time, 8 columns of a row a lane; the
 // 64 partial sums of a column are added in a fixed order.
 template <typename T>

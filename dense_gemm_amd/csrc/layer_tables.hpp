@@ -8,14 +8,14 @@
 namespace dg {
 
 // [forward and gradient with B stored K x N, with B stored N x K, weights]
-#define DG_LAYER_PIPE(BM, BN, WM, WN, STAGES, BK, RA, RB)                                      \
-    {(const void *)&layer_pipe_kernel<T, BM, BN, WM, WN, false, false, STAGES, BK, RA, RB>,    \
-     (const void *)&layer_pipe_kernel<T, BM, BN, WM, WN, false, true, STAGES, BK, RA, RB>,     \
-     (const void *)&layer_pipe_kernel<T, BM, BN, WM, WN, true, false, STAGES, BK, RA, RB>}
+#define DG_LAYER_PIPE(BM, BN, WM, WN, KG, STAGES, BK, RA, RB)                                  \
+    {(const void *)&layer_pipe_kernel<T, BM, BN, WM, WN, KG, false, false, STAGES, BK, RA, RB>,    \
+     (const void *)&layer_pipe_kernel<T, BM, BN, WM, WN, KG, false, true, STAGES, BK, RA, RB>,     \
+     (const void *)&layer_pipe_kernel<T, BM, BN, WM, WN, KG, true, false, STAGES, BK, RA, RB>}
 // an operand that the direct loads do not take: A, B, both
 #define DG_LAYER_ANY(BM, BN, WM, WN, BK)                                                       \
-    DG_LAYER_PIPE(BM, BN, WM, WN, 2, BK, true, false), DG_LAYER_PIPE(BM, BN, WM, WN, 2, BK, false, true), \
-        DG_LAYER_PIPE(BM, BN, WM, WN, 2, BK, true, true)
+    DG_LAYER_PIPE(BM, BN, WM, WN, 1, 2, BK, true, false), DG_LAYER_PIPE(BM, BN, WM, WN, 1, 2, BK, false, true), \
+        DG_LAYER_PIPE(BM, BN, WM, WN, 1, 2, BK, true, true)
 #define DG_LAYER_ROWS(MT, NWV)                                                                 \
     {(const void *)&layer_rows_kernel<T, MT, false, NWV, false>,                               \
      (const void *)&layer_rows_kernel<T, MT, true, NWV, false>, nullptr}
@@ -29,8 +29,8 @@ const void *layer_kernel_of(int config, int variant)
         static const void *const table[][3] = {
             DG_LAYER_ANY(64, 64, 32, 32, 32),
             DG_LAYER_ANY(128, 128, 64, 64, 16),
-            DG_LAYER_PIPE(64, 64, 32, 32, 3, 32, false, false),
-            DG_LAYER_PIPE(128, 128, 64, 64, 4, 16, false, false),
+            DG_LAYER_PIPE(64, 64, 32, 32, 1, 3, 32, false, false),
+            DG_LAYER_PIPE(128, 128, 64, 64, 1, 4, 16, false, false),
             DG_LAYER_NONE,
             DG_LAYER_NONE,
             DG_LAYER_NONE,
@@ -40,23 +40,30 @@ const void *layer_kernel_of(int config, int variant)
             DG_LAYER_STREAM(2, 8),
             DG_LAYER_STREAM(1, 16),
             DG_LAYER_STREAM(2, 16),
+            DG_LAYER_PIPE(64, 64, 32, 32, 1, 4, 32, false, false),
+            DG_LAYER_NONE, DG_LAYER_NONE, DG_LAYER_NONE, DG_LAYER_NONE
         };
         return table[config][variant];
     } else {
         static const void *const table[][3] = {
             DG_LAYER_ANY(64, 64, 32, 32, 64),
             DG_LAYER_ANY(128, 128, 64, 64, 64),
-            DG_LAYER_PIPE(64, 64, 32, 32, 4, 64, false, false),
-            DG_LAYER_PIPE(128, 128, 64, 64, 2, 64, false, false),
-            DG_LAYER_PIPE(256, 256, 128, 64, 2, 64, false, false),
-            DG_LAYER_PIPE(256, 128, 128, 64, 3, 32, false, false),
-            DG_LAYER_PIPE(256, 256, 128, 64, 4, 32, false, false),
+            DG_LAYER_PIPE(64, 64, 32, 32, 1, 4, 64, false, false),
+            DG_LAYER_PIPE(128, 128, 64, 64, 1, 2, 64, false, false),
+            DG_LAYER_PIPE(256, 256, 128, 64, 1, 2, 64, false, false),
+            DG_LAYER_PIPE(256, 128, 128, 64, 1, 3, 32, false, false),
+            DG_LAYER_PIPE(256, 256, 128, 64, 1, 4, 32, false, false),
             DG_LAYER_ROWS(1, 8),
             DG_LAYER_ROWS(2, 8),
             DG_LAYER_STREAM(1, 8),
             DG_LAYER_STREAM(2, 8),
             DG_LAYER_STREAM(1, 16),
             DG_LAYER_STREAM(2, 16),
+            DG_LAYER_PIPE(64, 64, 64, 32, 2, 4, 64, false, false),
+            DG_LAYER_PIPE(64, 64, 64, 32, 2, 2, 64, false, false),
+            DG_LAYER_PIPE(64, 64, 64, 32, 2, 3, 64, false, false),
+            DG_LAYER_PIPE(128, 128, 64, 64, 2, 4, 64, false, false),
+            DG_LAYER_PIPE(64, 128, 64, 64, 2, 3, 64, false, false),
         };
         return table[config][variant];
     }

@@ -283,6 +283,13 @@ struct LayerOperand : std::conditional<sizeof(T) == 2, SlabOperandH<T, BMN, KCON
     }
 };
 
+template <typename V8>
+__device__ __forceinline__ float sum8(V8 x)
+{
+    return (((float)x[0] + (float)x[1]) + ((float)x[2] + (float)x[3])) +
+           (((float)x[4] + (float)x[5]) + ((float)x[6] + (float)x[7]));
+}
+
 // BM x BN tile, waves of WM x WN, a ring of STAGES slabs of BK summed indices.
 //
 // 16 bits: fragments are double-buffered per step of 16 k.  The barrier of a slab sits
@@ -292,13 +299,16 @@ struct LayerOperand : std::conditional<sizeof(T) == 2, SlabOperandH<T, BMN, KCON
 // a barrier and loads and reads lie between MFMAs.  An operand through registers
 // (RA, RB; two stages) is fetched in a slab's last step and written to its stage before
 // the next slab's barrier.
+// Two K groups (KG): each runs half of a slab's steps, so that a tile has twice the
+// waves; their sums meet in LDS at the end.
 // fp32: one barrier at a slab's start, the loads of slab kt + STAGES - 1 spread over its
 // MFMAs (or fetched before them and written after them).
-template <typename T, int BM, int BN, int WM, int WN, bool DW, bool TB, int STAGES, int BK, bool RA, bool RB>
-__global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), 2) void layer_pipe_kernel(LayerParams p)
+template <typename T, int BM, int BN, int WM, int WN, int KG, bool DW, bool TB, int STAGES, int BK, bool RA, bool RB>
+__global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * KG, 2) void layer_pipe_kernel(LayerParams p)
 {
     constexpr bool H = sizeof(T) == 2;
-    constexpr int WAVES_N = BN / WN, NW = (BM / WM) * WAVES_N, TM = WM / 32, TN = WN / 32, NM = TM * TN;
+    constexpr int WAVES_N = BN / WN, NWG = (BM / WM) * WAVES_N, NW = NWG * KG, TM = WM / 32, TN = WN / 32, NM = TM * TN;
+    static_assert(KG == 1 || (H && KG == 2 && TM % 2 == 0), "two K groups: 16 bits, an even number of strips");
     typedef LayerOperand<T, BM, !DW, NW, BK, RA> OpA;
     typedef LayerOperand<T, BN, TB && !DW, NW, BK, RB> OpB;
     static_assert(!(RA || RB) || STAGES == 2, "an operand through registers: two stages");
@@ -315,7 +325,7 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), 2) void layer_pipe_kern
     if (!layer_tile(p, BM, BN, t)) return;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wm0 = (wave / WAVES_N) * WM, wn0 = (wave % WAVES_N) * WN;
+    const int kgroup = wave / NWG, wm0 = (wave % NWG / WAVES_N) * WM, wn0 = (wave % WAVES_N) * WN;
     const T *A = (const T *)p.A + (DW ? (t.row0 + t.k0) * p.lda : t.row0 * p.lda + t.k0);
     const T *B = (const T *)p.B + (DW ? (t.row0 + t.k0) * p.ldb
                                       : t.group * p.strideB + (TB ? (int64_t)t.k0 : t.k0 * p.ldb));
@@ -341,12 +351,22 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), 2) void layer_pipe_kern
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
 
+    // weights: the first tile column adds up A's columns for the bias's gradient from
+    // the fragments that it multiplies, each step in one of the waves that share them
+    float sums[TM];
+#pragma unroll
+    for (int i = 0; i < TM; ++i) sums[i] = 0.f;
+    const bool summing = DW && p.dbias && t.n0 == 0;
+    const int wcol = wave % WAVES_N;
+
     if constexpr (H) {
         typedef T V8 __attribute__((ext_vector_type(8)));
-        constexpr int KPW = BK / 16;
+        constexpr int KPW = BK / 16 / KG;
+        const int kk0 = kgroup * KPW;
+        static_assert(KPW % 2 == 0, "steps alternate between the two fragment sets");
         V8 fa[2][TM], fb[2][TN];
-        auto read_a = [&](const lds_char_t *st, int i, int s) { return ga.frag(st, wm0 + 32 * i, s, lane); };
-        auto read_b = [&](const lds_char_t *st, int j, int s) { return gb.frag(st + OpA::BYTES, wn0 + 32 * j, s, lane); };
+        auto read_a = [&](const lds_char_t *st, int i, int s) { return ga.frag(st, wm0 + 32 * i, kk0 + s, lane); };
+        auto read_b = [&](const lds_char_t *st, int j, int s) { return gb.frag(st + OpA::BYTES, wn0 + 32 * j, kk0 + s, lane); };
         // the ring, but for B of its last stage, which the first step loads (and
         // for an operand through registers, which holds its second slab)
 #pragma unroll
@@ -387,6 +407,10 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), 2) void layer_pipe_kern
 #pragma unroll
             for (int s = 0; s + 1 < KPW; ++s) {
                 const int cur = s & 1, nxt = cur ^ 1;
+                if (DW && summing && s % WAVES_N == wcol) {
+#pragma unroll
+                    for (int i = 0; i < TM; ++i) sums[i] += sum8(fa[cur][i]);
+                }
 #pragma unroll
                 for (int i = 0; i < TM; ++i)
 #pragma unroll
@@ -432,6 +456,10 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), 2) void layer_pipe_kern
                 if (more) gb.fetch();
             }
             constexpr int cur = (KPW - 1) & 1, nxt = cur ^ 1;
+            if (DW && summing && (KPW - 1) % WAVES_N == wcol) {
+#pragma unroll
+                for (int i = 0; i < TM; ++i) sums[i] += sum8(fa[cur][i]);
+            }
             // (after the last slab these reads fetch a stale stage, never used)
 #pragma unroll
             for (int i = 0; i < TM; ++i)
@@ -505,6 +533,10 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), 2) void layer_pipe_kern
                 for (int i = 0; i < TM; ++i) a[i] = ga.frag4(sA, wm0 + 32 * i, c2, lane);
 #pragma unroll
                 for (int j = 0; j < TN; ++j) b[j] = gb.frag4(sB, wn0 + 32 * j, c2, lane);
+                if (DW && summing && c2 % WAVES_N == wcol) {
+#pragma unroll
+                    for (int i = 0; i < TM; ++i) sums[i] += (a[i][0] + a[i][1]) + (a[i][2] + a[i][3]);
+                }
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
 #pragma unroll
@@ -535,7 +567,63 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), 2) void layer_pipe_kern
     }
     wait_vmcnt<0>();
     __syncthreads();                   // every wave is done with the ring
-    layer_store<T>(p, t, smem + wave * kStripBytes<WN>, acc, t.m0 + wm0, t.n0 + wn0, lane);
+    if (DW && summing) {
+        // [wave][32 * strip + row]: added over the waves that share the rows, in order
+        typedef __attribute__((address_space(3))) float lds_float_t;
+        lds_float_t *red = (lds_float_t *)smem;
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+            const float both = sums[i] + __shfl_xor(sums[i], 32);     // the lane halves' parts of the sum
+            if (lane < 32) red[wave * WM + 32 * i + lane] = both;
+        }
+        __syncthreads();
+        for (int m = threadIdx.x; m < BM; m += 64 * NW) {
+            if (t.m0 + m >= p.M) break;
+            float v = 0.f;
+#pragma unroll
+            for (int g = 0; g < KG; ++g)
+#pragma unroll
+                for (int c = 0; c < WAVES_N; ++c) v += red[(g * NWG + m / WM * WAVES_N + c) * WM + m % WM];
+            layer_dbias(p, t.group, t.m0 + m, v);
+        }
+        __syncthreads();
+    }
+    if constexpr (KG == 1) {
+        layer_store<T>(p, t, smem + wave * kStripBytes<WN>, acc, t.m0 + wm0, t.n0 + wn0, lane);
+    } else {
+        // the two K groups' sums: each wave keeps half of the strips and hands the
+        // other half to its partner, the same part of the tile in the other group
+        constexpr int HS = TM / 2, SLOT = HS * TN * 4096;
+        static_assert(NW * SLOT <= sizeof(smem_raw), "the exchange fits");
+        f32x16 mine[HS][TN];
+        lds_char_t *out = smem + wave * SLOT;
+        const lds_char_t *in = smem + (wave + NWG) % NW * SLOT;
+        typedef __attribute__((address_space(3))) f32x4 lds_f32x4_t;
+#pragma unroll
+        for (int i = 0; i < HS; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                const f32x16 give = kgroup ? acc[i][j] : acc[HS + i][j];
+                mine[i][j] = kgroup ? acc[HS + i][j] : acc[i][j];
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    *(lds_f32x4_t *)(out + ((i * TN + j) * 4 + c) * 1024 + lane * 16) =
+                        (f32x4){give[4 * c], give[4 * c + 1], give[4 * c + 2], give[4 * c + 3]};
+            }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < HS; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const f32x4 x = *(const lds_f32x4_t *)(in + ((i * TN + j) * 4 + c) * 1024 + lane * 16);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) mine[i][j][4 * c + e] += x[e];
+                }
+        __syncthreads();               // read before the strips are staged
+        layer_store<T>(p, t, smem + wave * kStripBytes<WN>, mine, t.m0 + wm0 + 32 * HS * kgroup, t.n0 + wn0, lane);
+    }
 }
 
 }  // namespace dg

@@ -515,7 +515,8 @@ int dg_gemm_dw(int64_t groups, const int32_t *offsets, int64_t rows, int64_t M, 
  * choice), for tests and measurement; DG_ERR_UNSUPPORTED when it cannot run the
  * problem.  The kernels' names (NULL when out of range), the ranges that splits = 0
  * gives (or -i: 1 M, 2 N, 3 K, 4 transB, 5 dtype; 1 groups, 2 rows, 3 M, 4 N, 5
- * dtype), and the workspace's bytes (0 for one range). */
+ * dtype), and the workspace's bytes, splits * groups * M * (N + 1) * 4 (0 for one
+ * range). */
 int dg_gemm_fused_with_kernel(dg_op_t transB, int64_t groups, const int32_t *offsets, int64_t M, int64_t N, int64_t K,
                               float alpha, const void *A, int64_t lda, const void *B, int64_t ldb, int64_t strideB,
                               const void *bias, int64_t strideBias, dg_epilogue_t epilogue, void *Z, int64_t ldz, float beta,

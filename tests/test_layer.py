@@ -33,7 +33,7 @@ COMMON = [({"transB": 2}, "transB"), ({"groups": -1}, "groups"), ({"groups": 2},
           ({"R": P + 1}, "R"), ({"ldr": 15}, "ldr"), ({"C": None}, "C"), ({"C": P + 1}, "C"), ({"C": P + 2, "dtype": 3, "bias": P, "R": None, "Z": P, "H": None}, "C"),
           ({"ldc": 15}, "ldc"), ({"dtype": 5}, "dtype"), ({"dtype": -1}, "dtype"), ({"splits": -1}, "splits"),
           ({"splits": 4097}, "splits"), ({"splits": 2}, "workspace"), ({"splits": 2, "workspace": P + 8}, "workspace"),
-          ({"splits": 2, "workspace": P, "workspace_bytes": 2 * 8 * 16 * 4 - 1}, "workspace_bytes")]
+          ({"splits": 2, "workspace": P, "workspace_bytes": 2 * 8 * 17 * 4 - 1}, "workspace_bytes")]
 
 
 @pytest.mark.parametrize("changes,name", COMMON + [
@@ -62,7 +62,7 @@ def test_act_grad_refusals(changes, name):
     ({"lda": 15}, "lda"), ({"B": None}, "B"), ({"B": P + 1}, "B"), ({"ldb": 31}, "ldb"), ({"C": None}, "C"), ({"C": P + 1}, "C"),
     ({"ldc": 31}, "ldc"), ({"strideC": -1}, "strideC"), ({"groups": 2, "offsets": P, "strideC": 511}, "strideC"),
     ({"dbias": P + 2}, "dbias"), ({"dtype": 7}, "dtype"), ({"splits": 5000}, "splits"), ({"splits": 2}, "workspace"),
-    ({"splits": 2, "workspace": P, "workspace_bytes": 4095}, "workspace_bytes"),
+    ({"splits": 2, "workspace": P, "workspace_bytes": 2 * 16 * 33 * 4 - 1}, "workspace_bytes"),
     ({"alpha": 0.0, "B": None, "A": None}, "A")])
 def test_dw_refusals(changes, name):
     args = {**DW, **changes}
@@ -105,7 +105,7 @@ def test_kernel_names_and_choices():
     for M, N, K in ((1, 16, 16), (64, 2048, 8192), (16384, 5632, 2048)):
         assert 1 <= dg.dg_gemm_fused_choose(M, N, K, 1, 1) <= 4096
         assert 1 <= dg.dg_gemm_dw_choose(4, K, M, N, 1) <= 4096
-    assert dg.dg_layer_workspace_size(3, 5, 7, 4) == 3 * 5 * 7 * 4 * 4 and dg.dg_layer_workspace_size(3, 5, 7, 1) == 0
+    assert dg.dg_layer_workspace_size(3, 5, 7, 4) == 3 * 5 * 8 * 4 * 4 and dg.dg_layer_workspace_size(3, 5, 7, 1) == 0
 
 
 def test_torch_refusals():

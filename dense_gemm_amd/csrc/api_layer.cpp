@@ -46,25 +46,17 @@ struct LayerFamily {
 const LayerFamily kLayer[] = {
     {"layer_64x64_any", 0, 64, 64, 4, 256, ANY},
     {"layer_128x128_any", 3, 128, 128, 4, 256, ANY},
-    {"layer_64x64_pipe", 6, 64, 64, 4, 256, DIRECT},
-    {"layer_128x128_pipe", 7, 128, 128, 4, 256, DIRECT},
-    {"layer_256x256_pipe", 8, 256, 256, 4, 512, DIRECT},
-    {"layer_256x128_pipe", 9, 256, 128, 4, 256, DIRECT},
-    {"layer_256x256_k32_pipe", 10, 256, 256, 4, 512, DIRECT},
-    {"layer_16_rows", 11, 16, 16, 1, 512, ROWS},
-    {"layer_32_rows", 12, 32, 16, 1, 512, ROWS},
+    {"layer_64x64_deep", 6, 64, 64, 4, 256, DIRECT},
+    {"layer_64x64", 7, 64, 64, 4, 256, DIRECT},
+    {"layer_128x128_deep", 8, 128, 128, 4, 512, DIRECT},
+    {"layer_128x128", 9, 128, 128, 4, 256, DIRECT},
+    {"layer_256x256", 10, 256, 256, 4, 512, DIRECT},
+    {"layer_256x128", 11, 256, 128, 4, 256, DIRECT},
+    {"layer_16_rows", 12, 16, 16, 1, 512, ROWS},
     {"layer_16_rows_stream", 13, 16, 16, 1, 512, STREAM},
-    {"layer_32_rows_stream", 14, 32, 16, 1, 512, STREAM},
-    {"layer_16_rows_stream_w16", 15, 16, 16, 1, 1024, STREAM},
-    {"layer_32_rows_stream_w16", 16, 32, 16, 1, 1024, STREAM},
-    {"x_64_k2_s4", 17, 64, 64, 4, 256, DIRECT},
-    {"x_64_k2_s2", 18, 64, 64, 4, 256, DIRECT},
-    {"x_64_k2_s3", 19, 64, 64, 4, 256, DIRECT},
-    {"x_128_k2_s4", 20, 128, 128, 4, 512, DIRECT},
-    {"x_64x128_k2", 21, 64, 128, 4, 256, DIRECT},
 };
 constexpr int kNumLayer = sizeof(kLayer) / sizeof(kLayer[0]);
-enum { K_ANY_64, K_ANY_128, K_PIPE_64, K_PIPE_128, K_PIPE_256 };
+enum { K_ANY_64, K_ANY_128, K_64_DEEP, K_64, K_128_DEEP, K_128, K_256, K_256x128, K_ROWS, K_STREAM };
 
 // What the choice of a kernel looks at.
 struct LayerShape {
@@ -99,7 +91,7 @@ bool supports(int k, const LayerShape &s)
     if (s.M > kMaxTiled || s.N > kMaxTiled || s.K > kMaxTiled) return false;
     if ((f.loads == DIRECT || f.loads == STREAM) && !s.direct()) return false;
     if (f.loads == STREAM && (s.kind == dg::LAYER_WEIGHTS || !s.tb)) return false;
-    if (((k >= K_PIPE_256 && k < 10) || k>13) && f.loads == DIRECT && s.type == 0) return false;
+    if (s.type == 0 && (k == K_128_DEEP || k == K_256 || k == K_256x128)) return false;
     // the row kernels' columns of a B stored K x N go four together
     if (f.loads == ROWS && (s.kind == dg::LAYER_WEIGHTS || (!s.tb && s.N < 4))) return false;
     // a launch holds fewer than 2^32 threads
@@ -108,9 +100,9 @@ bool supports(int k, const LayerShape &s)
 
 int choose(const LayerShape &s)
 {
-    int k = s.direct() ? K_PIPE_64 : K_ANY_64;
-    if (most_tiles(s, kLayer[K_PIPE_128]) >= 256) k = s.direct() ? K_PIPE_128 : K_ANY_128;
-    if (s.direct() && s.type != 0 && most_tiles(s, kLayer[K_PIPE_256]) >= 256) k = K_PIPE_256;
+    int k = s.direct() ? K_64_DEEP : K_ANY_64;
+    if (most_tiles(s, kLayer[K_128]) >= 256) k = s.direct() ? K_128 : K_ANY_128;
+    if (s.direct() && s.type != 0 && most_tiles(s, kLayer[K_256]) >= 256) k = K_256;
     return supports(k, s) ? k : supports(K_ANY_128, s) ? K_ANY_128 : -1;
 }
 

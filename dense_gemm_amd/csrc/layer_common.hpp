@@ -46,56 +46,52 @@ typedef hipError_t (*layer_launch_fn)(const LayerParams &p, hipStream_t s);
 
 #ifdef __HIPCC__
 
-// erfc(z), z >= 0, with gauss = exp(-z^2).  For 16-bit results erfc(z) exp(z^2) as a
-// polynomial in t = 1 / (1 + 0.44 z), fitted here to the least largest relative
-// error over 0 <= z <= 9: 5.2e-6, a thousandth of a bf16 step also far out on
-// gelu's negative side, for one step more than gelu()'s polynomial (whose
-// absolute error of 1.5e-7 is 4e-4 of gelu at -4).  For fp32 results the
-// device library's erfcf.
-template <bool EXACT>
-__device__ __forceinline__ float erfc_pos(float z, float gauss)
+// Phi(-a) / exp(-a^2 / 2), a >= 0, for 16-bit results: half of erfc(z) exp(z^2), z = a /
+// sqrt 2, as a polynomial in t = 1 / (1 + 0.44 z), fitted here to the least largest
+// relative error over 0 <= z <= 9: 5.2e-6, a thousandth of a bf16 step also far out on
+// gelu's negative side (gelu()'s approximation, of one degree less, has an absolute
+// error of 1.5e-7, 4e-4 of gelu at -4).  fp32 results take the device library's erfcf.
+__device__ __forceinline__ float tail_ratio(float a)
 {
-    if constexpr (EXACT) {
-        return erfcf(z);
-    } else {
-        const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.44f, z, 1.f));
-        float poly = __builtin_fmaf(t, -0.14608541f, 0.35058573f);
-        poly = __builtin_fmaf(t, poly, 0.040815864f);
-        poly = __builtin_fmaf(t, poly, 0.26353481f);
-        poly = __builtin_fmaf(t, poly, 0.24258447f);
-        poly = __builtin_fmaf(t, poly, 0.24855939f);
-        return poly * t * gauss;
-    }
+    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.31112698f, a, 1.f));
+    float poly = __builtin_fmaf(t, -0.073042706f, 0.17529286f);
+    poly = __builtin_fmaf(t, poly, 0.020407932f);
+    poly = __builtin_fmaf(t, poly, 0.13176741f);
+    poly = __builtin_fmaf(t, poly, 0.12129223f);
+    poly = __builtin_fmaf(t, poly, 0.12427969f);
+    return poly * t;
 }
+// exp(-a^2 / 2)
+__device__ __forceinline__ float gauss(float a) { return __builtin_amdgcn_exp2f(a * -0.72134752f * a); }
 
-// act(x) of the forward pass: gelu(x) = x Phi(x) with Phi(x) = 1 - q/2 (x >= 0) or
-// q/2, q = erfc(|x| / sqrt 2), so that the negative side keeps its relative accuracy.
+// act(x) of the forward pass.  gelu(x) = x Phi(x) = max(x, 0) - |x| Phi(-|x|), so that the
+// negative side keeps its relative accuracy; |x| is cut at 16, where Phi(-|x|) is zero
+// in fp32 and an infinite |x| would not be.
 template <bool EXACT>
 __device__ __forceinline__ float layer_act(int act, float x)
 {
-    if (act == ACT_RELU) return x < 0.f ? 0.f : x;
+    const float m = x < 0.f ? 0.f : x;               // NaN stays
+    if (act == ACT_RELU) return m;
     if (act == ACT_GELU) {
-        const float z = __builtin_fabsf(x) * 0.70710678118654752f;
-        const float q = erfc_pos<EXACT>(z, EXACT ? 0.f : __expf(-z * z));
-        return x >= 0.f ? x * __builtin_fmaf(-0.5f, q, 1.f) : 0.5f * x * q;
+        const float a = __builtin_fminf(__builtin_fabsf(x), 16.f);
+        const float q = EXACT ? 0.5f * erfcf(a * 0.70710678118654752f) : tail_ratio(a) * gauss(a);
+        return __builtin_fmaf(-a, q, m);
     }
     return x;
 }
 
 // h * act'(x).  relu chooses h or 0 (an infinite or NaN h does not pass a unit
-// that is off; a NaN x gives NaN).  gelu' = Phi(x) + x phi(x); at |x| >= 16
-// phi underflows and x phi is 0, infinities included.
+// that is off; a NaN x gives NaN).  gelu'(x) = Phi(x) + x phi(x), which is s for
+// x < 0 and 1 - s for x >= 0 with s = Phi(-|x|) - |x| phi(x).
 template <bool EXACT>
 __device__ __forceinline__ float layer_act_grad(int act, float h, float x)
 {
     if (act == ACT_RELU) return x > 0.f ? h : (x <= 0.f ? 0.f : x);
     if (act == ACT_GELU) {
-        const float a = __builtin_fabsf(x), z = a * 0.70710678118654752f;
-        const float gauss = EXACT ? expf(-0.5f * x * x) : __expf(-z * z);
-        const float q = erfc_pos<EXACT>(z, gauss);
-        const float cdf = x >= 0.f ? __builtin_fmaf(-0.5f, q, 1.f) : 0.5f * q;
-        const float slope = a < 16.f ? __builtin_fmaf(x * 0.39894228040143268f, gauss, cdf) : cdf;
-        return h * slope;
+        const float a = __builtin_fabsf(x), cut = __builtin_fminf(a, 16.f) * 0.39894228040143268f;
+        const float s = EXACT ? __builtin_fmaf(-cut, expf(-0.5f * a * a), 0.5f * erfcf(a * 0.70710678118654752f))
+                              : gauss(a) * (tail_ratio(a) - cut);
+        return h * (x >= 0.f ? 1.f - s : s);
     }
     return h;
 }
@@ -278,17 +274,16 @@ __device__ __forceinline__ void walk_tiles(int in, int tiles_m, int tiles_n, int
     tn = r / rows;
 }
 
-// The tile of this workgroup, or false where the launch has more workgroups
-// than tiles.  The host does not know how many rows a group has: the launch
+// Tile `id` (a workgroup's, in launch order), or false where there are fewer tiles.  The host does not know how many rows a group has: the launch
 // holds one workgroup for every tile there can be, and a wave counts the groups'
 // tiles (64 groups at a time, a lane each) to find its own.
-__device__ __forceinline__ bool layer_tile(const LayerParams &p, int bm, int bn, LayerTile &t)
+__device__ __forceinline__ bool layer_tile(const LayerParams &p, int bm, int bn, int id, LayerTile &t)
 {
-    int id = blockIdx.x;
     t.group = 0;
     t.row0 = 0;
     if (p.kind == LAYER_WEIGHTS) {
         const int per = p.tiles_m * p.tiles_n;
+        if (id >= per * p.groups) return false;
         id = xcd_contiguous(id, per * p.groups);
         t.group = id / per;
         int tm, tn;
@@ -318,6 +313,7 @@ __device__ __forceinline__ bool layer_tile(const LayerParams &p, int bm, int bn,
     if (p.offsets == nullptr) {
         tiles_m = p.tiles_m;
         t.rows = p.M;
+        if (id >= tiles_m * p.tiles_n) return false;
         id = xcd_contiguous(id, tiles_m * p.tiles_n);
         if (p.splits > 1) {
             const int chunk = ((p.K + p.splits - 1) / p.splits + 63) & ~63;

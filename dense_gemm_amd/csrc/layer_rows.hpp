@@ -73,7 +73,7 @@ __global__ __launch_bounds__(64 * NWV) void layer_rows_kernel(LayerParams p)
     red_t *red = (red_t *)smem_raw;
 
     LayerTile t;
-    if (!layer_tile(p, 16 * MT, BN, t)) return;
+    if (!layer_tile(p, 16 * MT, BN, blockIdx.x, t)) return;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, q = lane >> 4;
     const int K = t.k_len, steps = K / KS;

@@ -8,7 +8,7 @@
 namespace dg {
 
 // [forward and gradient with B stored K x N, with B stored N x K, weights]
-#define DG_LAYER_PIPE(BM, BN, WM, WN, KG, STAGES, BK, RA, RB)                                  \
+#define DG_LAYER_PIPE(BM, BN, WM, WN, KG, STAGES, BK, RA, RB)                                \
     {(const void *)&layer_pipe_kernel<T, BM, BN, WM, WN, KG, false, false, STAGES, BK, RA, RB>,    \
      (const void *)&layer_pipe_kernel<T, BM, BN, WM, WN, KG, false, true, STAGES, BK, RA, RB>,     \
      (const void *)&layer_pipe_kernel<T, BM, BN, WM, WN, KG, true, false, STAGES, BK, RA, RB>}
@@ -29,41 +29,28 @@ const void *layer_kernel_of(int config, int variant)
         static const void *const table[][3] = {
             DG_LAYER_ANY(64, 64, 32, 32, 32),
             DG_LAYER_ANY(128, 128, 64, 64, 16),
+            DG_LAYER_PIPE(64, 64, 32, 32, 1, 4, 32, false, false),
             DG_LAYER_PIPE(64, 64, 32, 32, 1, 3, 32, false, false),
+            DG_LAYER_NONE,
             DG_LAYER_PIPE(128, 128, 64, 64, 1, 4, 16, false, false),
             DG_LAYER_NONE,
             DG_LAYER_NONE,
-            DG_LAYER_NONE,
             DG_LAYER_ROWS(1, 8),
-            DG_LAYER_ROWS(2, 8),
             DG_LAYER_STREAM(1, 8),
-            DG_LAYER_STREAM(2, 8),
-            DG_LAYER_STREAM(1, 16),
-            DG_LAYER_STREAM(2, 16),
-            DG_LAYER_PIPE(64, 64, 32, 32, 1, 4, 32, false, false),
-            DG_LAYER_NONE, DG_LAYER_NONE, DG_LAYER_NONE, DG_LAYER_NONE
         };
         return table[config][variant];
     } else {
         static const void *const table[][3] = {
             DG_LAYER_ANY(64, 64, 32, 32, 64),
             DG_LAYER_ANY(128, 128, 64, 64, 64),
-            DG_LAYER_PIPE(64, 64, 32, 32, 1, 4, 64, false, false),
+            DG_LAYER_PIPE(64, 64, 64, 32, 2, 4, 64, false, false),
+            DG_LAYER_PIPE(64, 64, 32, 32, 1, 2, 64, false, false),
+            DG_LAYER_PIPE(128, 128, 64, 64, 2, 4, 64, false, false),
             DG_LAYER_PIPE(128, 128, 64, 64, 1, 2, 64, false, false),
             DG_LAYER_PIPE(256, 256, 128, 64, 1, 2, 64, false, false),
             DG_LAYER_PIPE(256, 128, 128, 64, 1, 3, 32, false, false),
-            DG_LAYER_PIPE(256, 256, 128, 64, 1, 4, 32, false, false),
             DG_LAYER_ROWS(1, 8),
-            DG_LAYER_ROWS(2, 8),
             DG_LAYER_STREAM(1, 8),
-            DG_LAYER_STREAM(2, 8),
-            DG_LAYER_STREAM(1, 16),
-            DG_LAYER_STREAM(2, 16),
-            DG_LAYER_PIPE(64, 64, 64, 32, 2, 4, 64, false, false),
-            DG_LAYER_PIPE(64, 64, 64, 32, 2, 2, 64, false, false),
-            DG_LAYER_PIPE(64, 64, 64, 32, 2, 3, 64, false, false),
-            DG_LAYER_PIPE(128, 128, 64, 64, 2, 4, 64, false, false),
-            DG_LAYER_PIPE(64, 128, 64, 64, 2, 3, 64, false, false),
         };
         return table[config][variant];
     }

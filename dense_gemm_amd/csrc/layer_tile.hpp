@@ -18,28 +18,30 @@
 namespace dg {
 
 // ---- epilogue of a wave's blocks -----------------------------------------------
-// Strips of 32 rows x W columns (W = 32 * TN): the sums go to this wave's slot as
-// fp32 [32][W + 8], then a lane takes 8 columns of a row per pass, so that W / 8
-// lanes read and write a row's W columns in one piece.  What the epilogue reads
-// beside the sums is fetched before the strip is staged.
-template <int W> constexpr int kStripBytes = 32 * (W + 8) * 4;
+// Strips of SR rows x W columns (W = 32 * TN): the sums go to this wave's slot as fp32
+// [SR][W], then a lane takes 8 columns of a row per pass, so that W / 8 lanes read
+// and write a row's W columns in one piece.  The 16-byte chunk c of row r sits at c ^
+// strip_swz(r): the chunks that 16 lanes read together lie on all banks.  What the epilogue
+// reads beside the sums is fetched before the strip is staged.
+template <int W, int SR> constexpr int kStripBytes = SR * W * 4;
+template <int W> __device__ __forceinline__ int strip_swz(int r) { return W == 64 ? r & 1 : (r >> 1) & 1; }
 
-template <typename TC, int TM, int TN>
+template <typename TC, int SR, int TM, int TN>
 __device__ __forceinline__ void layer_store_as(const LayerParams &p, const LayerTile &t, lds_char_t *stg,
                                                const f32x16 (&acc)[TM][TN], int row0, int col0, int lane, bool partial)
 {
     typedef __attribute__((address_space(3))) float lds_float_t;
     typedef __attribute__((address_space(3))) f32x4 lds_f32x4_t;
-    constexpr int W = 32 * TN, LPR = W / 8, RPP = 64 / LPR, PASSES = 32 / RPP;
+    constexpr int W = 32 * TN, LPR = W / 8, RPP = 64 / LPR, PASSES = SR / RPP, PER32 = 32 / SR;
     // passes fetched together: half of an fp32 strip's, for the registers
-    constexpr int TOGETHER = sizeof(TC) == 4 && PASSES > 1 ? PASSES / 2 : PASSES;
+    constexpr int TOGETHER = sizeof(TC) == 4 && PASSES > 2 ? PASSES / 2 : PASSES;
     const int lc = (lane % LPR) * 8, col = col0 + lc;
     const bool whole = col0 + W <= p.N;
     float bias[8];
     if (whole && !partial) layer_bias<TC, 8>(p, t.group, col, bias);
 #pragma unroll 1
-    for (int i = 0; i < TM; ++i) {
-        const int rows = t.rows - row0 - 32 * i;         // of this strip on
+    for (int i = 0; i < TM * PER32; ++i) {
+        const int top = row0 + SR * i, rows = t.rows - top;      // of this strip on
         // (opaque to the compiler, which would otherwise keep every pass's addresses
         // in registers from strip to strip)
         int lr0 = lane / LPR, lane1 = lane;
@@ -49,20 +51,21 @@ __device__ __forceinline__ void layer_store_as(const LayerParams &p, const Layer
             if (whole && !partial) {
 #pragma unroll
                 for (int ps = 0; ps < TOGETHER; ++ps)
-                    if (lr0 + (from + ps) * RPP < rows) aux[ps].fetch(p, t, row0 + 32 * i + lr0 + (from + ps) * RPP, col);
+                    if (lr0 + (from + ps) * RPP < rows) aux[ps].fetch(p, t, top + lr0 + (from + ps) * RPP, col);
             }
         };
         fetch(0);
         // register r of lane l holds row 8*(r/4) + 4*(l/32) + r%4, column l%32
 #pragma unroll
-        for (int s = 0; s < TM; ++s)
+        for (int s = 0; s < TM * PER32; ++s)
             if (s == i) {
 #pragma unroll
                 for (int j = 0; j < TN; ++j)
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) {
+                    for (int r = 0; r < SR / 2; ++r) {
                         const int row = 8 * (r >> 2) + (lane >> 5) * 4 + (r & 3);
-                        *(lds_float_t *)(stg + (row * (W + 8) + 32 * j + (lane & 31)) * 4) = acc[s][j][r];
+                        *(lds_float_t *)(stg + (row * W + ((32 * j + (lane & 31)) ^ (strip_swz<W>(row) << 2))) * 4) =
+                            acc[s / PER32][j][s % PER32 * (SR / 2) + r];
                     }
             }
         __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): the strip is staged
@@ -75,31 +78,31 @@ __device__ __forceinline__ void layer_store_as(const LayerParams &p, const Layer
                 float v[8];
 #pragma unroll
                 for (int c4 = 0; c4 < 2; ++c4) {
-                    const f32x4 x = *(const lds_f32x4_t *)(stg + (lr * (W + 8) + lc + 4 * c4) * 4);
+                    const f32x4 x = *(const lds_f32x4_t *)(stg + (lr * W + ((lc + 4 * c4) ^ (strip_swz<W>(lr) << 2))) * 4);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) v[4 * c4 + e] = x[e];
                 }
                 if (lr < rows) {
-                    if (partial) layer_partial<8>(p, t, row0 + 32 * i + lr, col, v);
-                    else layer_finish<TC, 8>(p, t, row0 + 32 * i + lr, col, v, aux[ps % TOGETHER], bias);
+                    if (partial) layer_partial<8>(p, t, top + lr, col, v);
+                    else layer_finish<TC, 8>(p, t, top + lr, col, v, aux[ps % TOGETHER], bias);
                 }
                 __builtin_amdgcn_sched_barrier(0);    // a pass's registers at a time
             }
         } else {
             // the last columns: one element a lane
 #pragma unroll 1
-            for (int at = lane1; at < 32 * W; at += 64) {
+            for (int at = lane1; at < SR * W; at += 64) {
                 const int lr = at / W, c = at % W;
                 if (lr >= rows || col0 + c >= p.N) continue;
-                float v[1] = {*(const lds_float_t *)(stg + (lr * (W + 8) + c) * 4)};
+                float v[1] = {*(const lds_float_t *)(stg + (lr * W + (c ^ (strip_swz<W>(lr) << 2))) * 4)};
                 if (partial) {
-                    layer_partial<1>(p, t, row0 + 32 * i + lr, col0 + c, v);
+                    layer_partial<1>(p, t, top + lr, col0 + c, v);
                 } else {
                     float b[1];
                     LayerAux<TC, 1> x;
                     layer_bias<TC, 1>(p, t.group, col0 + c, b);
-                    x.fetch(p, t, row0 + 32 * i + lr, col0 + c);
-                    layer_finish<TC, 1>(p, t, row0 + 32 * i + lr, col0 + c, v, x, b);
+                    x.fetch(p, t, top + lr, col0 + c);
+                    layer_finish<TC, 1>(p, t, top + lr, col0 + c, v, x, b);
                 }
             }
         }
@@ -108,13 +111,13 @@ __device__ __forceinline__ void layer_store_as(const LayerParams &p, const Layer
     }
 }
 
-template <typename T, int TM, int TN>
+template <typename T, int SR, int TM, int TN>
 __device__ __forceinline__ void layer_store(const LayerParams &p, const LayerTile &t, lds_char_t *stg,
                                             const f32x16 (&acc)[TM][TN], int row0, int col0, int lane)
 {
-    if (p.splits > 1) layer_store_as<float>(p, t, stg, acc, row0, col0, lane, true);
-    else if (sizeof(T) == 2 && p.ctype != 0) layer_store_as<T>(p, t, stg, acc, row0, col0, lane, false);
-    else layer_store_as<float>(p, t, stg, acc, row0, col0, lane, false);
+    if (p.splits > 1) layer_store_as<float, SR>(p, t, stg, acc, row0, col0, lane, true);
+    else if (sizeof(T) == 2 && p.ctype != 0) layer_store_as<T, SR>(p, t, stg, acc, row0, col0, lane, false);
+    else layer_store_as<float, SR>(p, t, stg, acc, row0, col0, lane, false);
 }
 
 // ---- operands -------------------------------------------------------------------------
@@ -149,7 +152,6 @@ struct SlabOperandH {
         const int p = (b % ROW_BYTES) >> 4;
         c = KCONT ? (p ^ swz(r)) * 8 : (((p >> 2) ^ swz(r)) << 5) + (p & 3) * 8;
     }
-    __device__ __forceinline__ void advance() { base += step; }
     __device__ __forceinline__ void issue_one(lds_char_t *lds, int wave, int i)
     {
         load_lds16(off[i], buffer_rsrc(base), (unsigned)(uintptr_t)(lds + (i * NW + wave) * SPAN));
@@ -241,14 +243,12 @@ struct LayerOperand : std::conditional<sizeof(T) == 2, SlabOperandH<T, BMN, KCON
         static_assert(!REG, "direct loads");
 #pragma unroll
         for (int i = 0; i < Base::LOADS; ++i) this->issue_one(lds, wave, i);
-        this->advance();
     }
     __device__ __forceinline__ void fetch()
     {
         static_assert(REG, "loads into registers");
 #pragma unroll
         for (int i = 0; i < Base::LOADS; ++i) held[i] = *(const Vu *)(this->base + far[i]);
-        this->advance();
     }
     __device__ __forceinline__ void commit(lds_char_t *lds, int wave, int lane) const
     {
@@ -279,8 +279,11 @@ struct LayerOperand : std::conditional<sizeof(T) == 2, SlabOperandH<T, BMN, KCON
             }
             *(lds_v_t *)(lds + b) = v;
         }
-        this->advance();
     }
+
+    // on to the next slab (without a branch, in which the compiler would merge the
+    // two operands' and keep their addresses in memory)
+    __device__ __forceinline__ void skip(bool on) { this->base += on ? this->step : 0; }
 };
 
 template <typename V8>
@@ -315,26 +318,25 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * KG, 2) void layer_pipe
     // direct loads of a slab, by operand
     constexpr int LA = RA ? 0 : OpA::LOADS, LBN = RB ? 0 : OpB::LOADS, LOADS = LA + LBN, STAGE = OpA::BYTES + OpB::BYTES;
     constexpr int PA = LA ? LA : 1, PB = LBN ? LBN : 1, PL = LOADS ? LOADS : 1;     // divisors
-    constexpr int RING = STAGES * STAGE, STRIPS = NW * kStripBytes<WN>;
-    static_assert((RING > STRIPS ? RING : STRIPS) <= 160 * 1024, "the ring and the strips fit the LDS");
+    constexpr int SR = 32, RING = STAGES * STAGE, STRIPS = NW * kStripBytes<WN, SR>, SMEM = RING > STRIPS ? RING : STRIPS;
+    static_assert(SMEM <= 160 * 1024, "the ring and the strips fit the LDS");
     static_assert((STAGES - 2) * LOADS + LA < 64, "the loads in flight can be counted");
-    __shared__ __attribute__((aligned(1024))) char smem_raw[RING > STRIPS ? RING : STRIPS];
+    __shared__ __attribute__((aligned(1024))) char smem_raw[SMEM];
     lds_char_t *smem = (lds_char_t *)smem_raw;
 
     LayerTile t;
-    if (!layer_tile(p, BM, BN, t)) return;
+    if (!layer_tile(p, BM, BN, blockIdx.x, t)) return;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int kgroup = wave / NWG, wm0 = (wave % NWG / WAVES_N) * WM, wn0 = (wave % WAVES_N) * WN;
+    OpA ga;
+    OpB gb;
     const T *A = (const T *)p.A + (DW ? (t.row0 + t.k0) * p.lda : t.row0 * p.lda + t.k0);
     const T *B = (const T *)p.B + (DW ? (t.row0 + t.k0) * p.ldb
                                       : t.group * p.strideB + (TB ? (int64_t)t.k0 : t.k0 * p.ldb));
     const int nk = (t.k_len + BK - 1) / BK, krem = t.k_len - (nk - 1) * BK;
     int nfull = OpA::ragged(krem, t.rows) || OpB::ragged(krem, p.N) ? nk - 1 : nk;
     if (OpA::narrow(t.rows) || OpB::narrow(p.N)) nfull = 0;
-
-    OpA ga;
-    OpB gb;
     ga.init(A, p.lda, t.m0, t.rows, wave, lane);
     gb.init(B, p.ldb, t.n0, p.N, wave, lane);
     auto slab_tail = [&](lds_char_t *st, int slab) {
@@ -344,20 +346,40 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * KG, 2) void layer_pipe
     };
 
     f32x16 acc[TM][TN];
+    float sums[TM];
 #pragma unroll
-    for (int i = 0; i < TM; ++i)
+    for (int i = 0; i < TM; ++i) {
+        sums[i] = 0.f;
 #pragma unroll
         for (int j = 0; j < TN; ++j)
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
-
+    }
     // weights: the first tile column adds up A's columns for the bias's gradient from
     // the fragments that it multiplies, each step in one of the waves that share them
-    float sums[TM];
-#pragma unroll
-    for (int i = 0; i < TM; ++i) sums[i] = 0.f;
     const bool summing = DW && p.dbias && t.n0 == 0;
     const int wcol = wave % WAVES_N;
+    auto add_up = [&]() {
+        // [wave][32 * strip + row]: added over the waves that share the rows, in order
+        typedef __attribute__((address_space(3))) float lds_float_t;
+        lds_float_t *red = (lds_float_t *)smem;
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+            const float both = sums[i] + __shfl_xor(sums[i], 32);     // the lane halves' parts of the sum
+            if (lane < 32) red[wave * WM + 32 * i + lane] = both;
+        }
+        __syncthreads();
+        for (int m = threadIdx.x; m < BM; m += 64 * NW) {
+            if (t.m0 + m >= p.M) break;
+            float v = 0.f;
+#pragma unroll
+            for (int g = 0; g < KG; ++g)
+#pragma unroll
+                for (int c = 0; c < WAVES_N; ++c) v += red[(g * NWG + m / WM * WAVES_N + c) * WM + m % WM];
+            layer_dbias(p, t.group, t.m0 + m, v);
+        }
+        __syncthreads();
+    };
 
     if constexpr (H) {
         typedef T V8 __attribute__((ext_vector_type(8)));
@@ -388,6 +410,8 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * KG, 2) void layer_pipe
             } else if (s < nk) {
                 slab_tail(st, s);
             }
+            ga.skip(s < nk);
+            if (RB || s < STAGES - 1) gb.skip(s < nk);
         }
         if (!(RA || RB) && nfull >= STAGES) wait_vmcnt<(STAGES - 2) * LOADS + LA>();
         else wait_vmcnt<0>();
@@ -430,7 +454,7 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * KG, 2) void layer_pipe
                         acc[i][j] = mfma_32x32x16(fa[cur][i], fb[cur][j], acc[i][j]);
                         __builtin_amdgcn_sched_barrier(0);
                     }
-                if (s == 0 && pend && !RB) gb.advance();
+                if (s == 0 && !RB) gb.skip(FAST || kt + STAGES - 1 < nk);
             }
             if constexpr (RA) {
                 if (pend) ga.commit(prev, wave, lane);
@@ -478,7 +502,8 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * KG, 2) void layer_pipe
                     acc[i][j] = mfma_32x32x16(fa[cur][i], fb[cur][j], acc[i][j]);
                     __builtin_amdgcn_sched_barrier(0);
                 }
-            if (more && !RA) ga.advance();
+            ga.skip(FAST || kt + STAGES < nk);
+            if (RB) gb.skip(FAST || kt + STAGES < nk);
         };
         int kt = 0;
         for (; kt + STAGES < nfull; ++kt) slab(std::true_type(), kt);
@@ -503,6 +528,8 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * KG, 2) void layer_pipe
             } else if (s < nk) {
                 slab_tail(st, s);
             }
+            ga.skip(s < nk);
+            gb.skip(s < nk);
         }
         int stage = 0;
         // FAST: slab kt + STAGES - 1 is whole
@@ -555,10 +582,10 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * KG, 2) void layer_pipe
             }
             if (more) {
                 if constexpr (RA) ga.commit(dst, wave, lane);
-                else ga.advance();
                 if constexpr (RB) gb.commit(dst + OpA::BYTES, wave, lane);
-                else gb.advance();
             }
+            ga.skip(FAST || ns < nk);
+            gb.skip(FAST || ns < nk);
             stage = stage + 1 == STAGES ? 0 : stage + 1;
         };
         int kt = 0;
@@ -567,29 +594,9 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * KG, 2) void layer_pipe
     }
     wait_vmcnt<0>();
     __syncthreads();                   // every wave is done with the ring
-    if (DW && summing) {
-        // [wave][32 * strip + row]: added over the waves that share the rows, in order
-        typedef __attribute__((address_space(3))) float lds_float_t;
-        lds_float_t *red = (lds_float_t *)smem;
-#pragma unroll
-        for (int i = 0; i < TM; ++i) {
-            const float both = sums[i] + __shfl_xor(sums[i], 32);     // the lane halves' parts of the sum
-            if (lane < 32) red[wave * WM + 32 * i + lane] = both;
-        }
-        __syncthreads();
-        for (int m = threadIdx.x; m < BM; m += 64 * NW) {
-            if (t.m0 + m >= p.M) break;
-            float v = 0.f;
-#pragma unroll
-            for (int g = 0; g < KG; ++g)
-#pragma unroll
-                for (int c = 0; c < WAVES_N; ++c) v += red[(g * NWG + m / WM * WAVES_N + c) * WM + m % WM];
-            layer_dbias(p, t.group, t.m0 + m, v);
-        }
-        __syncthreads();
-    }
+    if (summing) add_up();
     if constexpr (KG == 1) {
-        layer_store<T>(p, t, smem + wave * kStripBytes<WN>, acc, t.m0 + wm0, t.n0 + wn0, lane);
+        layer_store<T, SR>(p, t, smem + wave * kStripBytes<WN, SR>, acc, t.m0 + wm0, t.n0 + wn0, lane);
     } else {
         // the two K groups' sums: each wave keeps half of the strips and hands the
         // other half to its partner, the same part of the tile in the other group
@@ -622,7 +629,7 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * KG, 2) void layer_pipe
                     for (int e = 0; e < 4; ++e) mine[i][j][4 * c + e] += x[e];
                 }
         __syncthreads();               // read before the strips are staged
-        layer_store<T>(p, t, smem + wave * kStripBytes<WN>, mine, t.m0 + wm0 + 32 * HS * kgroup, t.n0 + wn0, lane);
+        layer_store<T, SR>(p, t, smem + wave * kStripBytes<WN, SR>, mine, t.m0 + wm0 + 32 * HS * kgroup, t.n0 + wn0, lane);
     }
 }
 

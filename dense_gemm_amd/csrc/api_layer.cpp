@@ -63,6 +63,7 @@ struct LayerShape {
     int kind, type;
     bool tb, ragged;
     int64_t groups, M, N, K;      // as LayerParams
+    bool out32;                   // C is fp32
     bool direct_a, direct_b;      // the direct loads take the operand
     bool direct() const { return direct_a && direct_b; }
 };
@@ -74,42 +75,99 @@ bool direct_ok(const void *x, int64_t ld, int64_t stride, int64_t bytes)
     return ((uintptr_t)x & 3) == 0 && ld * bytes % 4 == 0 && stride * bytes % 4 == 0 && 256 * ld * bytes < ((int64_t)1 << 31);
 }
 
+// Tiles are powers of two wide.
+int log2_of(int x) { return __builtin_ctz((unsigned)x); }
+int64_t tiles_of(int64_t x, int b) { return (x + b - 1) >> log2_of(b); }
 int bn_of(const LayerFamily &f, const LayerShape &s) { return f.loads == ROWS && !s.tb ? 64 : f.bn; }
 
 // The most tiles a launch can have: each group that has rows ends in a partial tile.
 int64_t most_tiles(const LayerShape &s, const LayerFamily &f)
 {
-    const int64_t tn = ceil_div(s.N, bn_of(f, s));
-    if (s.kind == dg::LAYER_WEIGHTS) return s.groups * ceil_div(s.M, f.bm) * tn;
+    const int64_t tn = tiles_of(s.N, bn_of(f, s));
+    if (s.kind == dg::LAYER_WEIGHTS) return s.groups * tiles_of(s.M, f.bm) * tn;
     const int64_t used = s.ragged && s.groups < s.M ? s.groups : s.ragged ? s.M : 1;
-    return (s.M + used * (f.bm - 1)) / f.bm * tn;
+    return ((s.M + used * (f.bm - 1)) >> log2_of(f.bm)) * tn;
 }
 
 bool supports(int k, const LayerShape &s)
 {
     const LayerFamily &f = kLayer[k];
     if (s.M > kMaxTiled || s.N > kMaxTiled || s.K > kMaxTiled) return false;
+    const bool dw = s.kind == dg::LAYER_WEIGHTS;
     if ((f.loads == DIRECT || f.loads == STREAM) && !s.direct()) return false;
-    if (f.loads == STREAM && (s.kind == dg::LAYER_WEIGHTS || !s.tb)) return false;
+    if (f.loads == STREAM && (dw || !s.tb)) return false;
     if (s.type == 0 && (k == K_128_DEEP || k == K_256 || k == K_256x128)) return false;
     // the row kernels' columns of a B stored K x N go four together
-    if (f.loads == ROWS && (s.kind == dg::LAYER_WEIGHTS || (!s.tb && s.N < 4))) return false;
+    if (f.loads == ROWS && (dw || (!s.tb && s.N < 4))) return false;
     // a launch holds fewer than 2^32 threads
-    return most_tiles(s, f) * f.threads < ((int64_t)1 << 32) && most_tiles(s, f) < kMaxDim;
+    return most_tiles(s, f) * f.threads < ((int64_t)1 << 32);
 }
 
-int choose(const LayerShape &s)
-{
-    int k = s.direct() ? K_64_DEEP : K_ANY_64;
-    if (most_tiles(s, kLayer[K_128]) >= 256) k = s.direct() ? K_128 : K_ANY_128;
-    if (s.direct() && s.type != 0 && most_tiles(s, kLayer[K_256]) >= 256) k = K_256;
-    return supports(k, s) ? k : supports(K_ANY_128, s) ? K_ANY_128 : -1;
-}
+// A kernel's time (us): fixed + (tile + slab * (slabs of 64 summed indices)) for as many
+// rounds as the tiles need, `share` of them a round, + C's megabytes times `out`.
+// Fitted to the times, replayed in a graph, of 6338 random problems (1 to 16384 rows,
+// 32 to 6000 columns and summed indices, 0 to 64 groups, aligned and not, all types).
+// Over these, with the K ranges below, the choice is 3% slower than the fastest kernel
+// and ranges by geometric mean, 24% at the 95th of a hundred, 1.8 times at the worst.
+// Both sides of some choices (M x N x K, bf16, nt, us): 32 x 2048 x 2048 stream 5.6, 64 deep 10.1; 512 x
+// 5632 x 2048 128 deep 19, 64 deep 23, 256 46; 16384 x 5632 x 2048 256 343, 128 388.
+struct LayerTime {
+    double fixed, tile, slab, share, out;
+};
+const LayerTime kTime16[kNumLayer] = {
+    {7.05, 0.05, 0.481, 347, 0.457}, {14.6, 0.05, 0.839, 250, 0.484}, {7.34, 0.29, 0.195, 161, 0.840},
+    {6.94, 0.05, 0.331, 267, 0.441}, {9.83, 0.83, 0.446, 159, 0.743}, {13.1, 0.05, 0.600, 199, 0.494},
+    {22.7, 1.06, 1.173, 138, 0.384}, {20.4, 0.05, 0.850, 174, 0.375}, {4.13, 0.30, 0.176, 175, 1.712},
+    {3.67, 0.40, 0.040, 146, 0.665},
+};
+const LayerTime kTime32[kNumLayer] = {
+    {7.17, 0.05, 1.403, 221, 0.020}, {12.5, 0.05, 5.162, 236, 0.067}, {6.87, 0.05, 1.189, 235, 0.337},
+    {7.06, 0.05, 1.173, 239, 0.163}, {}, {14.1, 0.05, 3.926, 203, 0.097},
+    {}, {}, {4.02, 0.14, 0.388, 157, 0.686}, {3.56, 0.48, 0.126, 192, 0.459},
+};
+// K_ROWS with a B stored N x K, which it takes where its rows are not aligned.
+const LayerTime kTimeRowsT = {3.58, 0.09, 0.220, 207, 2.0};
 
-int resolve_splits(const LayerShape &s, int splits)
+// A split sum's second launch and its partials' way out and back.
+constexpr double kJoin = 2.9, kJoinMb = 0.45;
+
+// The kernel, and with *splits = 0 the K ranges, of least time; a forced kernel or
+// number of ranges stays.  More than one range has to gain a tenth.
+int choose(const LayerShape &s, int kernel, int *splits)
 {
-    if (s.kind != dg::LAYER_WEIGHTS && s.ragged) return 1;
-    return splits < 1 ? 1 : splits;
+    const bool dw = s.kind == dg::LAYER_WEIGHTS;
+    const double groups = dw ? (double)s.groups : 1, mb = groups * (double)s.M * (double)s.N * 4e-6;
+    const double K = dw && s.ragged ? (double)s.K / (double)s.groups : (double)s.K;
+    const double used = (double)(s.groups < s.M ? s.groups : s.M);
+    const bool may_split = dw || !s.ragged;
+    double best = 1e300;
+    int k_best = -1, n_best = 1;
+    for (int k = kernel == DG_KERNEL_AUTO ? 0 : kernel; k < (kernel == DG_KERNEL_AUTO ? kNumLayer : kernel + 1); ++k) {
+        if (k < 0 || k >= kNumLayer || !supports(k, s)) continue;
+        const LayerFamily &f = kLayer[k];
+        const LayerTime &m = s.type == 0 ? kTime32[k] : k == K_ROWS && s.tb ? kTimeRowsT : kTime16[k];
+        // the tiles to expect: each group ends in half of one
+        const double tn = (double)tiles_of(s.N, bn_of(f, s)), rows = (double)s.M / f.bm;
+        const double tiles = dw ? groups * (double)tiles_of(s.M, f.bm) * tn
+                                : !s.ragged ? (double)tiles_of(s.M, f.bm) * tn
+                                            : (rows > used / 2 ? rows + used / 2 : used) * tn;
+        static const int kRanges[] = {1, 2, 3, 4, 6, 8, 12, 16};
+        const int many = *splits > 0 || !may_split || f.loads >= ROWS || tiles > 512 || K < 512 ? 1 : 8;
+        for (int i = 0; i < many; ++i) {
+            const int n = *splits > 0 ? *splits : kRanges[i];
+            if (i > 0 && (64. * n > K || tiles * n > 2048)) break;
+            const double slabs = K <= 64. * n ? 1 : K / n / 64, rounds = tiles * n / m.share;
+            double t = m.fixed + (m.tile + m.slab * slabs) * (rounds > 1 ? rounds : 1);
+            t += n == 1 ? m.out * mb * (s.out32 ? 1 : 0.5) : kJoin + kJoinMb * mb * n + 0.1 * t;
+            if (t < best) {
+                best = t;
+                k_best = k;
+                n_best = n;
+            }
+        }
+    }
+    *splits = may_split ? n_best : 1;
+    return k_best;
 }
 
 size_t workspace_bytes_of(int64_t groups, int64_t M, int64_t N, int splits)
@@ -121,10 +179,12 @@ size_t workspace_bytes_of(int64_t groups, int64_t M, int64_t N, int splits)
 int launch(LayerParams &p, const LayerShape &s, int dtype, int kernel, int splits, void *ws, size_t ws_bytes, int ws_arg,
            hipStream_t stream)
 {
-    if (kernel == DG_KERNEL_AUTO) kernel = choose(s);
-    if (kernel < 0 || kernel >= kNumLayer || !supports(kernel, s)) return DG_ERR_UNSUPPORTED;
+    // without a workspace, one range where the choice is the library's
+    if (splits == 0 && ws == nullptr) splits = 1;
+    kernel = choose(s, kernel, &splits);
+    if (kernel < 0) return DG_ERR_UNSUPPORTED;
     const LayerFamily &f = kLayer[kernel];
-    p.splits = resolve_splits(s, splits);
+    p.splits = splits;
     p.ws = (float *)ws;
     if (p.splits > 1) {
         if (bad_ptr(ws, 16)) return -ws_arg;
@@ -214,7 +274,7 @@ int rows_product(const RowsCall &c, LayerParams &p, F between)
     p.C = c.C;
     p.ldc = c.ldc;
     p.ctype = output_type(c.dtype);
-    const LayerShape s = {p.kind, operand_type(c.dtype), c.transB == DG_OP_T, c.offsets != nullptr, c.groups, c.M, c.N, p.K,
+    const LayerShape s = {p.kind, operand_type(c.dtype), c.transB == DG_OP_T, c.offsets != nullptr, c.groups, c.M, c.N, p.K, cb == 4,
                           direct_ok(c.A, c.lda, 0, eb), direct_ok(c.B, c.ldb, c.strideB, eb)};
     return launch(p, s, c.dtype, c.kernel, c.splits, c.workspace, c.workspace_bytes, 25, (hipStream_t)c.stream);
 }
@@ -349,7 +409,7 @@ int dg_gemm_dw_with_kernel(int64_t groups, const int32_t *offsets, int64_t rows,
         LayerParams q = p;
         if (!reads) q.K = 0;
         if (alone) q.dbias = nullptr;
-        const LayerShape s = {p.kind, operand_type(dtype), false, offsets != nullptr, groups, M, N, q.K,
+        const LayerShape s = {p.kind, operand_type(dtype), false, offsets != nullptr, groups, M, N, q.K, cb == 4,
                               direct_ok(A, lda, 0, eb), direct_ok(B, ldb, 0, eb)};
         const int rc = launch(q, s, dtype, kernel, splits, workspace, workspace_bytes, 18, (hipStream_t)stream);
         if (rc != DG_OK) return rc;
@@ -373,8 +433,11 @@ int dg_gemm_fused_choose(int64_t M, int64_t N, int64_t K, dg_op_t transB, dg_dty
     if (transB != DG_OP_N && transB != DG_OP_T) return -4;
     if (!is_dtype(dtype)) return -5;
     if (M == 0 || N == 0) return 1;
-    const LayerShape s = {dg::LAYER_FORWARD, operand_type(dtype), transB == DG_OP_T, false, 1, M, N, K, true, true};
-    return resolve_splits(s, 0);
+    const LayerShape s = {dg::LAYER_FORWARD, operand_type(dtype), transB == DG_OP_T, false, 1, M, N, K, output_type(dtype) == 0, true,
+                          true};
+    int splits = 0;
+    choose(s, DG_KERNEL_AUTO, &splits);
+    return splits;
 }
 
 int dg_gemm_dw_choose(int64_t groups, int64_t rows, int64_t M, int64_t N, dg_dtype_t dtype)
@@ -385,8 +448,11 @@ int dg_gemm_dw_choose(int64_t groups, int64_t rows, int64_t M, int64_t N, dg_dty
     if (N < 0 || N > kMaxDim) return -4;
     if (!is_dtype(dtype)) return -5;
     if (groups == 0 || M == 0 || N == 0) return 1;
-    const LayerShape s = {dg::LAYER_WEIGHTS, operand_type(dtype), false, groups > 1, groups, M, N, rows, true, true};
-    return resolve_splits(s, 0);
+    const LayerShape s = {dg::LAYER_WEIGHTS, operand_type(dtype), false, groups > 1, groups, M, N, rows, output_type(dtype) == 0,
+                          true, true};
+    int splits = 0;
+    choose(s, DG_KERNEL_AUTO, &splits);
+    return splits;
 }
 
 size_t dg_layer_workspace_size(int64_t groups, int64_t M, int64_t N, int splits)

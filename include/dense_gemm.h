@@ -465,9 +465,9 @@ size_t dg_act_backward_workspace_size(int64_t rows, int64_t cols);
  * Z not stored.  R may be C itself (ldr = ldc); otherwise outputs must not
  * overlap anything else.  beta == 0: R is not read.  K == 0 or alpha == 0: A and
  * B are not read.  M == 0 or N == 0 or groups == 0: nothing is done.
- *   splits: K ranges, as dg_gemm_splitk (0: the library's choice,
- *   dg_gemm_fused_choose; always one with offsets); their fp32 sums go to the
- *   workspace of dg_layer_workspace_size(1, M, N, splits) bytes.
+ *   splits: K ranges, as dg_gemm_splitk (0: the library's choice, which is one
+ *   range without a workspace; dg_gemm_fused_choose; always one with offsets); their
+ *   fp32 sums go to the workspace of dg_layer_workspace_size(1, M, N, splits) bytes.
  *   DG_ERR_UNSUPPORTED: M, N or K above 2^31 - 1025, or more tiles than a launch
  *   holds (2^32 / 256 of 64 x 64).
  *   1 transB, 2 groups, 3 offsets, 4 M, 5 N, 6 K, 7 alpha, 8 A, 9 lda, 10 B, 11 ldb,
@@ -500,7 +500,7 @@ int dg_gemm_act_grad(dg_op_t transB, int64_t groups, const int32_t *offsets, int
  * for each group, contiguous; NULL for none) receives the column sums of A_g, +
  * beta * dbias_g, unscaled by alpha.  A group without rows: beta * C_g and beta *
  * dbias_g.  beta == 0: C and dbias are not read; alpha == 0: B is not read.
- *   splits: ranges of each group's rows (0: the library's choice,
+ *   splits: ranges of each group's rows (0: the library's choice, as dg_gemm_fused;
  *   dg_gemm_dw_choose), their fp32 sums in the workspace of
  *   dg_layer_workspace_size(groups, M, N, splits) bytes.
  *   DG_ERR_UNSUPPORTED as dg_gemm_fused.

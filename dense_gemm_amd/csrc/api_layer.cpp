@@ -104,29 +104,32 @@ bool supports(int k, const LayerShape &s)
 }
 
 // A kernel's time (us): fixed + (tile + slab * (slabs of 64 summed indices)) for as many
-// rounds as the tiles need, `share` of them a round, + C's megabytes times `out`.
-// Fitted to the times, replayed in a graph, of 6338 random problems (1 to 16384 rows,
-// 32 to 6000 columns and summed indices, 0 to 64 groups, aligned and not, all types).
-// Over these, with the K ranges below, the choice is 3% slower than the fastest kernel
-// and ranges by geometric mean, 24% at the 95th of a hundred, 1.8 times at the worst.
-// Both sides of some choices (M x N x K, bf16, nt, us): 32 x 2048 x 2048 stream 5.6, 64 deep 10.1; 512 x
-// 5632 x 2048 128 deep 19, 64 deep 23, 256 46; 16384 x 5632 x 2048 256 343, 128 388.
+// rounds as the tiles need, `share` of them a round, but no less than the weights'
+// megabytes times `read`; + C's megabytes times `out`.  Fitted to the times, replayed
+// in a graph, of 12182 random problems (1 to 16384 rows, 32 to 6000 columns and summed
+// indices, 0 to 64 groups, aligned and not, all types).  Over these, with the K ranges
+// below, the choice is 3% slower than the fastest kernel and ranges by geometric mean,
+// 21% at the 95th of a hundred, 2.8 times at the worst (64 groups with half a row each, K =
+// 33).  Both sides of some choices (bf16, B stored N x K, M x N x K, us): 24 x 2048 x 5632 stream 12.5, 64
+// deep in 6 ranges and their join 11.6, in one 18.9; 512 x 5632 x 2048 128 deep 22, 64 deep
+// 27; 16384 x 5632 x 2048 256 343, 128 388; 8 groups of 2048 rows, 5632 x 2048 fp32 weight
+// gradients 256 x 128 524, 256 547.
 struct LayerTime {
-    double fixed, tile, slab, share, out;
+    double fixed, tile, slab, share, out, read;
 };
 const LayerTime kTime16[kNumLayer] = {
-    {7.05, 0.05, 0.481, 347, 0.457}, {14.6, 0.05, 0.839, 250, 0.484}, {7.34, 0.29, 0.195, 161, 0.840},
-    {6.94, 0.05, 0.331, 267, 0.441}, {9.83, 0.83, 0.446, 159, 0.743}, {13.1, 0.05, 0.600, 199, 0.494},
-    {22.7, 1.06, 1.173, 138, 0.384}, {20.4, 0.05, 0.850, 174, 0.375}, {4.13, 0.30, 0.176, 175, 1.712},
-    {3.67, 0.40, 0.040, 146, 0.665},
+    {6.68, 1.12, 0.581, 466, 0.168, 0.226}, {19.5, 2.46, 1.04, 366, 0.256, 0.217}, {7.27, 1.33, 0.205, 187, 0.011, 0.193},
+    {6.39, 0.969, 0.486, 467, 0.210, 0.209}, {10.7, 3.51, 0.414, 158, 0.165, 0.207}, {16.2, 2.28, 0.879, 342, 0.276, 0.198},
+    {26.8, 3.28, 1.3, 163, 0.301, 0.257}, {30.7, 0.05, 0.877, 202, 0.375, 0.222}, {4.29, 0.05, 0.203, 150, 1.867, 0.160},
+    {3.58, 0.421, 0.0436, 155, 2.0, 0.146},
 };
 const LayerTime kTime32[kNumLayer] = {
-    {7.17, 0.05, 1.403, 221, 0.020}, {12.5, 0.05, 5.162, 236, 0.067}, {6.87, 0.05, 1.189, 235, 0.337},
-    {7.06, 0.05, 1.173, 239, 0.163}, {}, {14.1, 0.05, 3.926, 203, 0.097},
-    {}, {}, {4.02, 0.14, 0.388, 157, 0.686}, {3.56, 0.48, 0.126, 192, 0.459},
+    {7.73, 0, 1.396, 256, 0.124, 0.271}, {19.3, 0, 5.0, 256, 0.1, 0.503}, {7.5, 0, 1.11, 256, 0.471, 0.304},
+    {8.03, 0, 1.086, 256, 0.233, 0.282}, {}, {21.2, 0, 4.06, 256, 0.152, 0.382},
+    {}, {}, {4.41, 0.05, 0.385, 141, 0.9, 0.161}, {3.7, 0.398, 0.124, 194, 2.0, 0.153},
 };
 // K_ROWS with a B stored N x K, which it takes where its rows are not aligned.
-const LayerTime kTimeRowsT = {3.58, 0.09, 0.220, 207, 2.0};
+const LayerTime kTimeRowsT = {4.1, 0.0874, 0.225, 293, 2.0, 0.361};
 
 // A split sum's second launch and its partials' way out and back.
 constexpr double kJoin = 2.9, kJoinMb = 0.45;
@@ -136,9 +139,10 @@ constexpr double kJoin = 2.9, kJoinMb = 0.45;
 int choose(const LayerShape &s, int kernel, int *splits)
 {
     const bool dw = s.kind == dg::LAYER_WEIGHTS;
-    const double groups = dw ? (double)s.groups : 1, mb = groups * (double)s.M * (double)s.N * 4e-6;
+    const double groups = dw ? (double)s.groups : 1, mb = groups * (double)s.M * (double)s.N * 4e-6;      // in fp32
     const double K = dw && s.ragged ? (double)s.K / (double)s.groups : (double)s.K;
     const double used = (double)(s.groups < s.M ? s.groups : s.M);
+    const double weights = dw ? 0 : used * (double)s.N * K * (s.type == 0 ? 4e-6 : 2e-6);
     const bool may_split = dw || !s.ragged;
     double best = 1e300;
     int k_best = -1, n_best = 1;
@@ -156,8 +160,13 @@ int choose(const LayerShape &s, int kernel, int *splits)
         for (int i = 0; i < many; ++i) {
             const int n = *splits > 0 ? *splits : kRanges[i];
             if (i > 0 && (64. * n > K || tiles * n > 2048)) break;
-            const double slabs = K <= 64. * n ? 1 : K / n / 64, rounds = tiles * n / m.share;
-            double t = m.fixed + (m.tile + m.slab * slabs) * (rounds > 1 ? rounds : 1);
+            const double slabs = K <= 64. * n ? 1 : K / n / 64;
+            double rounds = tiles * n / m.share;
+            // an fp32 tile keeps its unit's matrix cores busy: the last round is a whole one
+            if (s.type == 0 && f.loads < ROWS && rounds < 4) rounds = (double)(int)(rounds + 0.999);
+            if (rounds < 1) rounds = 1;
+            const double tiled = (m.tile + m.slab * slabs) * rounds, read = m.read * weights;
+            double t = m.fixed + (tiled > read ? tiled : read);
             t += n == 1 ? m.out * mb * (s.out32 ? 1 : 0.5) : kJoin + kJoinMb * mb * n + 0.1 * t;
             if (t < best) {
                 best = t;

@@ -96,45 +96,58 @@ __device__ __forceinline__ float layer_act_grad(int act, float h, float x)
     return h;
 }
 
-// W consecutive elements of a row as fp32 and back, by 16-byte accesses that need
-// no more than the element's alignment (the GPU takes misaligned vectors).
+// W consecutive elements of a row, by 16-byte accesses that need no more than the
+// element's alignment (the GPU takes misaligned vectors); where only n < W exist, one
+// by one, and the others are 0.
 template <typename T, int W>
-__device__ __forceinline__ auto load_raw(const T *x)
+__device__ __forceinline__ auto load_raw(const T *x, int n)
 {
     constexpr int PER = (int)(16 / sizeof(T)) < W ? (int)(16 / sizeof(T)) : W;
     typedef T V __attribute__((ext_vector_type(PER)));
     typedef V __attribute__((aligned(sizeof(T)))) Vu;
     typedef T VW __attribute__((ext_vector_type(W)));
-    VW v;
+    VW v = (VW)(T)0.f;
+    if (n >= W) {
 #pragma unroll
-    for (int c = 0; c < W / PER; ++c) {
-        const V y = *(const Vu *)(x + c * PER);
+        for (int c = 0; c < W / PER; ++c) {
+            const V y = *(const Vu *)(x + c * PER);
 #pragma unroll
-        for (int e = 0; e < PER; ++e) v[c * PER + e] = y[e];
+            for (int e = 0; e < PER; ++e) v[c * PER + e] = y[e];
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < W; ++e)
+            if (e < n) v[e] = x[e];
     }
     return v;
 }
 
 template <typename T, int W>
-__device__ __forceinline__ void load_row(const T *x, float (&v)[W])
+__device__ __forceinline__ void load_row(const T *x, float (&v)[W], int n)
 {
-    const auto y = load_raw<T, W>(x);
+    const auto y = load_raw<T, W>(x, n);
 #pragma unroll
     for (int e = 0; e < W; ++e) v[e] = (float)y[e];
 }
 
 template <typename T, int W>
-__device__ __forceinline__ void store_row(T *x, const float (&v)[W])
+__device__ __forceinline__ void store_row(T *x, const float (&v)[W], int n)
 {
     constexpr int PER = (int)(16 / sizeof(T)) < W ? (int)(16 / sizeof(T)) : W;
     typedef T V __attribute__((ext_vector_type(PER)));
     typedef V __attribute__((aligned(sizeof(T)))) Vu;
+    if (n >= W) {
 #pragma unroll
-    for (int c = 0; c < W / PER; ++c) {
-        V y;
+        for (int c = 0; c < W / PER; ++c) {
+            V y;
 #pragma unroll
-        for (int e = 0; e < PER; ++e) y[e] = (T)v[c * PER + e];
-        *(Vu *)(x + c * PER) = y;
+            for (int e = 0; e < PER; ++e) y[e] = (T)v[c * PER + e];
+            *(Vu *)(x + c * PER) = y;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < W; ++e)
+            if (e < n) x[e] = (T)v[e];
     }
 }
 
@@ -155,33 +168,33 @@ template <typename TC, int W>
 struct LayerAux {
     typedef TC V __attribute__((ext_vector_type(W)));
     V x;
-    __device__ __forceinline__ static V residual(const LayerParams &p, const LayerTile &t, int row, int col)
+    __device__ __forceinline__ static V residual(const LayerParams &p, const LayerTile &t, int row, int col, int n)
     {
-        return load_raw<TC, W>((const TC *)p.R + t.group * p.strideC + (t.out0 + row) * p.ldr + col);
+        return load_raw<TC, W>((const TC *)p.R + t.group * p.strideC + (t.out0 + row) * p.ldr + col, n);
     }
-    __device__ __forceinline__ void fetch(const LayerParams &p, const LayerTile &t, int row, int col)
+    __device__ __forceinline__ void fetch(const LayerParams &p, const LayerTile &t, int row, int col, int n = W)
     {
         x = (V)(TC)0.f;
-        if (p.Z) x = load_raw<TC, W>((const TC *)p.Z + (t.out0 + row) * p.ldz + col);
-        else if (p.R) x = residual(p, t, row, col);
+        if (p.Z) x = load_raw<TC, W>((const TC *)p.Z + (t.out0 + row) * p.ldz + col, n);
+        else if (p.R) x = residual(p, t, row, col, n);
     }
 };
 
-// The epilogue of W columns col .. of row `row`: v holds the sums.
+// The epilogue of W columns col .. of row `row`, n of which exist: v holds the sums.
 template <typename TC, int W>
 __device__ __forceinline__ void layer_finish(const LayerParams &p, const LayerTile &t, int row, int col,
-                                             float (&v)[W], const LayerAux<TC, W> &aux, const float (&bias)[W])
+                                             float (&v)[W], const LayerAux<TC, W> &aux, const float (&bias)[W], int n = W)
 {
     constexpr bool EXACT = sizeof(TC) == 4;
     const int64_t out = t.out0 + row;
 #pragma unroll
     for (int e = 0; e < W; ++e) v[e] = __builtin_fmaf(p.alpha, v[e], bias[e]);
     if (p.kind == LAYER_GRAD && p.R) {
-        const auto r = LayerAux<TC, W>::residual(p, t, row, col);
+        const auto r = LayerAux<TC, W>::residual(p, t, row, col, n);
 #pragma unroll
         for (int e = 0; e < W; ++e) v[e] = __builtin_fmaf(p.beta, (float)r[e], v[e]);
     }
-    if (p.keep) store_row<TC, W>((TC *)p.keep + out * p.ldk + col, v);
+    if (p.keep) store_row<TC, W>((TC *)p.keep + out * p.ldk + col, v, n);
     if (p.kind == LAYER_GRAD) {
         if (p.act == ACT_GELU) {
 #pragma unroll
@@ -207,15 +220,15 @@ __device__ __forceinline__ void layer_finish(const LayerParams &p, const LayerTi
 #pragma unroll
         for (int e = 0; e < W; ++e) v[e] = __builtin_fmaf(p.beta, (float)aux.x[e], v[e]);
     }
-    store_row<TC, W>((TC *)p.C + t.group * p.strideC + out * p.ldc + col, v);
+    store_row<TC, W>((TC *)p.C + t.group * p.strideC + out * p.ldc + col, v, n);
 }
 
 // The bias of W columns of a group.
 template <typename TC, int W>
-__device__ __forceinline__ void layer_bias(const LayerParams &p, int group, int col, float (&b)[W])
+__device__ __forceinline__ void layer_bias(const LayerParams &p, int group, int col, float (&b)[W], int n = W)
 {
     if (p.bias) {
-        load_row<TC, W>((const TC *)p.bias + group * p.stride_bias + col, b);
+        load_row<TC, W>((const TC *)p.bias + group * p.stride_bias + col, b, n);
     } else {
 #pragma unroll
         for (int e = 0; e < W; ++e) b[e] = 0.f;
@@ -225,10 +238,10 @@ __device__ __forceinline__ void layer_bias(const LayerParams &p, int group, int 
 // The raw sums of a split's W columns.
 template <int W>
 __device__ __forceinline__ void layer_partial(const LayerParams &p, const LayerTile &t, int row, int col,
-                                              const float (&v)[W])
+                                              const float (&v)[W], int n = W)
 {
     float *w = p.ws + (((int64_t)blockIdx.y * p.groups + t.group) * p.M + row) * p.N + col;
-    store_row<float, W>(w, v);
+    store_row<float, W>(w, v, n);
 }
 
 // One column's sum for the bias's gradient: a split's goes behind the splits' sums of

@@ -26,7 +26,7 @@ __device__ __forceinline__ void join(const LayerParams &p, int64_t grow, int col
         float x[4][W];
 #pragma unroll
         for (int u = 0; u < 4; ++u)
-            if (s + u < p.splits) load_row<float, W>(w + (s + u) * mn, x[u]);
+            if (s + u < p.splits) load_row<float, W>(w + (s + u) * mn, x[u], W);
 #pragma unroll
         for (int u = 0; u < 4; ++u)
             if (s + u < p.splits)
@@ -84,7 +84,7 @@ __global__ __launch_bounds__(512) void layer_colsum_kernel(LayerParams p)
             float v[4][8];
 #pragma unroll
             for (int u = 0; u < 4; ++u)
-                if (r + 64 * u < rows) load_row<T, 8>(a + (int64_t)(r + 64 * u) * p.lda, v[u]);
+                if (r + 64 * u < rows) load_row<T, 8>(a + (int64_t)(r + 64 * u) * p.lda, v[u], 8);
 #pragma unroll
             for (int u = 0; u < 4; ++u)
                 if (r + 64 * u < rows)

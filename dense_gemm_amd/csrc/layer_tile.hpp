@@ -38,14 +38,14 @@ __device__ __forceinline__ void layer_store_as(const LayerParams &p, const Layer
     const int lc = (lane % LPR) * 8, col = col0 + lc;
     const bool whole = col0 + W <= p.N;
     float bias[8];
-    if (whole && !partial) layer_bias<TC, 8>(p, t.group, col, bias);
+    if (!partial) layer_bias<TC, 8>(p, t.group, col < p.N ? col : 0, bias, col < p.N ? p.N - col : 0);
 #pragma unroll 1
     for (int i = 0; i < TM * PER32; ++i) {
         const int top = row0 + SR * i, rows = t.rows - top;      // of this strip on
         // (opaque to the compiler, which would otherwise keep every pass's addresses
         // in registers from strip to strip)
-        int lr0 = lane / LPR, lane1 = lane;
-        asm volatile("" : "+v"(lr0), "+v"(lane1));
+        int lr0 = lane / LPR;
+        asm volatile("" : "+v"(lr0));
         LayerAux<TC, 8> aux[TOGETHER];
         auto fetch = [&](int from) {
             if (whole && !partial) {
@@ -89,20 +89,24 @@ __device__ __forceinline__ void layer_store_as(const LayerParams &p, const Layer
                 __builtin_amdgcn_sched_barrier(0);    // a pass's registers at a time
             }
         } else {
-            // the last columns: one element a lane
+            // the last columns: a pass at a time, the piece across the end one by one
 #pragma unroll 1
-            for (int at = lane1; at < SR * W; at += 64) {
-                const int lr = at / W, c = at % W;
-                if (lr >= rows || col0 + c >= p.N) continue;
-                float v[1] = {*(const lds_float_t *)(stg + (lr * W + (c ^ (strip_swz<W>(lr) << 2))) * 4)};
+            for (int lr = lr0; lr < SR; lr += RPP) {
+                const int n = p.N - col;
+                float v[8];
+#pragma unroll
+                for (int c4 = 0; c4 < 2; ++c4) {
+                    const f32x4 x = *(const lds_f32x4_t *)(stg + (lr * W + ((lc + 4 * c4) ^ (strip_swz<W>(lr) << 2))) * 4);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[4 * c4 + e] = x[e];
+                }
+                if (lr >= rows || n <= 0) continue;
                 if (partial) {
-                    layer_partial<1>(p, t, top + lr, col0 + c, v);
+                    layer_partial<8>(p, t, top + lr, col, v, n);
                 } else {
-                    float b[1];
-                    LayerAux<TC, 1> x;
-                    layer_bias<TC, 1>(p, t.group, col0 + c, b);
-                    x.fetch(p, t, top + lr, col0 + c);
-                    layer_finish<TC, 1>(p, t, top + lr, col0 + c, v, x, b);
+                    LayerAux<TC, 8> x;
+                    x.fetch(p, t, top + lr, col, n);
+                    layer_finish<TC, 8>(p, t, top + lr, col, v, x, bias, n);
                 }
             }
         }
@@ -256,28 +260,37 @@ struct LayerOperand : std::conditional<sizeof(T) == 2, SlabOperandH<T, BMN, KCON
         for (int i = 0; i < Base::LOADS; ++i) *(lds_v_t *)(lds + (i * NW + wave) * Base::SPAN + lane * 16) = held[i];
     }
 
-    // a slab with krem summed indices left, straight to its stage
+    // a slab with krem summed indices left, straight to its stage: whole pieces first,
+    // then those across an end
     __device__ __forceinline__ void tail(lds_char_t *lds, int wave, int lane, int krem, int mn0, int ext)
     {
-#pragma unroll 1
-        for (int i = 0; i < Base::LOADS; ++i) {
-            const int b = (i * NW + wave) * Base::SPAN + lane * 16;
-            int r, c, valid;
-            Base::place(b, r, c);
+        auto place_of = [&](int i, int &valid) {
+            int r, c;
+            Base::place((i * NW + wave) * Base::SPAN + lane * 16, r, c);
             if constexpr (KCONT) {
                 valid = mn0 + r < ext ? krem - c : 0;
             } else {
                 valid = r < krem ? ext - mn0 - c : 0;
             }
-            const T *x = (const T *)(this->base + ((int64_t)r * row_step + (int64_t)c * (int)sizeof(T)));
-            V v;
-            if (valid >= PER) {
-                v = *(const Vu *)x;
-            } else {
+            return (const T *)(this->base + ((int64_t)r * row_step + (int64_t)c * (int)sizeof(T)));
+        };
+        V v[Base::LOADS];
+        int valid;
 #pragma unroll
-                for (int e = 0; e < PER; ++e) v[e] = e < valid ? x[e] : (T)0.f;
+        for (int i = 0; i < Base::LOADS; ++i) {
+            const T *x = place_of(i, valid);
+            v[i] = (V)(T)0.f;
+            if (valid >= PER) v[i] = *(const Vu *)x;
+        }
+#pragma unroll
+        for (int i = 0; i < Base::LOADS; ++i) {
+            const T *x = place_of(i, valid);
+            if (valid > 0 && valid < PER) {
+#pragma unroll
+                for (int e = 0; e < PER - 1; ++e)
+                    if (e < valid) v[i][e] = x[e];
             }
-            *(lds_v_t *)(lds + b) = v;
+            *(lds_v_t *)(lds + (i * NW + wave) * Base::SPAN + lane * 16) = v[i];
         }
     }
 

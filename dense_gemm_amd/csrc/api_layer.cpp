@@ -52,8 +52,8 @@ const LayerFamily kLayer[] = {
     {"layer_128x128", 9, 128, 128, 4, 256, DIRECT},
     {"layer_256x256", 10, 256, 256, 4, 512, DIRECT},
     {"layer_256x128", 11, 256, 128, 4, 256, DIRECT},
-    {"layer_16_rows", 12, 16, 16, 1, 512, ROWS},
-    {"layer_16_rows_stream", 13, 16, 16, 1, 512, STREAM},
+    {"layer_16_rows", 12, 16, 16, 8, 512, ROWS},
+    {"layer_16_rows_stream", 13, 16, 16, 8, 512, STREAM},
 };
 constexpr int kNumLayer = sizeof(kLayer) / sizeof(kLayer[0]);
 enum { K_ANY_64, K_ANY_128, K_64_DEEP, K_64, K_128_DEEP, K_128, K_256, K_256x128, K_ROWS, K_STREAM };
@@ -159,7 +159,7 @@ int choose(const LayerShape &s, int kernel, int *splits)
         const int many = *splits > 0 || !may_split || f.loads >= ROWS || tiles > 512 || K < 512 ? 1 : 8;
         for (int i = 0; i < many; ++i) {
             const int n = *splits > 0 ? *splits : kRanges[i];
-            if (i > 0 && (64. * n > K || tiles * n > 2048)) break;
+            if (i > 0 && (64. * n > K || tiles * n > 1024)) break;
             const double slabs = K <= 64. * n ? 1 : K / n / 64;
             double rounds = tiles * n / m.share;
             // an fp32 tile keeps its unit's matrix cores busy: the last round is a whole one
@@ -286,6 +286,34 @@ int rows_product(const RowsCall &c, LayerParams &p, F between)
     const LayerShape s = {p.kind, operand_type(c.dtype), c.transB == DG_OP_T, c.offsets != nullptr, c.groups, c.M, c.N, p.K, cb == 4,
                           direct_ok(c.A, c.lda, 0, eb), direct_ok(c.B, c.ldb, c.strideB, eb)};
     return launch(p, s, c.dtype, c.kernel, c.splits, c.workspace, c.workspace_bytes, 25, (hipStream_t)c.stream);
+}
+
+// The choice for operands that the direct loads take, or -i (1 M, 2 N, 3 K, 4 transB, 5
+// dtype; 1 groups, 2 rows, 3 M, 4 N, 5 dtype).
+int select_rows(int transB, int64_t groups, int64_t M, int64_t N, int64_t K, int dtype, bool ragged, int *splits)
+{
+    if (M < 0 || M > kMaxDim) return -1;
+    if (N < 0 || N > kMaxDim) return -2;
+    if (K < 0 || K > kMaxDim) return -3;
+    if (transB != DG_OP_N && transB != DG_OP_T) return -4;
+    if (!is_dtype(dtype)) return -5;
+    const LayerShape s = {dg::LAYER_FORWARD, operand_type(dtype), transB == DG_OP_T, ragged, max1(groups), max1(M), max1(N), K,
+                          output_type(dtype) == 0, true, true};
+    const int k = choose(s, DG_KERNEL_AUTO, splits);
+    return k < 0 ? DG_ERR_UNSUPPORTED : k;
+}
+
+int select_dw(int64_t groups, int64_t rows, int64_t M, int64_t N, int dtype, int *splits)
+{
+    if (groups < 0 || groups > kMaxGroups) return -1;
+    if (rows < 0 || rows > kMaxDim) return -2;
+    if (M < 0 || M > kMaxDim) return -3;
+    if (N < 0 || N > kMaxDim) return -4;
+    if (!is_dtype(dtype)) return -5;
+    const LayerShape s = {dg::LAYER_WEIGHTS, operand_type(dtype), false, groups > 1, max1(groups), max1(M), max1(N), rows,
+                          output_type(dtype) == 0, true, true};
+    const int k = choose(s, DG_KERNEL_AUTO, splits);
+    return k < 0 ? DG_ERR_UNSUPPORTED : k;
 }
 
 }  // namespace
@@ -436,32 +464,29 @@ int dg_gemm_dw(int64_t groups, const int32_t *offsets, int64_t rows, int64_t M, 
 
 int dg_gemm_fused_choose(int64_t M, int64_t N, int64_t K, dg_op_t transB, dg_dtype_t dtype)
 {
-    if (M < 0 || M > kMaxDim) return -1;
-    if (N < 0 || N > kMaxDim) return -2;
-    if (K < 0 || K > kMaxDim) return -3;
-    if (transB != DG_OP_N && transB != DG_OP_T) return -4;
-    if (!is_dtype(dtype)) return -5;
-    if (M == 0 || N == 0) return 1;
-    const LayerShape s = {dg::LAYER_FORWARD, operand_type(dtype), transB == DG_OP_T, false, 1, M, N, K, output_type(dtype) == 0, true,
-                          true};
     int splits = 0;
-    choose(s, DG_KERNEL_AUTO, &splits);
-    return splits;
+    const int k = select_rows(transB, 1, M, N, K, dtype, false, &splits);
+    return k < 0 ? k : splits;
+}
+
+int dg_gemm_fused_select(int64_t M, int64_t N, int64_t K, dg_op_t transB, dg_dtype_t dtype, int64_t groups, int splits)
+{
+    if (groups < 0 || groups > kMaxGroups) return -6;
+    if (splits < 0 || splits > 4096) return -7;
+    return select_rows(transB, groups, M, N, K, dtype, groups > 0, &splits);
 }
 
 int dg_gemm_dw_choose(int64_t groups, int64_t rows, int64_t M, int64_t N, dg_dtype_t dtype)
 {
-    if (groups < 0 || groups > kMaxGroups) return -1;
-    if (rows < 0 || rows > kMaxDim) return -2;
-    if (M < 0 || M > kMaxDim) return -3;
-    if (N < 0 || N > kMaxDim) return -4;
-    if (!is_dtype(dtype)) return -5;
-    if (groups == 0 || M == 0 || N == 0) return 1;
-    const LayerShape s = {dg::LAYER_WEIGHTS, operand_type(dtype), false, groups > 1, groups, M, N, rows, output_type(dtype) == 0,
-                          true, true};
     int splits = 0;
-    choose(s, DG_KERNEL_AUTO, &splits);
-    return splits;
+    const int k = select_dw(groups, rows, M, N, dtype, &splits);
+    return k < 0 ? k : splits;
+}
+
+int dg_gemm_dw_select(int64_t groups, int64_t rows, int64_t M, int64_t N, dg_dtype_t dtype, int splits)
+{
+    if (splits < 0 || splits > 4096) return -6;
+    return select_dw(groups, rows, M, N, dtype, &splits);
 }
 
 size_t dg_layer_workspace_size(int64_t groups, int64_t M, int64_t N, int splits)

@@ -14,6 +14,7 @@ torch stream of that device) is given, without waiting.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -45,6 +46,8 @@ _SIGNATURES = {
     "dg_gemm_dw": (_ci, _DW, _DW_NAMES),
     "dg_gemm_dw_with_kernel": (_ci, _DW + [_ci], _DW_NAMES + " kernel"),
     "dg_gemm_dw_choose": (_ci, [_i64, _i64, _i64, _i64, _ci], "groups rows M N dtype"),
+    "dg_gemm_fused_select": (_ci, [_i64, _i64, _i64, _ci, _ci, _i64, _ci], "M N K transB dtype groups splits"),
+    "dg_gemm_dw_select": (_ci, [_i64, _i64, _i64, _i64, _ci, _ci], "groups rows M N dtype splits"),
     "dg_layer_workspace_size": (_sz, [_i64, _i64, _i64, _ci], "groups M N splits"),
     "dg_layer_kernel_name": (ctypes.c_char_p, [_ci], "kernel"),
 }
@@ -90,6 +93,10 @@ def _run(function, index, args):
     if rc != DG_OK:
         raise LayerError(function, rc)
 
+
+# The library's choice of K ranges by shape.
+_fused_splits = functools.lru_cache(1024)(dg_gemm_fused_choose)  # noqa: F821
+_dw_splits = functools.lru_cache(1024)(dg_gemm_dw_choose)  # noqa: F821
 
 # (operand, output) -> the library's dtype
 _DTYPES = {(torch.float32, torch.float32): DG_F32, (torch.float16, torch.float16): DG_F16_F32ACC,
@@ -156,7 +163,7 @@ def _product(grad, A, B, offsets, C, transB, alpha, bias, activation, Z, R, beta
     if offsets is not None:
         splits = 1
     elif splits == 0:
-        splits = dg_gemm_fused_choose(M, N, K, transB, dtype)  # noqa: F821
+        splits = _fused_splits(M, N, K, transB, dtype)
     if splits > 1 and workspace is None:
         workspace = _empty(dg_layer_workspace_size(1, M, N, splits), torch.uint8, A.device, stream)  # noqa: F821
     ws, wsb = (None, 0) if workspace is None else _workspace(workspace)
@@ -279,7 +286,7 @@ def gemm_dw(A, B, C=None, offsets=None, alpha=1.0, beta=0.0, dbias=None, out_dty
         raise ValueError("dbias must be a contiguous float32 tensor of " + (f"[{M}]" if groups is None else f"[{groups}, {M}]"))
     lda, ldb = _plain(A, "A", rows, M), _plain(B, "B", rows, N)
     if splits == 0:
-        splits = dg_gemm_dw_choose(count, rows, M, N, dtype)  # noqa: F821
+        splits = _dw_splits(count, rows, M, N, dtype)
     if splits > 1 and workspace is None:
         workspace = _empty(dg_layer_workspace_size(count, M, N, splits), torch.uint8, A.device, stream)  # noqa: F821
     ws, wsb = (None, 0) if workspace is None else _workspace(workspace)

@@ -513,10 +513,11 @@ int dg_gemm_dw(int64_t groups, const int32_t *offsets, int64_t rows, int64_t M, 
 
 /* The same with a forced kernel (the last argument; DG_KERNEL_AUTO: the library's
  * choice), for tests and measurement; DG_ERR_UNSUPPORTED when it cannot run the
- * problem.  The kernels' names (NULL when out of range), the ranges that splits = 0
- * gives (or -i: 1 M, 2 N, 3 K, 4 transB, 5 dtype; 1 groups, 2 rows, 3 M, 4 N, 5
- * dtype), and the workspace's bytes, splits * groups * M * (N + 1) * 4 (0 for one
- * range). */
+ * problem.  The kernels' names (NULL when out of range).  For operands whose rows
+ * are 4-byte aligned: the ranges that splits = 0 gives (_choose) and the kernel for so
+ * many ranges (_select; 0: the library's choice; groups 0: none), or -i (1 M, 2 N, 3 K,
+ * 4 transB, 5 dtype, 6 groups, 7 splits; 1 groups, 2 rows, 3 M, 4 N, 5 dtype, 6
+ * splits).  The workspace's bytes: splits * groups * M * (N + 1) * 4, 0 for one range. */
 int dg_gemm_fused_with_kernel(dg_op_t transB, int64_t groups, const int32_t *offsets, int64_t M, int64_t N, int64_t K,
                               float alpha, const void *A, int64_t lda, const void *B, int64_t ldb, int64_t strideB,
                               const void *bias, int64_t strideBias, dg_epilogue_t epilogue, void *Z, int64_t ldz, float beta,
@@ -532,7 +533,9 @@ int dg_gemm_dw_with_kernel(int64_t groups, const int32_t *offsets, int64_t rows,
                            int64_t strideC, float *dbias, dg_dtype_t dtype, int splits, void *workspace,
                            size_t workspace_bytes, void *stream, int kernel);
 int dg_gemm_fused_choose(int64_t M, int64_t N, int64_t K, dg_op_t transB, dg_dtype_t dtype);
+int dg_gemm_fused_select(int64_t M, int64_t N, int64_t K, dg_op_t transB, dg_dtype_t dtype, int64_t groups, int splits);
 int dg_gemm_dw_choose(int64_t groups, int64_t rows, int64_t M, int64_t N, dg_dtype_t dtype);
+int dg_gemm_dw_select(int64_t groups, int64_t rows, int64_t M, int64_t N, dg_dtype_t dtype, int splits);
 size_t dg_layer_workspace_size(int64_t groups, int64_t M, int64_t N, int splits);
 const char *dg_layer_kernel_name(int kernel);
 

@@ -141,13 +141,18 @@ SIZES = [(1, 1, 1), (1, 130, 64), (2, 17, 3), (5, 64, 100), (16, 16, 16), (17, 2
          (128, 128, 128), (130, 250, 191), (257, 300, 320), (300, 515, 72), (31, 1032, 512)]
 
 
+def pads(kernel, i):
+    """Row paddings: all with the library's choice, in turn with a forced kernel."""
+    return (0, 1, 8) if kernel < 0 else ((0, 1, 8)[i % 3], (0, 8)[i % 2])
+
+
 @pytest.mark.parametrize("transB", [False, True])
 @pytest.mark.parametrize("ty,out", PAIRS)
 @pytest.mark.parametrize("kernel", [-1] + KERNELS)
 def test_fused(kernel, ty, out, transB):
     ran = 0
     for i, (M, N, K) in enumerate(SIZES):
-        for pad in (0, 1, 8):
+        for pad in pads(kernel, i):
             o = (i + pad) % 6
             ran += fused_case(100 * i + pad, M, N, K, ty, out, transB, ("none", "relu", "gelu")[o % 3], bias=o in (0, 2, 3), res=o in (1, 2, 4),
                               keep=o in (2, 3, 5), pad=pad, shift=(0, 1, 0)[i % 3] * (pad > 0), alpha=(1.0, -0.5)[i % 2],
@@ -160,7 +165,7 @@ def test_fused(kernel, ty, out, transB):
 @pytest.mark.parametrize("kernel", [-1] + KERNELS)
 def test_act_grad(kernel, ty, out, transB):
     for i, (M, N, K) in enumerate(SIZES):
-        for pad in (0, 1, 8):
+        for pad in pads(kernel, i):
             o = (i + pad) % 4
             grad_case(7000 + 100 * i + pad, M, N, K, ty, out, transB, ("gelu", "relu")[o % 2], res=o in (1, 2), keep=o in (2, 3), pad=pad,
                       alpha=(1.0, 2.0)[i % 2], beta=(1.0, -0.5)[i % 2], kernel=kernel)
@@ -170,7 +175,7 @@ def test_act_grad(kernel, ty, out, transB):
 @pytest.mark.parametrize("kernel", [-1] + KERNELS)
 def test_dw(kernel, ty, out):
     for i, (M, N, K) in enumerate(SIZES):
-        for pad in (0, 1, 8):
+        for pad in pads(kernel, i):
             o = (i + pad) % 4
             dw_case(9000 + 100 * i + pad, K, M, N, ty, out, bias=o in (0, 1), pad=pad, shift=(0, 1, 0)[i % 3] * (pad > 0),
                     alpha=(1.0, 0.5)[i % 2], beta=(0.0, 1.0, 0.5)[o % 3], kernel=kernel)

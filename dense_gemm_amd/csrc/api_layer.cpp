@@ -51,12 +51,11 @@ const LayerFamily kLayer[] = {
     {"layer_128x128_deep", 8, 128, 128, 4, 512, DIRECT},
     {"layer_128x128", 9, 128, 128, 4, 256, DIRECT},
     {"layer_256x256", 10, 256, 256, 4, 512, DIRECT},
-    {"layer_256x128", 11, 256, 128, 4, 256, DIRECT},
-    {"layer_16_rows", 12, 16, 16, 8, 512, ROWS},
-    {"layer_16_rows_stream", 13, 16, 16, 8, 512, STREAM},
+    {"layer_16_rows", 11, 16, 16, 8, 512, ROWS},
+    {"layer_16_rows_stream", 12, 16, 16, 8, 512, STREAM},
 };
 constexpr int kNumLayer = sizeof(kLayer) / sizeof(kLayer[0]);
-enum { K_ANY_64, K_ANY_128, K_64_DEEP, K_64, K_128_DEEP, K_128, K_256, K_256x128, K_ROWS, K_STREAM };
+enum { K_ANY_64, K_ANY_128, K_64_DEEP, K_64, K_128_DEEP, K_128, K_256, K_ROWS, K_STREAM };
 
 // What the choice of a kernel looks at.
 struct LayerShape {
@@ -80,11 +79,12 @@ int log2_of(int x) { return __builtin_ctz((unsigned)x); }
 int64_t tiles_of(int64_t x, int b) { return (x + b - 1) >> log2_of(b); }
 int bn_of(const LayerFamily &f, const LayerShape &s) { return f.loads == ROWS && !s.tb ? 64 : f.bn; }
 
-// The most tiles a launch can have: each group that has rows ends in a partial tile.
+// The most tiles a launch can have: each group that has rows ends in a partial tile
+// (weights: a multiple of 8 for each group).
 int64_t most_tiles(const LayerShape &s, const LayerFamily &f)
 {
     const int64_t tn = tiles_of(s.N, bn_of(f, s));
-    if (s.kind == dg::LAYER_WEIGHTS) return s.groups * tiles_of(s.M, f.bm) * tn;
+    if (s.kind == dg::LAYER_WEIGHTS) return s.groups * ((tiles_of(s.M, f.bm) * tn + 7) & ~(int64_t)7);
     const int64_t used = s.ragged && s.groups < s.M ? s.groups : s.ragged ? s.M : 1;
     return ((s.M + used * (f.bm - 1)) >> log2_of(f.bm)) * tn;
 }
@@ -96,7 +96,7 @@ bool supports(int k, const LayerShape &s)
     const bool dw = s.kind == dg::LAYER_WEIGHTS;
     if ((f.loads == DIRECT || f.loads == STREAM) && !s.direct()) return false;
     if (f.loads == STREAM && (dw || !s.tb)) return false;
-    if (s.type == 0 && (k == K_128_DEEP || k == K_256 || k == K_256x128)) return false;
+    if (s.type == 0 && (k == K_128_DEEP || k == K_256)) return false;
     // the row kernels' columns of a B stored K x N go four together
     if (f.loads == ROWS && (dw || (!s.tb && s.N < 4))) return false;
     // a launch holds fewer than 2^32 threads
@@ -112,21 +112,20 @@ bool supports(int k, const LayerShape &s)
 // 21% at the 95th of a hundred, 2.8 times at the worst (64 groups with half a row each, K =
 // 33).  Both sides of some choices (bf16, B stored N x K, M x N x K, us): 24 x 2048 x 5632 stream 12.5, 64
 // deep in 6 ranges and their join 11.6, in one 18.9; 512 x 5632 x 2048 128 deep 22, 64 deep
-// 27; 16384 x 5632 x 2048 256 343, 128 388; 8 groups of 2048 rows, 5632 x 2048 fp32 weight
-// gradients 256 x 128 524, 256 547.
+// 27; 16384 x 5632 x 2048 256 343, 128 388.
 struct LayerTime {
     double fixed, tile, slab, share, out, read;
 };
 const LayerTime kTime16[kNumLayer] = {
     {6.68, 1.12, 0.581, 466, 0.168, 0.226}, {19.5, 2.46, 1.04, 366, 0.256, 0.217}, {7.27, 1.33, 0.205, 187, 0.011, 0.193},
     {6.39, 0.969, 0.486, 467, 0.210, 0.209}, {10.7, 3.51, 0.414, 158, 0.165, 0.207}, {16.2, 2.28, 0.879, 342, 0.276, 0.198},
-    {26.8, 3.28, 1.3, 163, 0.301, 0.257}, {30.7, 0.05, 0.877, 202, 0.375, 0.222}, {4.29, 0.05, 0.203, 150, 1.867, 0.160},
+    {26.8, 3.28, 1.3, 163, 0.301, 0.257}, {4.29, 0.05, 0.203, 150, 1.867, 0.160},
     {3.58, 0.421, 0.0436, 155, 2.0, 0.146},
 };
 const LayerTime kTime32[kNumLayer] = {
     {7.73, 0, 1.396, 256, 0.124, 0.271}, {19.3, 0, 5.0, 256, 0.1, 0.503}, {7.5, 0, 1.11, 256, 0.471, 0.304},
     {8.03, 0, 1.086, 256, 0.233, 0.282}, {}, {21.2, 0, 4.06, 256, 0.152, 0.382},
-    {}, {}, {4.41, 0.05, 0.385, 141, 0.9, 0.161}, {3.7, 0.398, 0.124, 194, 2.0, 0.153},
+    {}, {4.41, 0.05, 0.385, 141, 0.9, 0.161}, {3.7, 0.398, 0.124, 194, 2.0, 0.153},
 };
 // K_ROWS with a B stored N x K, which it takes where its rows are not aligned.
 const LayerTime kTimeRowsT = {4.1, 0.0874, 0.225, 293, 2.0, 0.361};

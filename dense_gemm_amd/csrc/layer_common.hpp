@@ -295,12 +295,27 @@ __device__ __forceinline__ bool layer_tile(const LayerParams &p, int bm, int bn,
     t.group = 0;
     t.row0 = 0;
     if (p.kind == LAYER_WEIGHTS) {
-        const int per = p.tiles_m * p.tiles_n;
-        if (id >= per * p.groups) return false;
-        id = xcd_contiguous(id, per * p.groups);
-        t.group = id / per;
+        // Every group goes over all XCDs, in a multiple of 8 workgroups, the group with
+        // most rows first: a group's tiles take as long as it has rows, so that a group to
+        // an XCD, or a long one at the end, would leave the others idle (8 uneven groups of 2048
+        // rows, 5632 x 2048 on the 256 tile: 583 us, 375 with this; equal groups 371).
+        const int per = p.tiles_m * p.tiles_n, slots = (per + 7) & ~7, slot = id / slots;
+        id -= slot * slots;
+        if (id >= per) return false;
+        id = xcd_contiguous(id, per);
+        t.group = slot;
+        if (p.offsets && p.groups > 1 && p.groups <= 64) {
+            const int lane = threadIdx.x & 63;
+            int b, n = -1, rank = 0;
+            if (lane < p.groups) group_rows(p, lane, p.K, b, n);
+            for (int g = 0; g < p.groups; ++g) {
+                const int m = __builtin_amdgcn_readlane(n, g);
+                rank += m > n || (m == n && g < lane);
+            }
+            t.group = __ffsll((unsigned long long)__ballot(rank == slot)) - 1;
+        }
         int tm, tn;
-        walk_tiles(id - t.group * per, p.tiles_m, p.tiles_n, p.group_m, tm, tn);
+        walk_tiles(id, p.tiles_m, p.tiles_n, p.group_m, tm, tn);
         t.m0 = tm * bm;
         t.n0 = tn * bn;
         t.rows = p.M;

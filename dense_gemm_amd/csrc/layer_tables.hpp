@@ -34,7 +34,6 @@ const void *layer_kernel_of(int config, int variant)
             DG_LAYER_NONE,
             DG_LAYER_PIPE(128, 128, 64, 64, 1, 4, 16, false, false),
             DG_LAYER_NONE,
-            DG_LAYER_NONE,
             DG_LAYER_ROWS(1, 8),
             DG_LAYER_STREAM(1, 8),
         };
@@ -48,7 +47,6 @@ const void *layer_kernel_of(int config, int variant)
             DG_LAYER_PIPE(128, 128, 64, 64, 2, 4, 64, false, false),
             DG_LAYER_PIPE(128, 128, 64, 64, 1, 2, 64, false, false),
             DG_LAYER_PIPE(256, 256, 128, 64, 1, 2, 64, false, false),
-            DG_LAYER_PIPE(256, 128, 128, 64, 1, 3, 32, false, false),
             DG_LAYER_ROWS(1, 8),
             DG_LAYER_STREAM(1, 8),
         };

@@ -201,6 +201,7 @@ int launch(LayerParams &p, const LayerShape &s, int dtype, int kernel, int split
     p.tiles_m = (int32_t)ceil_div(p.M, f.bm);
     p.tiles_n = (int32_t)ceil_div(p.N, bn_of(f, s));
     p.group_m = f.group_m;
+    p.past_caches = (double)(s.kind == dg::LAYER_WEIGHTS ? s.groups : 1) * (double)s.M * (double)s.N * (s.out32 ? 4 : 2) > 64e6;
     const int type = operand_type(dtype), variant = s.kind == dg::LAYER_WEIGHTS ? 2 : s.tb;
     // (an ANY kernel forced on operands that both could load directly takes both through registers)
     const int config = f.config + (f.loads != ANY || (!s.direct_a && s.direct_b) ? 0 : s.direct_a && !s.direct_b ? 1 : 2);

@@ -37,6 +37,7 @@ struct LayerParams {
     int64_t ldc, strideC;           // strideC: weights, from a group's C to the next (else 0)
     int32_t ctype;                  // element of C, R, Z, keep and bias: 0 fp32, 1 fp16, 2 bf16
     int32_t tiles_m, tiles_n, group_m;
+    int32_t past_caches;            // outputs too large for the caches
     int32_t splits;                 // K ranges, a grid dimension; with more than one the raw sums go to ws
     float *ws;                      // [splits][groups][M][N], and weights: [splits][groups][M] behind them
     float *dbias;                   // weights: [groups][M], or NULL
@@ -130,7 +131,7 @@ __device__ __forceinline__ void load_row(const T *x, float (&v)[W], int n)
     for (int e = 0; e < W; ++e) v[e] = (float)y[e];
 }
 
-template <typename T, int W>
+template <typename T, int W, bool NT = false>
 __device__ __forceinline__ void store_row(T *x, const float (&v)[W], int n)
 {
     constexpr int PER = (int)(16 / sizeof(T)) < W ? (int)(16 / sizeof(T)) : W;
@@ -142,7 +143,8 @@ __device__ __forceinline__ void store_row(T *x, const float (&v)[W], int n)
             V y;
 #pragma unroll
             for (int e = 0; e < PER; ++e) y[e] = (T)v[c * PER + e];
-            *(Vu *)(x + c * PER) = y;
+            if constexpr (NT) __builtin_nontemporal_store(y, (Vu *)(x + c * PER));
+            else *(Vu *)(x + c * PER) = y;
         }
     } else {
 #pragma unroll
@@ -181,7 +183,8 @@ struct LayerAux {
 };
 
 // The epilogue of W columns col .. of row `row`, n of which exist: v holds the sums.
-template <typename TC, int W>
+// NT: stores that do not stay in the caches.
+template <typename TC, int W, bool NT = false>
 __device__ __forceinline__ void layer_finish(const LayerParams &p, const LayerTile &t, int row, int col,
                                              float (&v)[W], const LayerAux<TC, W> &aux, const float (&bias)[W], int n = W)
 {
@@ -194,7 +197,7 @@ __device__ __forceinline__ void layer_finish(const LayerParams &p, const LayerTi
 #pragma unroll
         for (int e = 0; e < W; ++e) v[e] = __builtin_fmaf(p.beta, (float)r[e], v[e]);
     }
-    if (p.keep) store_row<TC, W>((TC *)p.keep + out * p.ldk + col, v, n);
+    if (p.keep) store_row<TC, W, NT>((TC *)p.keep + out * p.ldk + col, v, n);
     if (p.kind == LAYER_GRAD) {
         if (p.act == ACT_GELU) {
 #pragma unroll
@@ -220,7 +223,7 @@ __device__ __forceinline__ void layer_finish(const LayerParams &p, const LayerTi
 #pragma unroll
         for (int e = 0; e < W; ++e) v[e] = __builtin_fmaf(p.beta, (float)aux.x[e], v[e]);
     }
-    store_row<TC, W>((TC *)p.C + t.group * p.strideC + out * p.ldc + col, v, n);
+    store_row<TC, W, NT>((TC *)p.C + t.group * p.strideC + out * p.ldc + col, v, n);
 }
 
 // The bias of W columns of a group.

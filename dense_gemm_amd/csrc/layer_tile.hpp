@@ -26,7 +26,7 @@ namespace dg {
 template <int W, int SR> constexpr int kStripBytes = SR * W * 4;
 template <int W> __device__ __forceinline__ int strip_swz(int r) { return W == 64 ? r & 1 : (r >> 1) & 1; }
 
-template <typename TC, int SR, int TM, int TN>
+template <typename TC, int SR, bool NT, int TM, int TN>
 __device__ __forceinline__ void layer_store_as(const LayerParams &p, const LayerTile &t, lds_char_t *stg,
                                                const f32x16 (&acc)[TM][TN], int row0, int col0, int lane, bool partial)
 {
@@ -84,7 +84,7 @@ __device__ __forceinline__ void layer_store_as(const LayerParams &p, const Layer
                 }
                 if (lr < rows) {
                     if (partial) layer_partial<8>(p, t, top + lr, col, v);
-                    else layer_finish<TC, 8>(p, t, top + lr, col, v, aux[ps % TOGETHER], bias);
+                    else layer_finish<TC, 8, NT>(p, t, top + lr, col, v, aux[ps % TOGETHER], bias);
                 }
                 __builtin_amdgcn_sched_barrier(0);    // a pass's registers at a time
             }
@@ -115,13 +115,14 @@ __device__ __forceinline__ void layer_store_as(const LayerParams &p, const Layer
     }
 }
 
-template <typename T, int SR, int TM, int TN>
+template <typename T, int SR, bool NT, int TM, int TN>
 __device__ __forceinline__ void layer_store(const LayerParams &p, const LayerTile &t, lds_char_t *stg,
                                             const f32x16 (&acc)[TM][TN], int row0, int col0, int lane)
 {
-    if (p.splits > 1) layer_store_as<float, SR>(p, t, stg, acc, row0, col0, lane, true);
-    else if (sizeof(T) == 2 && p.ctype != 0) layer_store_as<T, SR>(p, t, stg, acc, row0, col0, lane, false);
-    else layer_store_as<float, SR>(p, t, stg, acc, row0, col0, lane, false);
+    if (p.splits > 1) layer_store_as<float, SR, false>(p, t, stg, acc, row0, col0, lane, true);
+    else if (sizeof(T) == 4 || p.ctype == 0) layer_store_as<float, SR, false>(p, t, stg, acc, row0, col0, lane, false);
+    else if (NT && p.past_caches) layer_store_as<T, SR, true>(p, t, stg, acc, row0, col0, lane, false);
+    else layer_store_as<T, SR, false>(p, t, stg, acc, row0, col0, lane, false);
 }
 
 // ---- operands -------------------------------------------------------------------------
@@ -331,6 +332,11 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * KG, 2) void layer_pipe
     // direct loads of a slab, by operand
     constexpr int LA = RA ? 0 : OpA::LOADS, LBN = RB ? 0 : OpB::LOADS, LOADS = LA + LBN, STAGE = OpA::BYTES + OpB::BYTES;
     constexpr int PA = LA ? LA : 1, PB = LBN ? LBN : 1, PL = LOADS ? LOADS : 1;     // divisors
+    // The 256 tile's 16-bit outputs bypass the caches from 64 MB on (the host's rule): its
+    // rounds of tiles end in 32 to 64 MB of them at once.  16384 x 5632 with gelu and Z,
+    // K = 2048: 414 us, 387 so; a whole layer forward of 16384 rows 722 and 681, of 8192 353
+    // and 344, of 4096 211 and 214; fp32 outputs 390 and 387, smaller tiles no difference.
+    constexpr bool NT = BM == 256;
     constexpr int SR = 32, RING = STAGES * STAGE, STRIPS = NW * kStripBytes<WN, SR>, SMEM = RING > STRIPS ? RING : STRIPS;
     static_assert(SMEM <= 160 * 1024, "the ring and the strips fit the LDS");
     static_assert((STAGES - 2) * LOADS + LA < 64, "the loads in flight can be counted");
@@ -609,7 +615,7 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * KG, 2) void layer_pipe
     __syncthreads();                   // every wave is done with the ring
     if (summing) add_up();
     if constexpr (KG == 1) {
-        layer_store<T, SR>(p, t, smem + wave * kStripBytes<WN, SR>, acc, t.m0 + wm0, t.n0 + wn0, lane);
+        layer_store<T, SR, NT>(p, t, smem + wave * kStripBytes<WN, SR>, acc, t.m0 + wm0, t.n0 + wn0, lane);
     } else {
         // the two K groups' sums: each wave keeps half of the strips and hands the
         // other half to its partner, the same part of the tile in the other group
@@ -642,7 +648,7 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * KG, 2) void layer_pipe
                     for (int e = 0; e < 4; ++e) mine[i][j][4 * c + e] += x[e];
                 }
         __syncthreads();               // read before the strips are staged
-        layer_store<T, SR>(p, t, smem + wave * kStripBytes<WN, SR>, mine, t.m0 + wm0 + 32 * HS * kgroup, t.n0 + wn0, lane);
+        layer_store<T, SR, NT>(p, t, smem + wave * kStripBytes<WN, SR>, mine, t.m0 + wm0 + 32 * HS * kgroup, t.n0 + wn0, lane);
     }
 }
 

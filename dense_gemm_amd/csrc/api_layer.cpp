@@ -276,7 +276,7 @@ int rows_product(const RowsCall &c, LayerParams &p, F between)
     p.M = (int32_t)c.M;
     p.N = (int32_t)c.N;
     p.K = reads ? (int32_t)c.K : 0;
-    p.alpha = c.alpha;
+    p.alpha = reads ? c.alpha : 0.f;
     p.offsets = c.offsets;
     p.groups = (int32_t)c.groups;
     if (p.beta == 0.f) p.R = nullptr;
@@ -439,19 +439,23 @@ int dg_gemm_dw_with_kernel(int64_t groups, const int32_t *offsets, int64_t rows,
     p.strideC = strideC;
     p.ctype = output_type(dtype);
     p.dbias = dbias;
-    if (sums && (M > kMaxTiled || rows > kMaxTiled)) return DG_ERR_UNSUPPORTED;
     // the bias's gradient comes with the product, or by a pass of its own without one
-    const bool alone = sums && rows > 0 && !reads;
+    const bool alone = sums && !reads && (rows > 0 || !work);
+    // (a launch of 512 threads for 64 columns holds fewer than 2^32)
+    if (alone && (M > ((int64_t)1 << 28) || rows > kMaxTiled)) return DG_ERR_UNSUPPORTED;
     if (work) {
         LayerParams q = p;
-        if (!reads) q.K = 0;
+        if (!reads) {
+            q.K = 0;
+            q.alpha = 0.f;
+        }
         if (alone) q.dbias = nullptr;
         const LayerShape s = {p.kind, operand_type(dtype), false, offsets != nullptr, groups, M, N, q.K, cb == 4,
                               direct_ok(A, lda, 0, eb), direct_ok(B, ldb, 0, eb)};
         const int rc = launch(q, s, dtype, kernel, splits, workspace, workspace_bytes, 18, (hipStream_t)stream);
         if (rc != DG_OK) return rc;
     }
-    return alone || (sums && !work) ? dg::launch_status(dg::launch_layer_colsum(p, operand_type(dtype), (hipStream_t)stream)) : DG_OK;
+    return alone ? dg::launch_status(dg::launch_layer_colsum(p, operand_type(dtype), (hipStream_t)stream)) : DG_OK;
 }
 
 int dg_gemm_dw(int64_t groups, const int32_t *offsets, int64_t rows, int64_t M, int64_t N, float alpha, const void *A,

@@ -10,7 +10,7 @@ namespace {
 // applies the epilogue: 4 columns of a row a thread, n of which exist, so that small
 // outputs too have many threads; 8 splits' loads in flight.  Behind the rows, a thread
 // for every column sum of the bias's gradient.  Latency bounds it: 2048 x 32 of 12 ranges
-// with a bias 3.4 us (7.6 with 8 columns a thread, 4 splits' loads and the column sums
+// with a bias 3.9 us (7.6 with 8 columns a thread, 4 splits' loads and the column sums
 // in the rows' first threads).
 template <typename TC>
 __global__ __launch_bounds__(256) void layer_join_kernel(LayerParams p)

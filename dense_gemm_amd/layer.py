@@ -94,9 +94,16 @@ def _run(function, index, args):
         raise LayerError(function, rc)
 
 
-# The library's choice of K ranges by shape.
-_fused_splits = functools.lru_cache(1024)(dg_gemm_fused_choose)  # noqa: F821
-_dw_splits = functools.lru_cache(1024)(dg_gemm_dw_choose)  # noqa: F821
+@functools.lru_cache(1024)
+def _fused_splits(*shape):
+    """The library's choice of K ranges by shape (1 where the call itself will refuse it)."""
+    return max(dg_gemm_fused_choose(*shape), 1)  # noqa: F821
+
+
+@functools.lru_cache(1024)
+def _dw_splits(*shape):
+    return max(dg_gemm_dw_choose(*shape), 1)  # noqa: F821
+
 
 # (operand, output) -> the library's dtype
 _DTYPES = {(torch.float32, torch.float32): DG_F32, (torch.float16, torch.float16): DG_F16_F32ACC,

@@ -503,7 +503,7 @@ int dg_gemm_act_grad(dg_op_t transB, int64_t groups, const int32_t *offsets, int
  *   splits: ranges of each group's rows (0: the library's choice, as dg_gemm_fused;
  *   dg_gemm_dw_choose), their fp32 sums in the workspace of
  *   dg_layer_workspace_size(groups, M, N, splits) bytes.
- *   DG_ERR_UNSUPPORTED as dg_gemm_fused.
+ *   DG_ERR_UNSUPPORTED as dg_gemm_fused (alone with dbias, without a product: M above 2^28).
  *   1 groups, 2 offsets, 3 rows, 4 M, 5 N, 6 alpha, 7 A, 8 lda, 9 B, 10 ldb, 11 beta,
  *   12 C, 13 ldc, 14 strideC, 15 dbias, 16 dtype, 17 splits, 18 workspace, 19
  *   workspace_bytes, 20 stream. */

@@ -288,6 +288,29 @@ def test_offsets_outside_the_matrices():
         torch.cuda.synchronize()
 
 
+def test_rows_claimed_by_many_groups():
+    """Offsets that go up and down claim the same rows many times over, more tiles than the
+    launch holds: it ends, and writes nothing outside the claimed rows."""
+    M, N, K = 150, 72, 64
+    rng = np.random.default_rng(5)
+    for ty in ("f32", "bf16"):
+        A = matrix(rng, M, K, T[ty])
+        for pairs in (3, 40, 300):
+            off = torch.tensor([20, M - 10] * pairs, dtype=torch.int32, device=DEV)
+            B = torch.randn(1, K, N, device=DEV).to(T[ty]).expand(2 * pairs - 1, K, N)
+            for kernel in [-1] + KERNELS:
+                whole = output(M, N, T[ty], 8)
+                if runs(kernel, lambda: dg.gemm_grouped(A, B, off, C=whole, kernel=kernel)) is not None:
+                    assert (whole[:20] == SENTINEL).all() and (whole[M - 10:] == SENTINEL).all()
+                    padding_kept(whole)
+            want = layer_ref.dw(np64(A[20:M - 10]), np64(A[20:M - 10]), None, out=T[ty])["C"]
+            got = dg.gemm_dw(A, A, offsets=off)              # every other group has the same rows, the rest none
+            for g in (0, pairs - pairs % 2, 2 * pairs - 2):
+                check(got[g], want)
+            assert (got[1] == 0).all()
+            torch.cuda.synchronize()
+
+
 # ---- K ranges -------------------------------------------------------------------------------
 @pytest.mark.parametrize("ty,out", PAIRS)
 @pytest.mark.parametrize("splits", [0, 2, 5, 16])
@@ -471,6 +494,39 @@ def test_captured_step():
             assert torch.equal(a, b)
 
 
+def test_two_graphs_of_split_sums():
+    """Two graphs whose split sums have workspaces of their own, replayed in turn and on two streams at once."""
+    A, B = [torch.randn(40, 2048, device=DEV).half() for _ in range(2)], torch.randn(2048, 72, device=DEV).half()
+    C = [torch.empty(40, 72, dtype=torch.float16, device=DEV) for _ in range(2)]
+    D = [torch.empty(2048, 2048, device=DEV) for _ in range(2)]
+    d = [torch.empty(2048, device=DEV) for _ in range(2)]
+    dg.gemm_fused(A[0], B, C[0], splits=4)
+    torch.cuda.synchronize()
+    graphs = []
+    for i in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            dg.gemm_fused(A[i], B, C[i], splits=4)
+            dg.gemm_dw(A[i], A[i], D[i], dbias=d[i], splits=2)
+        graphs.append(g)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for seed in range(4):
+        for a in A:
+            a.copy_(torch.randn(40, 2048, device=DEV))
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            if seed % 2:
+                with torch.cuda.stream(s):
+                    g.replay()
+            else:
+                g.replay()
+        torch.cuda.synchronize()
+        for i in range(2):
+            e = torch.empty(2048, device=DEV)
+            assert torch.equal(C[i], dg.gemm_fused(A[i], B, splits=4))
+            assert torch.equal(D[i], dg.gemm_dw(A[i], A[i], dbias=e, splits=2, out_dtype=torch.float32)) and torch.equal(d[i], e)
+
+
 def test_streams():
     """Calls on two streams at once, each with its own outputs; the caller's stream orders them."""
     M, D, F, G, dtype = 300, 256, 512, 4, torch.float16
@@ -527,6 +583,33 @@ def test_large_rows_against_a_sample():
     want = layer_ref.dw(np64(Z[:, cols]), np64(A), off.tolist())
     check(W[:, cols], want["C"])
     check(d[:, cols], want["dbias"])
+
+
+@pytest.mark.parametrize("ty", ["f16", "bf16"])
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_outputs_past_the_caches(kernel, ty):
+    """Outputs above 64 MB, with ragged ends and rows padded: sampled rows against 64 bits, and every element
+    against the first kernel's (whose own bound, of the same sums, doubles the tolerance)."""
+    M, N, K, t = 8200, 4099, 72, T[ty]
+    g = torch.Generator(device=DEV).manual_seed(7)
+    A, B = torch.randn(M, K, generator=g, device=DEV).to(t), (torch.randn(N, K, generator=g, device=DEV) / 9).to(t)
+    b, R = torch.randn(N, generator=g, device=DEV).to(t), torch.randn(M, N, generator=g, device=DEV).to(t)
+    kw = dict(transB=True, bias=b, activation="gelu", R=R)
+    C, Z = output(M, N, t, 5), output(M, N, t, 5)
+    if runs(kernel, lambda: dg.gemm_fused(A, B, C, Z=Z, kernel=kernel, **kw)) is None:
+        pytest.skip("the kernel does not take the problem")
+    padding_kept(C, Z)
+    rows = [0, 1, 255, 256, 4097, 8191, 8192, 8199]
+    want = layer_ref.forward(np64(A[rows]), np64(B), transB=True, bias=np64(b), activation="gelu", R=np64(R[rows]), beta=1.0, out=t)
+    check(C[rows], want["C"])
+    check(Z[rows], want["Z"])
+    # two roundings (half a step each) of fp32 values that differ by both sums' errors, each at most K 2^-24 times
+    # the sum of |a b| (K = 72 terms of 0.07 on average, 10 at the most), times gelu's slope 1.13: 1e-4
+    C0, Z0 = torch.empty(M, N, dtype=t, device=DEV), torch.empty(M, N, dtype=t, device=DEV)
+    dg.gemm_fused(A, B, C0, Z=Z0, kernel=0, **kw)
+    for x, y in ((C, C0), (Z, Z0)):
+        off = (x.float() - y.float()).abs() - torch.finfo(t).eps * torch.maximum(x.float().abs(), y.float().abs())
+        assert float(off.max()) < 2e-4
 
 
 def test_row_strides_past_32_bits():

@@ -88,6 +88,30 @@ def test_too_large_is_unsupported():
     assert dg.dg_gemm_dw_with_kernel(*{**DW, "kernel": -2}.values()) == u
 
 
+def test_choice_of_a_refused_shape():
+    """The library's choice of ranges never hides why a call is refused."""
+    huge = 2 ** 31 - 1
+    assert dg.dg_gemm_fused_choose(huge, 1, 8, 0, 1) == dg.DG_ERR_UNSUPPORTED
+    assert dg.layer._fused_splits(huge, 1, 8, 0, 1) == 1 and dg.layer._dw_splits(1, huge, 8, 8, 1) == 1
+
+
+def test_select():
+    names = dg.layer_kernel_names()
+    for dtype in range(5):
+        for M in (1, 16, 17, 500, 16384):
+            for groups in (0, 1, 8, 300):
+                for splits in (0, 1, 4):
+                    k = dg.dg_gemm_fused_select(M, 2048, 5632, 1, dtype, groups, splits)
+                    assert 0 <= k < len(names) and "any" not in names[k]
+                    k = dg.dg_gemm_dw_select(max(groups, 1), M, 512, 300, dtype, splits)
+                    assert 0 <= k < len(names) and "rows" not in names[k]
+    # one token reads its weights once; many rows go to large tiles (not in fp32: no such tile)
+    assert "16_rows" in names[dg.dg_gemm_fused_select(1, 2048, 5632, 1, dg.DG_BF16_F32ACC, 0, 0)]
+    assert names[dg.dg_gemm_fused_select(16384, 5632, 2048, 1, dg.DG_BF16_F32ACC, 0, 0)] == "layer_256x256"
+    assert dg.dg_gemm_fused_select(1, 1, 1, 0, 0, -1, 0) == -6 and dg.dg_gemm_fused_select(1, 1, 1, 0, 0, 0, 5000) == -7
+    assert dg.dg_gemm_dw_select(-1, 1, 1, 1, 0, 0) == -1 and dg.dg_gemm_dw_select(1, 1, 1, 1, 0, -1) == -6
+
+
 def test_error_names_the_argument():
     e = dg.LayerError("dg_gemm_fused", -13)
     assert "13 (bias)" in str(e) and e.status == -13

@@ -300,24 +300,35 @@ __device__ __forceinline__ bool layer_tile(const LayerParams &p, int bm, int bn,
     t.group = 0;
     t.row0 = 0;
     if (p.kind == LAYER_WEIGHTS) {
-        // Every group goes over all XCDs, in a multiple of 8 workgroups, the group with
-        // most rows first: a group's tiles take as long as it has rows, so that a group to
-        // an XCD, or a long one at the end, would leave the others idle (8 uneven groups of 2048
-        // rows, 5632 x 2048 on the 256 tile: 583 us, 375 with this; equal groups 371).
+        // Every group goes over all XCDs, in a multiple of 8 workgroups, and where groups are
+        // long the one with most rows first: a group's tiles take as long as it has rows, so that
+        // a group to an XCD, or a long one at the end, would leave the others idle (8 uneven
+        // groups of 2048 rows on average, 5632 x 2048 on the 256 tile: 583 us, 375 with this; equal
+        // groups 371).  Finding the order takes every wave a microsecond: 32 uneven groups
+        // of 2048 rows 388 us, 476 as they come (2048 x 1408), of 512 rows 147 and 150, of 128
+        // rows 104 and 90; 64 groups of 128 rows (1031 x 517) 73 and 60.
         const int per = p.tiles_m * p.tiles_n, slots = (per + 7) & ~7, slot = id / slots;
         id -= slot * slots;
         if (id >= per) return false;
         id = xcd_contiguous(id, per);
         t.group = slot;
-        if (p.offsets && p.groups > 1 && p.groups <= 64) {
+        int begin = 0, n = p.K;
+        if (p.offsets && p.groups > 1 && p.groups <= 64 && p.K >= 1024 * p.groups) {
             const int lane = threadIdx.x & 63;
-            int b, n = -1, rank = 0;
-            if (lane < p.groups) group_rows(p, lane, p.K, b, n);
-            for (int g = 0; g < p.groups; ++g) {
-                const int m = __builtin_amdgcn_readlane(n, g);
-                rank += m > n || (m == n && g < lane);
-            }
+            int b = 0, m = 0, rank = 0;
+            if (lane < p.groups) group_rows(p, lane, p.K, b, m);
+            // (rows and, among equals, the group, in one word; lanes past the groups come last)
+            const uint32_t key = lane < p.groups ? ((uint32_t)(m < 0x1ffffff ? m : 0x1ffffff) << 6 | (63 - lane)) + 1 : 0;
+            for (int g = 0; g < p.groups; g += 8)
+#pragma unroll
+                for (int u = 0; u < 8; ++u) rank += (uint32_t)__builtin_amdgcn_readlane(key, g + u) > key;
             t.group = __ffsll((unsigned long long)__ballot(rank == slot)) - 1;
+            begin = __builtin_amdgcn_readlane(b, t.group);
+            n = __builtin_amdgcn_readlane(m, t.group);
+        } else if (p.offsets) {
+            group_rows(p, slot, p.K, begin, n);
+            begin = __builtin_amdgcn_readfirstlane(begin);
+            n = __builtin_amdgcn_readfirstlane(n);
         }
         int tm, tn;
         walk_tiles(id, p.tiles_m, p.tiles_n, p.group_m, tm, tn);
@@ -325,10 +336,7 @@ __device__ __forceinline__ bool layer_tile(const LayerParams &p, int bm, int bn,
         t.n0 = tn * bn;
         t.rows = p.M;
         t.out0 = 0;
-        int begin = 0, n = p.K;
-        if (p.offsets) group_rows(p, t.group, p.K, begin, n);
-        t.row0 = __builtin_amdgcn_readfirstlane(begin);
-        n = __builtin_amdgcn_readfirstlane(n);
+        t.row0 = begin;
         t.k0 = 0;
         t.k_len = n;
         if (p.splits > 1) {
@@ -358,8 +366,9 @@ __device__ __forceinline__ bool layer_tile(const LayerParams &p, int bm, int bn,
         // (no group is counted with more tile rows than the launch has workgroups for,
         // so that no offsets, ascending or not, let the sums overflow)
         const int lane = threadIdx.x & 63, limit = gridDim.x / p.tiles_n;
+        int b, n;                               // of the group that a lane looked at last
         auto tiles_of = [&](int g) {
-            int b = 0, n = 0;
+            b = n = 0;
             if (g < p.groups) group_rows(p, g, p.M, b, n);
             const int x = (n + bm - 1) / bm;
             return x < limit ? x : limit;
@@ -373,7 +382,7 @@ __device__ __forceinline__ bool layer_tile(const LayerParams &p, int bm, int bn,
             return x;
         };
         int sum = scan(tiles_of(lane)), total = __builtin_amdgcn_readlane(sum, 63);
-        const int sum0 = sum, total0 = total;
+        const int sum0 = sum, total0 = total, b0 = b, n0 = n;
         for (int base = 64; base < p.groups && total < limit; base += 64) {
             sum = scan(tiles_of(base + lane));
             total += __builtin_amdgcn_readlane(sum, 63);
@@ -384,6 +393,8 @@ __device__ __forceinline__ bool layer_tile(const LayerParams &p, int bm, int bn,
         const int row = id / p.tiles_n;         // tile row, counted over all groups
         int base = 0, before = 0;
         sum = sum0;
+        b = b0;
+        n = n0;
         for (int upto = total0; row >= upto && base + 64 < p.groups;) {
             base += 64;
             before = upto;
@@ -397,10 +408,8 @@ __device__ __forceinline__ bool layer_tile(const LayerParams &p, int bm, int bn,
         const int upto = before + __builtin_amdgcn_readlane(sum, l);
         first = l == 0 ? before : before + __builtin_amdgcn_readlane(sum, l - 1);
         tiles_m = upto - first;
-        int begin, n;
-        group_rows(p, t.group, p.M, begin, n);
-        t.row0 = t.out0 = __builtin_amdgcn_readfirstlane(begin);
-        t.rows = __builtin_amdgcn_readfirstlane(n);
+        t.row0 = t.out0 = __builtin_amdgcn_readlane(b, l);
+        t.rows = __builtin_amdgcn_readlane(n, l);
     }
     int tm, tn;
     walk_tiles(id - first * p.tiles_n, tiles_m, p.tiles_n, p.group_m, tm, tn);

@@ -373,12 +373,13 @@ __device__ __forceinline__ bool layer_tile(const LayerParams &p, int bm, int bn,
             const int x = (n + bm - 1) / bm;
             return x < limit ? x : limit;
         };
-        auto scan = [&](int x) {                // inclusive sums over the lanes
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1) {
-                const int y = __shfl_up(x, d);
-                if (lane >= d) x += y;
-            }
+        auto scan = [&](int x) {                // inclusive sums over the lanes: within rows of 16, then over them
+            x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, false);
+            x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, false);
+            x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, false);
+            x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, false);
+            x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false);
+            x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false);
             return x;
         };
         int sum = scan(tiles_of(lane)), total = __builtin_amdgcn_readlane(sum, 63);

@@ -1,12 +1,16 @@
 // Few rows (single tokens, a decoding batch, a few tokens an expert): the product is
 // bound by reading the weights once.
 //
-// A workgroup takes 16 * MT rows of A and a strip of columns; its NWV waves share out
-// the summed index in steps of KS (32 of 16 bits, 16 of fp32) and their sums meet in
-// LDS in wave order.  Weights and rows come from global memory into fragments with no
-// barrier before the end, so that every wave keeps several steps of loads in flight.  The weights are the matrix instruction's row operand:
-// register e of lane l belongs to weight column 4 * (l / 16) + e of the fragment and to
-// row l % 16 of A.
+// A workgroup takes 16 rows of A and a strip of columns; its NWV waves share out the
+// summed index in steps of KS (32 of 16 bits, 16 of fp32) and their sums meet in LDS in
+// wave order.  Weights and rows come from global memory into fragments with no barrier
+// before the end, so that every wave keeps several steps of loads in flight.  The weights
+// are the matrix instruction's row operand: register e of lane l belongs to weight column
+// 4 * (l / 16) + e of the fragment and to row l % 16 of A.
+// Measured (bf16, weights stored N x K, in a graph): 1 x 5632 x 2048 with gelu 6.8 us, 3.4
+// TB/s (the same strips by 64-byte pieces, layer_16_rows, 7.9); 14 experts of 5632 x 2048
+// 71 us, 4.5 TB/s.  24 rows are two strips of rows that read the weights twice, from L2 the
+// second time: 24 x 2048 x 5632 10.7 us, bound by the wait for a chunk's loads.
 // STREAM (4-byte aligned rows): B passes through LDS on its way, so that a load
 // fetches 512 bytes in a row of it in place of 64 (probes of 5632 x 2048, 16 bits, read
 // alone: 4.3 against 5.8 us; 2048 columns of 12 KB 4.5 against 7.0).
@@ -54,7 +58,7 @@ template <> struct RowStep<float> {
 // The columns of a workgroup's strip.
 constexpr int layer_rows_columns(bool tb) { return tb ? 16 : 64; }
 
-template <typename T, int MT, bool TB, int NWV, bool STREAM>
+template <typename T, bool TB, int NWV, bool STREAM>
 __global__ __launch_bounds__(64 * NWV) void layer_rows_kernel(LayerParams p)
 {
     typedef RowStep<T> S;
@@ -62,31 +66,25 @@ __global__ __launch_bounds__(64 * NWV) void layer_rows_kernel(LayerParams p)
     typedef vec __attribute__((aligned(sizeof(T)))) vecu;
     typedef T T4 __attribute__((ext_vector_type(4)));
     typedef T4 __attribute__((aligned(sizeof(T)))) T4u;
-    constexpr int PER = S::PER, KS = 4 * PER, NF = TB ? 1 : 4, BN = layer_rows_columns(TB), OUT = 16 * MT * BN;
+    constexpr int PER = S::PER, KS = 4 * PER, NF = TB ? 1 : 4, BN = layer_rows_columns(TB), OUT = 16 * BN;
     // steps whose loads are in flight together
-    constexpr int U = STREAM ? 1 : TB ? (MT <= 2 ? 8 : 4) : 2;
+    constexpr int U = STREAM ? 1 : TB ? 8 : 2;
     static_assert(TB || !STREAM, "STREAM: B stored N x K");
-    constexpr int CHUNK = 16 * 512, RED = NWV * MT * NF * 64 * 16;
+    constexpr int CHUNK = 16 * 512, RED = NWV * NF * 64 * 16;
     constexpr int SMEM = STREAM && NWV * CHUNK > RED ? NWV * CHUNK : RED;
     __shared__ __attribute__((aligned(1024))) char smem_raw[SMEM];
-    typedef f32x4 red_t[MT][NF][64];
+    typedef f32x4 red_t[NF][64];
     red_t *red = (red_t *)smem_raw;
 
     LayerTile t;
-    if (!layer_tile(p, 16 * MT, BN, blockIdx.x, t)) return;
+    if (!layer_tile(p, 16, BN, blockIdx.x, t)) return;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, q = lane >> 4;
     const int K = t.k_len, steps = K / KS;
     // this lane's row of A, and its column (or its first of four, moved back from the
     // matrix's end: columns that it then shares with its neighbour are not its own)
-    const T *A[MT];
-    bool has[MT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        const int row = t.m0 + 16 * m + r;
-        has[m] = row < t.rows;
-        A[m] = (const T *)p.A + (t.row0 + (has[m] ? row : t.rows - 1)) * p.lda + t.k0 + PER * q;
-    }
+    const bool has = t.m0 + r < t.rows;
+    const T *A = (const T *)p.A + (t.row0 + (has ? t.m0 + r : t.rows - 1)) * p.lda + t.k0 + PER * q;
     const T *B = (const T *)p.B + t.group * p.strideB;
     if constexpr (TB) {
         const int col = t.n0 + r < p.N ? t.n0 + r : p.N - 1;
@@ -115,17 +113,13 @@ __global__ __launch_bounds__(64 * NWV) void layer_rows_kernel(LayerParams p)
         else fetch(0.f);
     }
 
-    f32x4 acc[MT][NF];
+    f32x4 acc[NF];
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int f = 0; f < NF; ++f) acc[m][f] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    for (int f = 0; f < NF; ++f) acc[f] = (f32x4){0.f, 0.f, 0.f, 0.f};
 
-    auto products = [&](const vec (&a)[MT], const vec (&b)[NF]) {
+    auto products = [&](vec a, const vec (&b)[NF]) {
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int f = 0; f < NF; ++f) acc[m][f] = S::mfma(b[f], a[m], acc[m][f]);
+        for (int f = 0; f < NF; ++f) acc[f] = S::mfma(b[f], a, acc[f]);
     };
     // The wave's chunks of 8 steps, 512 bytes of each of the 16 columns, through its own
     // 8 KB of LDS: a direct load fetches two columns' 512 bytes, and the 16-byte piece
@@ -145,14 +139,12 @@ __global__ __launch_bounds__(64 * NWV) void layer_rows_kernel(LayerParams p)
             const i32x4_rsrc rsrc = buffer_rsrc(base + (int64_t)ch * 512);
 #pragma unroll
             for (int i = 0; i < 8; ++i) load_lds16(off[i], rsrc, (unsigned)(uintptr_t)(mine + i * 1024));
-            vec a[8][MT];
+            vec a[8];
 #pragma unroll
-            for (int u = 0; u < 8; ++u)
-#pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    a[u][m] = (vec)(T)0.f;
-                    if (has[m]) a[u][m] = *(const vecu *)(A[m] + ((int64_t)ch * 8 + u) * KS);
-                }
+            for (int u = 0; u < 8; ++u) {
+                a[u] = (vec)(T)0.f;
+                if (has) a[u] = *(const vecu *)(A + ((int64_t)ch * 8 + u) * KS);
+            }
             wait_vmcnt<0>();
             asm volatile("" ::: "memory");
 #pragma unroll
@@ -166,7 +158,7 @@ __global__ __launch_bounds__(64 * NWV) void layer_rows_kernel(LayerParams p)
     }
     // U steps at a time, their loads first
     for (int s0 = chunks * 8 + wave * U; s0 < steps; s0 += NWV * U) {
-        vec a[U][MT], b[U];
+        vec a[U], b[U];
         T4 x[U][PER];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -178,11 +170,8 @@ __global__ __launch_bounds__(64 * NWV) void layer_rows_kernel(LayerParams p)
 #pragma unroll
                 for (int i = 0; i < PER; ++i) x[u][i] = *(const T4u *)(B + (k + i) * p.ldb);
             }
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                a[u][m] = (vec)(T)0.f;
-                if (has[m]) a[u][m] = *(const vecu *)(A[m] + k);
-            }
+            a[u] = (vec)(T)0.f;
+            if (has) a[u] = *(const vecu *)(A + k);
         }
         __builtin_amdgcn_sched_barrier(0);    // the loads stay ahead of the products
 #pragma unroll
@@ -204,7 +193,7 @@ __global__ __launch_bounds__(64 * NWV) void layer_rows_kernel(LayerParams p)
     if (K % KS != 0 && wave == NWV - 1) {
         const int64_t k = (int64_t)steps * KS;
         const int left = K - steps * KS - PER * q;
-        vec a[MT], f[NF];
+        vec a, f[NF];
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const bool in = i < left;
@@ -214,17 +203,14 @@ __global__ __launch_bounds__(64 * NWV) void layer_rows_kernel(LayerParams p)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) f[j][i] = in ? B[(k + i) * p.ldb + j] : (T)0.f;
             }
-#pragma unroll
-            for (int m = 0; m < MT; ++m) a[m][i] = in && has[m] ? A[m][k + i] : (T)0.f;
+            a[i] = in && has ? A[k + i] : (T)0.f;
         }
         products(a, f);
     }
 
     if constexpr (STREAM) __syncthreads();       // the chunks' memory is the sums' now
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int f = 0; f < NF; ++f) red[wave][m][f][lane] = acc[m][f];
+    for (int f = 0; f < NF; ++f) red[wave][f][lane] = acc[f];
     __syncthreads();
     auto finish = [&](auto type) {
         typedef decltype(type) TC;
@@ -248,7 +234,7 @@ __global__ __launch_bounds__(64 * NWV) void layer_rows_kernel(LayerParams p)
                 layer_bias<TC, 1>(p, t.group, col, bias);
             }
 #pragma unroll
-            for (int w = 0; w < NWV; ++w) v[0] += red[w][m >> 4][f][(lc >> 2) * 16 + (m & 15)][lc & 3];
+            for (int w = 0; w < NWV; ++w) v[0] += red[w][f][(lc >> 2) * 16 + m][lc & 3];
             if (p.splits > 1) layer_partial<1>(p, t, row, col, v);
             else layer_finish<TC, 1>(p, t, row, col, v, aux, bias);
         }

@@ -16,10 +16,10 @@ namespace dg {
 #define DG_LAYER_ANY(BM, BN, WM, WN, BK)                                                       \
     DG_LAYER_PIPE(BM, BN, WM, WN, 1, 2, BK, true, false), DG_LAYER_PIPE(BM, BN, WM, WN, 1, 2, BK, false, true), \
         DG_LAYER_PIPE(BM, BN, WM, WN, 1, 2, BK, true, true)
-#define DG_LAYER_ROWS(MT, NWV)                                                                 \
-    {(const void *)&layer_rows_kernel<T, MT, false, NWV, false>,                               \
-     (const void *)&layer_rows_kernel<T, MT, true, NWV, false>, nullptr}
-#define DG_LAYER_STREAM(MT, NWV) {nullptr, (const void *)&layer_rows_kernel<T, MT, true, NWV, true>, nullptr}
+#define DG_LAYER_ROWS(NWV)                                                                 \
+    {(const void *)&layer_rows_kernel<T, false, NWV, false>,                               \
+     (const void *)&layer_rows_kernel<T, true, NWV, false>, nullptr}
+#define DG_LAYER_STREAM(NWV) {nullptr, (const void *)&layer_rows_kernel<T, true, NWV, true>, nullptr}
 #define DG_LAYER_NONE {nullptr, nullptr, nullptr}
 
 template <typename T>
@@ -34,8 +34,8 @@ const void *layer_kernel_of(int config, int variant)
             DG_LAYER_NONE,
             DG_LAYER_PIPE(128, 128, 64, 64, 1, 4, 16, false, false),
             DG_LAYER_NONE,
-            DG_LAYER_ROWS(1, 8),
-            DG_LAYER_STREAM(1, 8),
+            DG_LAYER_ROWS(8),
+            DG_LAYER_STREAM(8),
         };
         return table[config][variant];
     } else {
@@ -47,8 +47,8 @@ const void *layer_kernel_of(int config, int variant)
             DG_LAYER_PIPE(128, 128, 64, 64, 2, 4, 64, false, false),
             DG_LAYER_PIPE(128, 128, 64, 64, 1, 2, 64, false, false),
             DG_LAYER_PIPE(256, 256, 128, 64, 1, 2, 64, false, false),
-            DG_LAYER_ROWS(1, 8),
-            DG_LAYER_STREAM(1, 8),
+            DG_LAYER_ROWS(8),
+            DG_LAYER_STREAM(8),
         };
         return table[config][variant];
     }

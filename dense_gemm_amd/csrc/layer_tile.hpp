@@ -320,6 +320,18 @@ __device__ __forceinline__ float sum8(V8 x)
 // waves; their sums meet in LDS at the end.
 // fp32: one barrier at a slab's start, the loads of slab kt + STAGES - 1 spread over its
 // MFMAs (or fetched before them and written after them).
+//
+// Measured, and what bounds it (M x N x K, weights N x K, in a graph):
+//   256 tile, bf16 16384 x 5632 x 2048 with gelu and Z: 368 us, 1.03 PFLOP/s, the matrix
+//     cores busy 55% of the units' cycles, no bank conflicts.  Its 1408 tiles are 5.5 rounds,
+//     each 44 us of products at the clock that the chip holds under them and 17 us of the first
+//     slabs, gelu and 64 MB of outputs.  Grouped (8 uneven experts) 412, the gradient through
+//     gelu 421, weight gradients 376; 8192^3 857 us, 1.28 PFLOP/s.
+//   128 tile with two K groups, fp16 512 x 5632 x 2048 through gelu's gradient: 21.6 us; 176
+//     tiles on 256 units, 11.7 us of them products.
+//   64 tile, fp16 over 64 experts of 64 rows, 1032 x 2040 through registers: 102 us for 287 MB.
+//   64 tile, fp32 511 x 1031 x 2047 in 3 ranges: 30 us (the matrix cores of units that hold two
+//     of the 408 workgroups 20 us) and 5 of join.
 template <typename T, int BM, int BN, int WM, int WN, int KG, bool DW, bool TB, int STAGES, int BK, bool RA, bool RB>
 __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * KG, 2) void layer_pipe_kernel(LayerParams p)
 {

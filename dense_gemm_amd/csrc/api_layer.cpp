@@ -111,7 +111,7 @@ bool supports(int k, const LayerShape &s)
 // below, the choice is 3% slower than the fastest kernel and ranges by geometric mean, 21% at
 // the 95th of a hundred, 2.8 times at the worst (64 groups with half a row each, K = 33).
 // Both sides of some choices (bf16, B stored N x K, M x N x K, us): 24 x 2048 x 5632 stream
-// 10.7, 64 deep in 6 ranges and their join 11.6, in one 18.9; 512 x 5632 x 2048 128 deep 22,
+// 8.8, 64 deep in 6 ranges and their join 11.6, in one 18.9; 512 x 5632 x 2048 128 deep 22,
 // 64 deep 27; 16384 x 5632 x 2048 256 343, 128 388.
 struct LayerTime {
     double fixed, tile, slab, share, out, read;

@@ -7,10 +7,10 @@
 // before the end, so that every wave keeps several steps of loads in flight.  The weights
 // are the matrix instruction's row operand: register e of lane l belongs to weight column
 // 4 * (l / 16) + e of the fragment and to row l % 16 of A.
-// Measured (bf16, weights stored N x K, in a graph): 1 x 5632 x 2048 with gelu 6.8 us, 3.4
+// Measured (bf16, weights stored N x K, in a graph): 1 x 5632 x 2048 with gelu 7.0 us, 3.3
 // TB/s (the same strips by 64-byte pieces, layer_16_rows, 7.9); 14 experts of 5632 x 2048
-// 71 us, 4.5 TB/s.  24 rows are two strips of rows that read the weights twice, from L2 the
-// second time: 24 x 2048 x 5632 10.7 us, bound by the wait for a chunk's loads.
+// 70 us, 4.6 TB/s.  24 rows are two strips of rows that read the weights twice, from L2 the
+// second time: 24 x 2048 x 5632 8.8 us, bound by the wait for a chunk's loads.
 // STREAM (4-byte aligned rows): B passes through LDS on its way, so that a load
 // fetches 512 bytes in a row of it in place of 64 (probes of 5632 x 2048, 16 bits, read
 // alone: 4.3 against 5.8 us; 2048 columns of 12 KB 4.5 against 7.0).
@@ -59,7 +59,7 @@ template <> struct RowStep<float> {
 constexpr int layer_rows_columns(bool tb) { return tb ? 16 : 64; }
 
 template <typename T, bool TB, int NWV, bool STREAM>
-__global__ __launch_bounds__(64 * NWV) void layer_rows_kernel(LayerParams p)
+__global__ __launch_bounds__(64 * NWV, 4) void layer_rows_kernel(LayerParams p)
 {
     typedef RowStep<T> S;
     typedef typename S::vec vec;
@@ -135,22 +135,65 @@ __global__ __launch_bounds__(64 * NWV) void layer_rows_kernel(LayerParams p)
             const int c = 2 * i + (lane >> 5), col = t.n0 + c < p.N ? c : p.N - 1 - t.n0;
             off[i] = (uint32_t)((int64_t)col * p.ldb * (int)sizeof(T)) + (((lane & 31) ^ c) << 4);
         }
+        // More than four rows of A come the same way, through registers and then the memory that
+        // B's chunk has left: 64-byte pieces of them take 10.7 us, this 8.8 (24 x 2048 x 5632;
+        // 14 experts 70.7 and 69.9; one token so 7.2, by pieces 6.8).  What a row that does not exist
+        // reads is not stored.
+        const int n = t.rows - t.m0;
+        const bool few = n <= 4;
+        const char *rows = (const char *)((const T *)p.A + (t.row0 + t.m0) * p.lda + t.k0);
+        uint32_t aoff[8];
+        if (!few) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int row = 2 * i + (lane >> 5);
+                aoff[i] = (uint32_t)((int64_t)(row < n ? row : n - 1) * p.lda * (int)sizeof(T)) + ((lane & 31) << 4);
+            }
+        }
+        // fragment u of a chunk in LDS, and the place of the pieces that a lane fetches of rows 2i
+        int frag = r * 512 + ((q ^ r) << 4), piece = (lane >> 5) * 512 + (((lane & 31) ^ (lane >> 5)) << 4);
+        auto b_of = [&](int u) { return *(const lds_vec_t *)(mine + (frag ^ (u << 6))); };
         for (int ch = wave; ch < chunks; ch += NWV) {
             const i32x4_rsrc rsrc = buffer_rsrc(base + (int64_t)ch * 512);
 #pragma unroll
             for (int i = 0; i < 8; ++i) load_lds16(off[i], rsrc, (unsigned)(uintptr_t)(mine + i * 1024));
+            // (opaque to the compiler, which would otherwise keep every address in a register)
+            asm volatile("" : "+v"(frag), "+v"(piece));
             vec a[8];
+            if (few) {
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                a[u] = (vec)(T)0.f;
-                if (has) a[u] = *(const vecu *)(A + ((int64_t)ch * 8 + u) * KS);
-            }
-            wait_vmcnt<0>();
-            asm volatile("" ::: "memory");
+                for (int u = 0; u < 8; ++u) {
+                    a[u] = (vec)(T)0.f;
+                    if (has) a[u] = *(const vecu *)(A + ((int64_t)ch * 8 + u) * KS);
+                }
+                wait_vmcnt<0>();
+                asm volatile("" ::: "memory");
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                const vec b[1] = {*(const lds_vec_t *)(mine + r * 512 + (((4 * u + q) ^ r) << 4))};
-                products(a[u], b);
+                for (int u = 0; u < 8; ++u) {
+                    const vec f[1] = {b_of(u)};
+                    products(a[u], f);
+                }
+            } else {
+                vec b[8];
+                const char *at = rows + (int64_t)ch * 512;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (2 * i < n) a[i] = *(const vecu *)(at + aoff[i]);
+                wait_vmcnt<0>();
+                asm volatile("" ::: "memory");
+#pragma unroll
+                for (int u = 0; u < 8; ++u) b[u] = b_of(u);
+                __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): read before it is overwritten
+                asm volatile("" ::: "memory");
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (2 * i < n) *(lds_vec_t *)(mine + (piece ^ (i << 5)) + i * 1024) = a[i];
+                asm volatile("" ::: "memory");
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    const vec f[1] = {b[u]};
+                    products(b_of(u), f);        // A's now
+                }
             }
             __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): read before it is overwritten
             asm volatile("" ::: "memory");

@@ -10,6 +10,7 @@
 #pragma once
 
 #include "gemm_common.hpp"
+#include "layer_ranges.hpp"
 
 namespace dg {
 
@@ -339,12 +340,7 @@ __device__ __forceinline__ bool layer_tile(const LayerParams &p, int bm, int bn,
         t.row0 = begin;
         t.k0 = 0;
         t.k_len = n;
-        if (p.splits > 1) {
-            const int chunk = ((n + p.splits - 1) / p.splits + 63) & ~63;
-            const int64_t b = (int64_t)blockIdx.y * chunk;
-            t.k0 = b < n ? (int)b : n;
-            t.k_len = n - t.k0 < chunk ? n - t.k0 : chunk;
-        }
+        if (p.splits > 1) range_of(n, p.splits, (int)blockIdx.y, t.k0, t.k_len);
         return true;
     }
     t.out0 = t.row0;
@@ -356,12 +352,7 @@ __device__ __forceinline__ bool layer_tile(const LayerParams &p, int bm, int bn,
         t.rows = p.M;
         if (id >= tiles_m * p.tiles_n) return false;
         id = xcd_contiguous(id, tiles_m * p.tiles_n);
-        if (p.splits > 1) {
-            const int chunk = ((p.K + p.splits - 1) / p.splits + 63) & ~63;
-            const int64_t b = (int64_t)blockIdx.y * chunk;
-            t.k0 = b < p.K ? (int)b : p.K;
-            t.k_len = p.K - t.k0 < chunk ? p.K - t.k0 : chunk;
-        }
+        if (p.splits > 1) range_of(p.K, p.splits, (int)blockIdx.y, t.k0, t.k_len);
     } else {
         // (no group is counted with more tile rows than the launch has workgroups for,
         // so that no offsets, ascending or not, let the sums overflow)

@@ -134,7 +134,8 @@ const LayerTime kTimeRowsT = {4.1, 0.0874, 0.225, 293, 2.0, 0.361};
 constexpr double kJoin = 2.9, kJoinMb = 0.45;
 
 // The kernel, and with *splits = 0 the K ranges, of least time; a forced kernel or
-// number of ranges stays.  More than one range has to gain a tenth.
+// number of ranges stays (but groups of rows have one).  More than one range has to
+// gain a tenth.
 int choose(const LayerShape &s, int kernel, int *splits)
 {
     const bool dw = s.kind == dg::LAYER_WEIGHTS;
@@ -142,7 +143,7 @@ int choose(const LayerShape &s, int kernel, int *splits)
     const double K = dw && s.ragged ? (double)s.K / (double)s.groups : (double)s.K;
     const double used = (double)(s.groups < s.M ? s.groups : s.M);
     const double weights = dw ? 0 : used * (double)s.N * K * (s.type == 0 ? 4e-6 : 2e-6);
-    const bool may_split = dw || !s.ragged;
+    if (s.ragged && !dw) *splits = 1;      // groups of rows are not split
     double best = 1e300;
     int k_best = -1, n_best = 1;
     for (int k = kernel == DG_KERNEL_AUTO ? 0 : kernel; k < (kernel == DG_KERNEL_AUTO ? kNumLayer : kernel + 1); ++k) {
@@ -155,7 +156,7 @@ int choose(const LayerShape &s, int kernel, int *splits)
                                 : !s.ragged ? (double)tiles_of(s.M, f.bm) * tn
                                             : (rows > used / 2 ? rows + used / 2 : used) * tn;
         static const int kRanges[] = {1, 2, 3, 4, 6, 8, 12, 16};
-        const int many = *splits > 0 || !may_split || f.loads >= ROWS || tiles > 512 || K < 512 ? 1 : 8;
+        const int many = *splits > 0 || f.loads >= ROWS || tiles > 512 || K < 512 ? 1 : 8;
         for (int i = 0; i < many; ++i) {
             const int n = *splits > 0 ? *splits : kRanges[i];
             if (i > 0 && (64. * n > K || tiles * n > 1024)) break;
@@ -174,7 +175,7 @@ int choose(const LayerShape &s, int kernel, int *splits)
             }
         }
     }
-    *splits = may_split ? n_best : 1;
+    *splits = n_best;
     return k_best;
 }
 

@@ -133,10 +133,16 @@ const LayerTime kTimeRowsT = {4.1, 0.0874, 0.225, 293, 2.0, 0.361};
 // A split sum's second launch and its partials' way out and back.
 constexpr double kJoin = 2.9, kJoinMb = 0.45;
 
+size_t workspace_bytes_of(int64_t groups, int64_t M, int64_t N, int splits)
+{
+    if (groups <= 0 || M <= 0 || N <= 0 || splits <= 1) return 0;
+    return (size_t)splits * (size_t)groups * (size_t)M * (size_t)(N + 1) * 4;     // and a bias's gradient
+}
+
 // The kernel, and with *splits = 0 the K ranges, of least time; a forced kernel or
 // number of ranges stays (but groups of rows have one).  More than one range has to
-// gain a tenth.
-int choose(const LayerShape &s, int kernel, int *splits)
+// gain a tenth, and the workspace holds those that are chosen.
+int choose(const LayerShape &s, int kernel, int *splits, size_t ws_bytes = SIZE_MAX)
 {
     const bool dw = s.kind == dg::LAYER_WEIGHTS;
     const double groups = dw ? (double)s.groups : 1, mb = groups * (double)s.M * (double)s.N * 4e-6;      // in fp32
@@ -159,7 +165,7 @@ int choose(const LayerShape &s, int kernel, int *splits)
         const int many = *splits > 0 || f.loads >= ROWS || tiles > 512 || K < 512 ? 1 : 8;
         for (int i = 0; i < many; ++i) {
             const int n = *splits > 0 ? *splits : kRanges[i];
-            if (i > 0 && (64. * n > K || tiles * n > 1024)) break;
+            if (i > 0 && (64. * n > K || tiles * n > 1024 || workspace_bytes_of(s.groups, s.M, s.N, n) > ws_bytes)) break;
             const double slabs = K <= 64. * n ? 1 : K / n / 64;
             double rounds = tiles * n / m.share;
             // an fp32 tile keeps its unit's matrix cores busy: the last round is a whole one
@@ -179,18 +185,10 @@ int choose(const LayerShape &s, int kernel, int *splits)
     return k_best;
 }
 
-size_t workspace_bytes_of(int64_t groups, int64_t M, int64_t N, int splits)
-{
-    if (groups <= 0 || M <= 0 || N <= 0 || splits <= 1) return 0;
-    return (size_t)splits * (size_t)groups * (size_t)M * (size_t)(N + 1) * 4;     // and a bias's gradient
-}
-
 int launch(LayerParams &p, const LayerShape &s, int dtype, int kernel, int splits, void *ws, size_t ws_bytes, int ws_arg,
            hipStream_t stream)
 {
-    // without a workspace, one range where the choice is the library's
-    if (splits == 0 && ws == nullptr) splits = 1;
-    kernel = choose(s, kernel, &splits);
+    kernel = choose(s, kernel, &splits, ws == nullptr ? 0 : ws_bytes);
     if (kernel < 0) return DG_ERR_UNSUPPORTED;
     const LayerFamily &f = kLayer[kernel];
     p.splits = splits;

@@ -465,9 +465,10 @@ size_t dg_act_backward_workspace_size(int64_t rows, int64_t cols);
  * Z not stored.  R may be C itself (ldr = ldc); otherwise outputs must not
  * overlap anything else.  beta == 0: R is not read.  K == 0 or alpha == 0: A and
  * B are not read.  M == 0 or N == 0 or groups == 0: nothing is done.
- *   splits: K ranges, as dg_gemm_splitk (0: the library's choice, which is one
- *   range without a workspace; dg_gemm_fused_choose; always one with offsets); their
- *   fp32 sums go to the workspace of dg_layer_workspace_size(1, M, N, splits) bytes.
+ *   splits: K ranges, as dg_gemm_splitk (0: the library's choice among those that the
+ *   workspace holds, one without a workspace; dg_gemm_fused_choose; always one with
+ *   offsets); their fp32 sums go to the workspace of dg_layer_workspace_size(1, M, N,
+ *   splits) bytes.
  *   DG_ERR_UNSUPPORTED: M, N or K above 2^31 - 1025, or more tiles than a launch
  *   holds (2^32 / 256 of 64 x 64).
  *   1 transB, 2 groups, 3 offsets, 4 M, 5 N, 6 K, 7 alpha, 8 A, 9 lda, 10 B, 11 ldb,

@@ -30,3 +30,34 @@ def test_longest_sum_in_many_ranges(splits):
     print(f"weights, {splits} ranges", flush=True)
     d = torch.empty(1, device=DEV)
     assert dg.gemm_dw(few[:, None], one[:, None], dbias=d, splits=splits).item() == len(at) and d.item() == len(at)
+
+
+# ---- the library's choice of ranges -----------------------------------------------------------
+def fused_call(A, B, C, splits, workspace, nbytes):
+    """dg_gemm_fused, C = A B^T, with a workspace of `nbytes` bytes."""
+    (M, K), N = A.shape, B.shape[0]
+    code = {torch.float16: dg.DG_F16_F32ACC, torch.bfloat16: dg.DG_BF16_F32ACC, torch.float32: dg.DG_F32}[A.dtype]
+    return dg.dg_gemm_fused(1, 1, None, M, N, K, 1.0, A.data_ptr(), A.stride(0), B.data_ptr(), B.stride(0), 0, None, 0, dg.DG_EPI_NONE,
+                            None, N, 0.0, None, N, C.data_ptr(), C.stride(0), code, splits, workspace.data_ptr(), nbytes,
+                            torch.cuda.current_stream().cuda_stream)
+
+
+@pytest.mark.parametrize("ty", ["f16", "f32"])
+@pytest.mark.parametrize("M,N,K", [(64, 2047, 5631), (16, 96, 5631), (40, 130, 2049), (3, 1000, 4095)])
+def test_choice_within_the_workspace(M, N, K, ty):
+    """splits = 0 takes no more ranges than the workspace holds, whatever its size and however the
+    operands lie (the query's answer is for aligned ones)."""
+    rng = np.random.default_rng(K)
+    t = T[ty]
+    n = dg.dg_gemm_fused_choose(M, N, K, 1, dg.DG_F16_F32ACC if ty == "f16" else dg.DG_F32)
+    A, B = (torch.from_numpy(rng.standard_normal(s) / 8).to(t).to(DEV) for s in ((M, K), (N, K)))
+    want = layer_ref.forward(np64(A), np64(B), transB=True, out=t)["C"]
+    for ranges in (n, 0, 1, 2, 3, 16):
+        nbytes = dg.dg_layer_workspace_size(1, M, N, ranges) or 16
+        for less in (0, 4):
+            ws = torch.full((nbytes // 4 + 64,), float("nan"), device=DEV)
+            C = torch.full((M, N), float("nan"), dtype=t, device=DEV)
+            assert fused_call(A, B, C, 0, ws, nbytes - less) == dg.DG_OK, (ranges, less)
+            check(C, want)
+            assert torch.isnan(ws[(nbytes - less) // 4:]).all()
+    assert fused_call(A, B, C, 3, ws, dg.dg_layer_workspace_size(1, M, N, 3) - 4) == -26

@@ -287,30 +287,46 @@ int rows_product(const RowsCall &c, LayerParams &p, F between)
     return launch(p, s, c.dtype, c.kernel, c.splits, c.workspace, c.workspace_bytes, 25, (hipStream_t)c.stream);
 }
 
-// The choice for operands that the direct loads take, or -i (1 M, 2 N, 3 K, 4 transB, 5
-// dtype; 1 groups, 2 rows, 3 M, 4 N, 5 dtype).
-int select_rows(int transB, int64_t groups, int64_t M, int64_t N, int64_t K, int dtype, bool ragged, int *splits)
+// An operand as a query of the choice knows it: by its address and row stride, or one
+// that the direct loads take.
+struct Operand {
+    const void *x;
+    int64_t ld;
+};
+constexpr Operand kAligned = {nullptr, 0};
+
+// The choice for such operands, or -i (1 M, 2 N, 3 K, 4 transB, 5 dtype; 1 groups, 2
+// rows, 3 M, 4 N, 5 dtype; 7 A's row stride, 9 B's).
+int select_rows(int transB, int64_t groups, int64_t M, int64_t N, int64_t K, int dtype, bool ragged, int *splits,
+                Operand A = kAligned, Operand B = kAligned)
 {
     if (M < 0 || M > kMaxDim) return -1;
     if (N < 0 || N > kMaxDim) return -2;
     if (K < 0 || K > kMaxDim) return -3;
     if (transB != DG_OP_N && transB != DG_OP_T) return -4;
     if (!is_dtype(dtype)) return -5;
+    if (A.ld < 0) return -7;
+    if (B.ld < 0) return -9;
+    const int64_t eb = bytes_of(operand_type(dtype));
     const LayerShape s = {dg::LAYER_FORWARD, operand_type(dtype), transB == DG_OP_T, ragged, max1(groups), max1(M), max1(N), K,
-                          output_type(dtype) == 0, true, true};
+                          output_type(dtype) == 0, direct_ok(A.x, A.ld, 0, eb), direct_ok(B.x, B.ld, 0, eb)};
     const int k = choose(s, DG_KERNEL_AUTO, splits);
     return k < 0 ? DG_ERR_UNSUPPORTED : k;
 }
 
-int select_dw(int64_t groups, int64_t rows, int64_t M, int64_t N, int dtype, int *splits)
+int select_dw(int64_t groups, int64_t rows, int64_t M, int64_t N, int dtype, int *splits, Operand A = kAligned,
+              Operand B = kAligned)
 {
     if (groups < 0 || groups > kMaxGroups) return -1;
     if (rows < 0 || rows > kMaxDim) return -2;
     if (M < 0 || M > kMaxDim) return -3;
     if (N < 0 || N > kMaxDim) return -4;
     if (!is_dtype(dtype)) return -5;
+    if (A.ld < 0) return -7;
+    if (B.ld < 0) return -9;
+    const int64_t eb = bytes_of(operand_type(dtype));
     const LayerShape s = {dg::LAYER_WEIGHTS, operand_type(dtype), false, groups > 1, max1(groups), max1(M), max1(N), rows,
-                          output_type(dtype) == 0, true, true};
+                          output_type(dtype) == 0, direct_ok(A.x, A.ld, 0, eb), direct_ok(B.x, B.ld, 0, eb)};
     const int k = choose(s, DG_KERNEL_AUTO, splits);
     return k < 0 ? DG_ERR_UNSUPPORTED : k;
 }
@@ -472,6 +488,14 @@ int dg_gemm_fused_choose(int64_t M, int64_t N, int64_t K, dg_op_t transB, dg_dty
     return k < 0 ? k : splits;
 }
 
+int dg_gemm_fused_choose_for(int64_t M, int64_t N, int64_t K, dg_op_t transB, dg_dtype_t dtype, const void *A, int64_t lda,
+                             const void *B, int64_t ldb)
+{
+    int splits = 0;
+    const int k = select_rows(transB, 1, M, N, K, dtype, false, &splits, {A, lda}, {B, ldb});
+    return k < 0 ? k : splits;
+}
+
 int dg_gemm_fused_select(int64_t M, int64_t N, int64_t K, dg_op_t transB, dg_dtype_t dtype, int64_t groups, int splits)
 {
     if (groups < 0 || groups > kMaxGroups) return -6;
@@ -483,6 +507,14 @@ int dg_gemm_dw_choose(int64_t groups, int64_t rows, int64_t M, int64_t N, dg_dty
 {
     int splits = 0;
     const int k = select_dw(groups, rows, M, N, dtype, &splits);
+    return k < 0 ? k : splits;
+}
+
+int dg_gemm_dw_choose_for(int64_t groups, int64_t rows, int64_t M, int64_t N, dg_dtype_t dtype, const void *A, int64_t lda,
+                          const void *B, int64_t ldb)
+{
+    int splits = 0;
+    const int k = select_dw(groups, rows, M, N, dtype, &splits, {A, lda}, {B, ldb});
     return k < 0 ? k : splits;
 }
 

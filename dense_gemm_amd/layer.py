@@ -41,11 +41,13 @@ _SIGNATURES = {
     "dg_gemm_fused": (_ci, _FUSED, _FUSED_NAMES),
     "dg_gemm_fused_with_kernel": (_ci, _FUSED + [_ci], _FUSED_NAMES + " kernel"),
     "dg_gemm_fused_choose": (_ci, [_i64, _i64, _i64, _ci, _ci], "M N K transB dtype"),
+    "dg_gemm_fused_choose_for": (_ci, [_i64, _i64, _i64, _ci, _ci, _vp, _i64, _vp, _i64], "M N K transB dtype A lda B ldb"),
     "dg_gemm_act_grad": (_ci, _GRAD, _GRAD_NAMES),
     "dg_gemm_act_grad_with_kernel": (_ci, _GRAD + [_ci], _GRAD_NAMES + " kernel"),
     "dg_gemm_dw": (_ci, _DW, _DW_NAMES),
     "dg_gemm_dw_with_kernel": (_ci, _DW + [_ci], _DW_NAMES + " kernel"),
     "dg_gemm_dw_choose": (_ci, [_i64, _i64, _i64, _i64, _ci], "groups rows M N dtype"),
+    "dg_gemm_dw_choose_for": (_ci, [_i64, _i64, _i64, _i64, _ci, _vp, _i64, _vp, _i64], "groups rows M N dtype A lda B ldb"),
     "dg_gemm_fused_select": (_ci, [_i64, _i64, _i64, _ci, _ci, _i64, _ci], "M N K transB dtype groups splits"),
     "dg_gemm_dw_select": (_ci, [_i64, _i64, _i64, _i64, _ci, _ci], "groups rows M N dtype splits"),
     "dg_layer_workspace_size": (_sz, [_i64, _i64, _i64, _ci], "groups M N splits"),
@@ -95,14 +97,15 @@ def _run(function, index, args):
 
 
 @functools.lru_cache(1024)
-def _fused_splits(*shape):
-    """The library's choice of K ranges by shape (1 where the call itself will refuse it)."""
-    return max(dg_gemm_fused_choose(*shape), 1)  # noqa: F821
+def _fused_splits(M, N, K, transB, dtype, A=0, lda=0, B=0, ldb=0):
+    """The library's choice of K ranges by shape and alignment, A and B being addresses modulo
+    4 (1 where the call itself will refuse it)."""
+    return max(dg_gemm_fused_choose_for(M, N, K, transB, dtype, A, lda, B, ldb), 1)  # noqa: F821
 
 
 @functools.lru_cache(1024)
-def _dw_splits(*shape):
-    return max(dg_gemm_dw_choose(*shape), 1)  # noqa: F821
+def _dw_splits(groups, rows, M, N, dtype, A=0, lda=0, B=0, ldb=0):
+    return max(dg_gemm_dw_choose_for(groups, rows, M, N, dtype, A, lda, B, ldb), 1)  # noqa: F821
 
 
 # (operand, output) -> the library's dtype
@@ -164,19 +167,19 @@ def _product(grad, A, B, offsets, C, transB, alpha, bias, activation, Z, R, beta
     if dtype is None:
         raise TypeError(f"unsupported operand/output dtypes {A.dtype}/{cd} (float32, float16 or bfloat16 operands; an "
                         "output of the operand dtype, or float32)")
-    lda, ldc = _plain(A, "A", M, K), _plain(C, "C", M, N)
+    lda, ldc, a, b = _plain(A, "A", M, K), _plain(C, "C", M, N), A.data_ptr(), B.data_ptr()
     k, ldk = (None, N or 1) if keep is None else _rows(keep, "H" if grad else "Z", shape, cd)
     r, ldr = (None, N or 1) if R is None else _rows(R, "R", shape, cd)
     if offsets is not None:
         splits = 1
-    elif splits == 0:
-        splits = _fused_splits(M, N, K, transB, dtype)
+    elif splits == 0 and workspace is None:
+        splits = _fused_splits(M, N, K, transB, dtype, a & 3, lda, b & 3, ldb)
     if splits > 1 and workspace is None:
         workspace = _empty(dg_layer_workspace_size(1, M, N, splits), torch.uint8, A.device, stream)  # noqa: F821
     ws, wsb = (None, 0) if workspace is None else _workspace(workspace)
     if grad:
         z, ldz = _rows(Z, "Z", shape, cd)
-    b, stride_bias = None, 0
+    bias_at, stride_bias = None, 0
     if bias is not None:
         if bias.dtype != cd:
             raise TypeError("bias must have C's dtype")
@@ -187,15 +190,15 @@ def _product(grad, A, B, offsets, C, transB, alpha, bias, activation, Z, R, beta
             if bias.shape != (groups, N) or (N > 1 and bias.stride(1) != 1):
                 raise ValueError(f"bias must be [{groups}, {N}], its rows contiguous")
             stride_bias = bias.stride(0) if groups > 1 else 0
-        b = bias.data_ptr()
+        bias_at = bias.data_ptr()
     index, handle = _stream_of(stream, (A, B, C, offsets, workspace, bias, Z, R, keep))
     if grad:
         _run("dg_gemm_act_grad_with_kernel", index,
-             (transB, groups, address, M, N, K, alpha, A.data_ptr(), lda, B.data_ptr(), ldb, strideB, beta, r, ldr, k, ldk,
+             (transB, groups, address, M, N, K, alpha, a, lda, b, ldb, strideB, beta, r, ldr, k, ldk,
               activation, z, ldz, C.data_ptr(), ldc, dtype, splits, ws, wsb, handle, kernel))
         return C
     _run("dg_gemm_fused_with_kernel", index,
-         (transB, groups, address, M, N, K, alpha, A.data_ptr(), lda, B.data_ptr(), ldb, strideB, b, stride_bias, activation,
+         (transB, groups, address, M, N, K, alpha, a, lda, b, ldb, strideB, bias_at, stride_bias, activation,
           k, ldk, beta, r, ldr, C.data_ptr(), ldc, dtype, splits, ws, wsb, handle, kernel))
     return C
 
@@ -218,9 +221,9 @@ def gemm_fused(A, B, C=None, transB=False, alpha=1.0, bias=None, activation="non
     R may be C itself.  activation: "none", "relu" or "gelu".  Sums are fp32, and
     each output is rounded once.
 
-    `splits` cuts K into ranges (0: the library's choice) whose fp32 sums go to
-    `workspace`, a 16-byte aligned tensor of dg_layer_workspace_size(1, M, N,
-    splits) bytes, or to one allocated here."""
+    `splits` cuts K into ranges (0: the library's choice, among those that a given
+    workspace holds) whose fp32 sums go to `workspace`, a 16-byte aligned tensor of
+    dg_layer_workspace_size(1, M, N, splits) bytes, or to one allocated here."""
     return _product(False, A, B, None, C, transB, alpha, bias, _activation(EPILOGUES, activation), None, R, beta, Z, out_dtype,
                     splits, workspace, kernel, stream)
 
@@ -269,9 +272,10 @@ def gemm_dw(A, B, C=None, offsets=None, alpha=1.0, beta=0.0, dbias=None, out_dty
     [groups, M], contiguous), receives A's column sums, + beta * dbias; alpha does
     not scale it.
 
-    `splits` cuts every group's rows into ranges (0: the library's choice) whose
-    fp32 sums go to `workspace` (dg_layer_workspace_size(groups, M, N, splits)
-    bytes, 16-byte aligned) or to one allocated here."""
+    `splits` cuts every group's rows into ranges (0: the library's choice, among
+    those that a given workspace holds) whose fp32 sums go to `workspace`
+    (dg_layer_workspace_size(groups, M, N, splits) bytes, 16-byte aligned) or to one
+    allocated here."""
     if A.dim() != 2 or B.dim() != 2:
         raise ValueError("A and B must be 2-D")
     if B.dtype != A.dtype:
@@ -291,14 +295,14 @@ def gemm_dw(A, B, C=None, offsets=None, alpha=1.0, beta=0.0, dbias=None, out_dty
     if dbias is not None and (dbias.dtype != torch.float32 or dbias.shape != ((M,) if groups is None else (groups, M))
                               or not dbias.is_contiguous()):
         raise ValueError("dbias must be a contiguous float32 tensor of " + (f"[{M}]" if groups is None else f"[{groups}, {M}]"))
-    lda, ldb = _plain(A, "A", rows, M), _plain(B, "B", rows, N)
-    if splits == 0:
-        splits = _dw_splits(count, rows, M, N, dtype)
+    lda, ldb, a, b = _plain(A, "A", rows, M), _plain(B, "B", rows, N), A.data_ptr(), B.data_ptr()
+    if splits == 0 and workspace is None:
+        splits = _dw_splits(count, rows, M, N, dtype, a & 3, lda, b & 3, ldb)
     if splits > 1 and workspace is None:
         workspace = _empty(dg_layer_workspace_size(count, M, N, splits), torch.uint8, A.device, stream)  # noqa: F821
     ws, wsb = (None, 0) if workspace is None else _workspace(workspace)
     index, handle = _stream_of(stream, (A, B, C, offsets, dbias, workspace))
     _run("dg_gemm_dw_with_kernel", index,
-         (count, address, rows, M, N, alpha, A.data_ptr(), lda, B.data_ptr(), ldb, beta, C.data_ptr(), ldc, strideC,
+         (count, address, rows, M, N, alpha, a, lda, b, ldb, beta, C.data_ptr(), ldc, strideC,
           None if dbias is None else dbias.data_ptr(), dtype, splits, ws, wsb, handle, kernel))
     return C

@@ -466,7 +466,7 @@ size_t dg_act_backward_workspace_size(int64_t rows, int64_t cols);
  * overlap anything else.  beta == 0: R is not read.  K == 0 or alpha == 0: A and
  * B are not read.  M == 0 or N == 0 or groups == 0: nothing is done.
  *   splits: K ranges, as dg_gemm_splitk (0: the library's choice among those that the
- *   workspace holds, one without a workspace; dg_gemm_fused_choose; always one with
+ *   workspace holds, one without a workspace; dg_gemm_fused_choose_for; always one with
  *   offsets); their fp32 sums go to the workspace of dg_layer_workspace_size(1, M, N,
  *   splits) bytes.
  *   DG_ERR_UNSUPPORTED: M, N or K above 2^31 - 1025, or more tiles than a launch
@@ -502,7 +502,7 @@ int dg_gemm_act_grad(dg_op_t transB, int64_t groups, const int32_t *offsets, int
  * beta * dbias_g, unscaled by alpha.  A group without rows: beta * C_g and beta *
  * dbias_g.  beta == 0: C and dbias are not read; alpha == 0: B is not read.
  *   splits: ranges of each group's rows (0: the library's choice, as dg_gemm_fused;
- *   dg_gemm_dw_choose), their fp32 sums in the workspace of
+ *   dg_gemm_dw_choose_for), their fp32 sums in the workspace of
  *   dg_layer_workspace_size(groups, M, N, splits) bytes.
  *   DG_ERR_UNSUPPORTED as dg_gemm_fused (alone with dbias, without a product: M above 2^28).
  *   1 groups, 2 offsets, 3 rows, 4 M, 5 N, 6 alpha, 7 A, 8 lda, 9 B, 10 ldb, 11 beta,
@@ -514,11 +514,13 @@ int dg_gemm_dw(int64_t groups, const int32_t *offsets, int64_t rows, int64_t M, 
 
 /* The same with a forced kernel (the last argument; DG_KERNEL_AUTO: the library's
  * choice), for tests and measurement; DG_ERR_UNSUPPORTED when it cannot run the
- * problem.  The kernels' names (NULL when out of range).  For operands whose rows
- * are 4-byte aligned: the ranges that splits = 0 gives (_choose) and the kernel for so
- * many ranges (_select; 0: the library's choice; groups 0: none), or -i (1 M, 2 N, 3 K,
- * 4 transB, 5 dtype, 6 groups, 7 splits; 1 groups, 2 rows, 3 M, 4 N, 5 dtype, 6
- * splits).  The workspace's bytes: splits * groups * M * (N + 1) * 4, 0 for one range. */
+ * problem.  The kernels' names (NULL when out of range).  The ranges that splits = 0
+ * gives with a workspace that holds them: _choose_for for the operands that are given
+ * (their addresses are looked at, not read), _choose for ones with 4-byte aligned
+ * rows less than 8 MiB apart.  The kernel for so many ranges of those (_select; 0: the
+ * library's choice; groups 0: none).  Or -i (1 M, 2 N, 3 K, 4 transB, 5 dtype, 6 groups,
+ * 7 splits; 1 groups, 2 rows, 3 M, 4 N, 5 dtype, 6 splits; _choose_for: 7 lda, 9 ldb, below
+ * 0).  The workspace's bytes: splits * groups * M * (N + 1) * 4, 0 for one range. */
 int dg_gemm_fused_with_kernel(dg_op_t transB, int64_t groups, const int32_t *offsets, int64_t M, int64_t N, int64_t K,
                               float alpha, const void *A, int64_t lda, const void *B, int64_t ldb, int64_t strideB,
                               const void *bias, int64_t strideBias, dg_epilogue_t epilogue, void *Z, int64_t ldz, float beta,
@@ -534,8 +536,12 @@ int dg_gemm_dw_with_kernel(int64_t groups, const int32_t *offsets, int64_t rows,
                            int64_t strideC, float *dbias, dg_dtype_t dtype, int splits, void *workspace,
                            size_t workspace_bytes, void *stream, int kernel);
 int dg_gemm_fused_choose(int64_t M, int64_t N, int64_t K, dg_op_t transB, dg_dtype_t dtype);
+int dg_gemm_fused_choose_for(int64_t M, int64_t N, int64_t K, dg_op_t transB, dg_dtype_t dtype, const void *A, int64_t lda,
+                             const void *B, int64_t ldb);
 int dg_gemm_fused_select(int64_t M, int64_t N, int64_t K, dg_op_t transB, dg_dtype_t dtype, int64_t groups, int splits);
 int dg_gemm_dw_choose(int64_t groups, int64_t rows, int64_t M, int64_t N, dg_dtype_t dtype);
+int dg_gemm_dw_choose_for(int64_t groups, int64_t rows, int64_t M, int64_t N, dg_dtype_t dtype, const void *A, int64_t lda,
+                          const void *B, int64_t ldb);
 int dg_gemm_dw_select(int64_t groups, int64_t rows, int64_t M, int64_t N, dg_dtype_t dtype, int splits);
 size_t dg_layer_workspace_size(int64_t groups, int64_t M, int64_t N, int splits);
 const char *dg_layer_kernel_name(int kernel);

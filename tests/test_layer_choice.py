@@ -2,6 +2,9 @@
 GPU: the queries only compute)."""
 import random
 
+import pytest
+import torch
+
 import dense_gemm_amd as dg
 
 
@@ -13,3 +16,63 @@ def test_ranges_do_not_change_a_grouped_choice():
         want = dg.dg_gemm_fused_select(*shape, 1)
         for splits in (0, 2, 8, 4096):
             assert dg.dg_gemm_fused_select(*shape, splits) == want, (shape, splits)
+
+
+def test_choice_for_operands():
+    """The query for given operands: as the one for aligned ones where they are aligned, another where not;
+    the rows' distance and the address count."""
+    rng, other = random.Random(1), 0
+    for _ in range(3000):
+        M, N, K, tb, dtype = rng.randint(1, 600), rng.randint(16, 6000), rng.randint(16, 6000), rng.randrange(2), rng.randrange(5)
+        lda, ldb = -(-K // 2) * 2, -(-(K if tb else N) // 2) * 2
+        n = dg.dg_gemm_fused_choose(M, N, K, tb, dtype)
+        assert dg.dg_gemm_fused_choose_for(M, N, K, tb, dtype, 256, lda, 256, ldb) == n
+        odd = dg.dg_gemm_fused_choose_for(M, N, K, tb, dtype, 258, lda, 256, ldb)
+        assert 1 <= odd <= 16 and (dtype or odd == dg.dg_gemm_fused_choose_for(M, N, K, tb, dtype, 258, lda, 256, ldb))
+        assert odd == dg.dg_gemm_fused_choose_for(M, N, K, tb, dtype, 256, 1 << 23, 256, ldb)
+        if dtype:
+            assert odd == dg.dg_gemm_fused_choose_for(M, N, K, tb, dtype, 256, lda + 1, 256, ldb)
+        other += odd != n
+        groups = rng.randint(1, 40)
+        n = dg.dg_gemm_dw_choose(groups, K, M, N, dtype)
+        assert dg.dg_gemm_dw_choose_for(groups, K, M, N, dtype, 0, M + M % 2, 4, N + N % 2) == n
+        assert 1 <= dg.dg_gemm_dw_choose_for(groups, K, M, N, dtype, 0, M + M % 2, 2, N + N % 2) <= 16
+    assert other > 100
+    assert dg.dg_gemm_fused_choose_for(-1, 1, 1, 0, 0, 0, 1, 0, 1) == -1 and dg.dg_gemm_fused_choose_for(1, 1, 1, 0, 9, 0, 1, 0, 1) == -5
+    assert dg.dg_gemm_fused_choose_for(1, 1, 1, 0, 0, 0, -1, 0, 1) == -7 and dg.dg_gemm_fused_choose_for(1, 1, 1, 0, 0, 0, 1, 0, -1) == -9
+    assert dg.dg_gemm_dw_choose_for(70000, 1, 1, 1, 0, 0, 1, 0, 1) == -1 and dg.dg_gemm_dw_choose_for(1, 1, 1, 1, 0, 0, 1, 0, -1) == -9
+    assert dg.dg_gemm_fused_choose_for(2 ** 31 - 1, 1, 8, 0, 1, 0, 8, 0, 1) == dg.DG_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("shift,pad", [(0, 0), (1, 0), (0, 1), (1, 1)])
+def test_binding_takes_the_choice_of_its_operands(monkeypatch, shift, pad):
+    """What the torch functions pass for splits = 0 is the choice for the operands that they were given
+    (and 0 itself beside a caller's workspace, which bounds it)."""
+    calls = []
+    monkeypatch.setattr(dg.layer, "_stream_of", lambda stream, tensors: (0, None))
+    monkeypatch.setattr(dg.layer, "_run", lambda function, index, args: calls.append((function, args)))
+
+    def matrix(rows, cols):
+        whole = torch.zeros(rows * (cols + pad) + shift, dtype=torch.float16)
+        return whole[shift:].view(rows, cols + pad)[:, :cols]
+
+    ws, changed = torch.zeros(1 << 16, dtype=torch.uint8), False
+    for M, N, K in ((512, 1032, 5632), (24, 2048, 5632), (64, 2048, 5632), (100, 300, 2048)):
+        A, B = matrix(M, K), matrix(N, K)
+        for f in (lambda **kw: dg.gemm_fused(A, B, transB=True, **kw), lambda **kw: dg.gemm_act_grad(A, B, A[:, :1].expand(M, N).contiguous(), transB=True, **kw)):
+            names = dg.layer._SIGNATURES["dg_gemm_fused"][2].split()       # splits stands at the same place in both
+            f()
+            want = dg.dg_gemm_fused_choose_for(M, N, K, 1, 1, A.data_ptr(), A.stride(0), B.data_ptr(), B.stride(0))
+            assert calls.pop()[1][names.index("splits")] == want
+            changed |= want != dg.dg_gemm_fused_choose(M, N, K, 1, 1)
+            f(workspace=ws)
+            assert calls.pop()[1][names.index("splits")] == 0
+        X, Y = matrix(K, M), matrix(K, N)
+        names = dg.layer._SIGNATURES["dg_gemm_dw"][2].split()
+        dg.gemm_dw(X, Y)
+        want = dg.dg_gemm_dw_choose_for(1, K, M, N, 1, X.data_ptr(), X.stride(0), Y.data_ptr(), Y.stride(0))
+        assert calls.pop()[1][names.index("splits")] == want
+        changed |= want != dg.dg_gemm_dw_choose(1, K, M, N, 1)
+        dg.gemm_dw(X, Y, workspace=ws)
+        assert calls.pop()[1][names.index("splits")] == 0
+    assert changed == bool(shift or pad)

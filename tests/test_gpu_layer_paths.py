@@ -85,3 +85,52 @@ def test_library_choice_for_unaligned_operands(ty):
         check(got, layer_ref.dw(np64(X), np64(Y), out=t)["C"])
         several += (n > 1) + (m > 1)
     assert several
+
+
+# ---- row strides past 32 bits -------------------------------------------------------------------
+@pytest.mark.parametrize("kernel", [-1, 0, 1, 7])
+@pytest.mark.parametrize("ty", ["f16", "f32"])
+def test_far_rows(ty, kernel):
+    """Rows so far apart that 256 of them span more than 2^31 bytes, which the direct loads do not take: A, B
+    or both through registers, and every matrix of the epilogue, each by value."""
+    t, ld = T[ty], 5_000_000 // (torch.finfo(T[ty]).bits // 16)
+    rng = np.random.default_rng(2)
+    big = torch.full((300 * ld,), float("nan"), dtype=t, device=DEV).view(300, ld)
+    at = [0]
+
+    def far(rows, cols, std=1.0):
+        """Columns of their own of the wide matrix, with values."""
+        v = big[:rows, at[0]:at[0] + cols]
+        at[0] += cols + 64
+        return v.copy_(torch.from_numpy(rng.standard_normal((rows, cols)) * std))
+
+    def near(rows, cols, std=1.0):
+        return torch.from_numpy(rng.standard_normal((rows, cols)) * std).to(t).to(DEV)
+
+    M, N, K = 300, 44, 96
+    for a_far, b_far in ((1, 0), (0, 1), (1, 1)):
+        for transB in (False, True):
+            A, B = (far if a_far else near)(M, K), (far if b_far else near)(*((N, K) if transB else (K, N)), 0.1)
+            R, Z, C, K2, bias = far(M, N), far(M, N), far(M, N), far(M, N), near(1, N)[0]
+            kw = dict(transB=transB, kernel=kernel)
+            want = layer_ref.forward(np64(A), np64(B), transB=transB, bias=np64(bias), activation="gelu", R=np64(R), beta=0.5, out=t)
+            dg.gemm_fused(A, B, C, bias=bias, activation="gelu", R=R, beta=0.5, Z=Z, **kw)
+            check(C, want["C"], (a_far, b_far, transB))
+            check(Z, want["Z"], (a_far, b_far, transB))
+            want = layer_ref.forward(np64(A), np64(B), transB=transB, activation="relu", R=np64(R), out=t)
+            check(dg.gemm_fused(A, B, R, activation="relu", R=R, **kw), want["C"])            # the residual in place
+            want = layer_ref.act_grad(np64(A), np64(B), np64(Z), transB=transB, R=np64(R), beta=2.0, out=t)
+            dg.gemm_act_grad(A, B, Z, C, R=R, beta=2.0, H=K2, **kw)
+            check(C, want["C"])
+            check(K2, want["H"])
+            torch.cuda.synchronize()
+        if kernel == 7:
+            continue                                  # (few rows: no weight gradients)
+        X, Y, W = (far if a_far else near)(M, 40), (far if b_far else near)(M, 33), far(40, 33)
+        d = torch.randn(40, device=DEV)
+        want = layer_ref.dw(np64(X), np64(Y), beta=0.5, alpha=0.25, C=np64(W), dbias=np64(d), out=t)
+        check(dg.gemm_dw(X, Y, W, alpha=0.25, beta=0.5, dbias=d, kernel=kernel), want["C"])
+        check(d, want["dbias"])
+        off = torch.tensor([3, 100, 100, 290], dtype=torch.int32, device=DEV)
+        check(dg.gemm_dw(X, Y, offsets=off, kernel=kernel), layer_ref.dw(np64(X), np64(Y), off.tolist(), out=t)["C"])
+        torch.cuda.synchronize()

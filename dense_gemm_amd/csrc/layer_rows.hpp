@@ -272,7 +272,7 @@ __global__ __launch_bounds__(64 * NWV, 4) void layer_rows_kernel(LayerParams p)
             if constexpr (AHEAD) {
                 aux.x[0] = (TC)ahead_x;
                 bias[0] = ahead_bias;
-            } else {
+            } else if (p.splits <= 1) {       // (TC is their type then; a split's sums meet them in the join)
                 aux.fetch(p, t, row, col);
                 layer_bias<TC, 1>(p, t.group, col, bias);
             }

@@ -134,3 +134,29 @@ def test_far_rows(ty, kernel):
         off = torch.tensor([3, 100, 100, 290], dtype=torch.int32, device=DEV)
         check(dg.gemm_dw(X, Y, offsets=off, kernel=kernel), layer_ref.dw(np64(X), np64(Y), off.tolist(), out=t)["C"])
         torch.cuda.synchronize()
+
+
+# ---- few rows in K ranges ---------------------------------------------------------------------------
+@pytest.mark.parametrize("transB", [False, True])
+@pytest.mark.parametrize("ty,out", [("f16", "f16"), ("bf16", "bf16"), ("f16", "f32"), ("f32", "f32")])
+def test_few_rows_in_ranges(ty, out, transB):
+    """The few-rows kernel on a range of K: bias, residual, Z and what is kept belong to the join alone (the
+    kernel's sums are fp32 where those are 16 bits wide, so that it must not read them by its own type)."""
+    t, o = T[ty], T[out]
+    rows = dg.layer_kernel_names().index("layer_16_rows")
+    for i, (M, N, K) in enumerate([(1, 40, 512), (5, 40, 514), (16, 100, 300), (24, 68, 1100), (3, 260, 129)]):
+        rng = np.random.default_rng(i)
+        r = lambda a, b, d, s=1.0: torch.from_numpy(rng.standard_normal((a, b)) * s).to(d).to(DEV)  # noqa: E731
+        A, B, R, Z, bias = r(M, K, t), r(*((N, K) if transB else (K, N)), t, K ** -0.5), r(M, N, o), r(M, N, o), r(1, N, o)[0]
+        for kernel in (rows, -1):
+            for splits in (2, 3, 16, 0, 1):
+                keep = torch.empty(M, N, dtype=o, device=DEV)
+                want = layer_ref.forward(np64(A), np64(B), transB=transB, bias=np64(bias), activation="gelu", R=np64(R), beta=0.5, out=o)
+                got = dg.gemm_fused(A, B, transB=transB, bias=bias, activation="gelu", R=R, beta=0.5, Z=keep, out_dtype=o, splits=splits,
+                                    kernel=kernel)
+                check(got, want["C"], (M, N, K, kernel, splits))
+                check(keep, want["Z"])
+                want = layer_ref.act_grad(np64(A), np64(B), np64(Z), transB=transB, R=np64(R), out=o)
+                check(dg.gemm_act_grad(A, B, Z, transB=transB, R=R, H=keep, splits=splits, kernel=kernel), want["C"], (M, N, K, kernel, splits))
+                check(keep, want["H"])
+    torch.cuda.synchronize()

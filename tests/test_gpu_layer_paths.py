@@ -63,25 +63,26 @@ def test_choice_within_the_workspace(M, N, K, ty):
     assert fused_call(A, B, C, 3, ws, dg.dg_layer_workspace_size(1, M, N, 3) - 4) == -26
 
 
+@pytest.mark.parametrize("transB", [False, True])
+@pytest.mark.parametrize("pad", [0, 1])
 @pytest.mark.parametrize("ty", ["f16", "bf16", "f32"])
-def test_library_choice_for_unaligned_operands(ty):
-    """The torch functions with splits = 0 give, bit for bit, what the ranges of the query for their
-    operands give, and what the choice within a large enough workspace gives."""
+def test_the_library_s_choice(ty, pad, transB):
+    """The torch functions with splits = 0 give, bit for bit, what the library's choice of kernel and ranges
+    within a large enough workspace gives, aligned operands or not."""
     t, code = T[ty], {"f16": dg.DG_F16_F32ACC, "bf16": dg.DG_BF16_F32ACC, "f32": dg.DG_F32}[ty]
     g = torch.Generator(device=DEV).manual_seed(1)
-    r = lambda a, b: (torch.randn(a, b + 1, generator=g, device=DEV) / 8).to(t)[:, :b]  # noqa: E731
+    r = lambda a, b: (torch.randn(a, b + pad, generator=g, device=DEV) / 8).to(t)[:, :b]  # noqa: E731
     ws = torch.empty(1 << 26, dtype=torch.uint8, device=DEV)
     several = 0
-    for M, N, K in ((512, 1032, 5632), (64, 2048, 5632), (24, 300, 4096), (163, 328, 4202)):
-        A, B, X, Y = r(M, K), r(N, K), r(K, M), r(K, N)
-        n = dg.dg_gemm_fused_choose_for(M, N, K, 1, code, A.data_ptr(), A.stride(0), B.data_ptr(), B.stride(0))
-        got = dg.gemm_fused(A, B, transB=True)
-        assert torch.equal(got, dg.gemm_fused(A, B, transB=True, splits=n))
-        assert torch.equal(got, dg.gemm_fused(A, B, transB=True, workspace=ws))
-        check(got, layer_ref.forward(np64(A), np64(B), transB=True, out=t)["C"])
+    for M, N, K in ((512, 1032, 5632), (64, 2048, 5632), (24, 300, 4096), (163, 328, 4202), (2, 2048, 5632), (8, 1184, 4464)):
+        A, B, X, Y = r(M, K), r(*((N, K) if transB else (K, N))), r(K, M), r(K, N)
+        n = dg.dg_gemm_fused_choose_for(M, N, K, transB, code, A.data_ptr(), A.stride(0), B.data_ptr(), B.stride(0))
+        got = dg.gemm_fused(A, B, transB=transB)
+        assert torch.equal(got, dg.gemm_fused(A, B, transB=transB, workspace=ws))
+        check(got, layer_ref.forward(np64(A), np64(B), transB=transB, out=t)["C"])
         m = dg.dg_gemm_dw_choose_for(1, K, M, N, code, X.data_ptr(), X.stride(0), Y.data_ptr(), Y.stride(0))
         got = dg.gemm_dw(X, Y)
-        assert torch.equal(got, dg.gemm_dw(X, Y, splits=m)) and torch.equal(got, dg.gemm_dw(X, Y, workspace=ws))
+        assert torch.equal(got, dg.gemm_dw(X, Y, workspace=ws))
         check(got, layer_ref.dw(np64(X), np64(Y), out=t)["C"])
         several += (n > 1) + (m > 1)
     assert several

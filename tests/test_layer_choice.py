@@ -46,33 +46,41 @@ def test_choice_for_operands():
 
 @pytest.mark.parametrize("shift,pad", [(0, 0), (1, 0), (0, 1), (1, 1)])
 def test_binding_takes_the_choice_of_its_operands(monkeypatch, shift, pad):
-    """What the torch functions pass for splits = 0 is the choice for the operands that they were given
-    (and 0 itself beside a caller's workspace, which bounds it)."""
+    """For splits = 0 the torch functions leave the choice to the library, beside a workspace that holds the
+    ranges that it makes of the operands given, or without one pass one range.  A caller's workspace is
+    passed as it is."""
     calls = []
     monkeypatch.setattr(dg.layer, "_stream_of", lambda stream, tensors: (0, None))
-    monkeypatch.setattr(dg.layer, "_run", lambda function, index, args: calls.append((function, args)))
+    monkeypatch.setattr(dg.layer, "_run", lambda function, index, args: calls.append(dict(zip(dg.layer._SIGNATURES[function][2].split(), args))))
 
     def matrix(rows, cols):
         whole = torch.zeros(rows * (cols + pad) + shift, dtype=torch.float16)
         return whole[shift:].view(rows, cols + pad)[:, :cols]
 
     ws, changed = torch.zeros(1 << 16, dtype=torch.uint8), False
-    for M, N, K in ((512, 1032, 5632), (24, 2048, 5632), (64, 2048, 5632), (100, 300, 2048)):
-        A, B = matrix(M, K), matrix(N, K)
-        for f in (lambda **kw: dg.gemm_fused(A, B, transB=True, **kw), lambda **kw: dg.gemm_act_grad(A, B, A[:, :1].expand(M, N).contiguous(), transB=True, **kw)):
-            names = dg.layer._SIGNATURES["dg_gemm_fused"][2].split()       # splits stands at the same place in both
-            f()
-            want = dg.dg_gemm_fused_choose_for(M, N, K, 1, 1, A.data_ptr(), A.stride(0), B.data_ptr(), B.stride(0))
-            assert calls.pop()[1][names.index("splits")] == want
-            changed |= want != dg.dg_gemm_fused_choose(M, N, K, 1, 1)
-            f(workspace=ws)
-            assert calls.pop()[1][names.index("splits")] == 0
+
+    def passes(f, want, aligned, size):
+        nonlocal changed
+        f()
+        c = calls.pop()
+        assert (c["splits"], c["workspace_bytes"]) == ((0, dg.dg_layer_workspace_size(*size, want)) if want > 1 else (1, 0))
+        f(workspace=ws)
+        c = calls.pop()
+        assert (c["splits"], c["workspace_bytes"]) == (0, 1 << 16)
+        for splits in (1, 2):
+            f(splits=splits)
+            c = calls.pop()
+            assert (c["splits"], c["workspace_bytes"]) == (splits, dg.dg_layer_workspace_size(*size, splits))
+        changed |= want != aligned
+
+    for M, N, K in ((512, 1032, 5632), (24, 2048, 5632), (64, 2048, 5632), (100, 300, 2048), (2, 2048, 5632)):
+        for transB in (False, True):
+            A, B, Z = matrix(M, K), matrix(N, K) if transB else matrix(K, N), torch.zeros(M, N, dtype=torch.float16)
+            want = dg.dg_gemm_fused_choose_for(M, N, K, transB, 1, A.data_ptr(), A.stride(0), B.data_ptr(), B.stride(0))
+            aligned = dg.dg_gemm_fused_choose(M, N, K, transB, 1)
+            passes(lambda **kw: dg.gemm_fused(A, B, transB=transB, **kw), want, aligned, (1, M, N))
+            passes(lambda **kw: dg.gemm_act_grad(A, B, Z, transB=transB, **kw), want, aligned, (1, M, N))
         X, Y = matrix(K, M), matrix(K, N)
-        names = dg.layer._SIGNATURES["dg_gemm_dw"][2].split()
-        dg.gemm_dw(X, Y)
         want = dg.dg_gemm_dw_choose_for(1, K, M, N, 1, X.data_ptr(), X.stride(0), Y.data_ptr(), Y.stride(0))
-        assert calls.pop()[1][names.index("splits")] == want
-        changed |= want != dg.dg_gemm_dw_choose(1, K, M, N, 1)
-        dg.gemm_dw(X, Y, workspace=ws)
-        assert calls.pop()[1][names.index("splits")] == 0
+        passes(lambda **kw: dg.gemm_dw(X, Y, **kw), want, dg.dg_gemm_dw_choose(1, K, M, N, 1), (1, M, N))
     assert changed == bool(shift or pad)

@@ -161,3 +161,114 @@ def test_few_rows_in_ranges(ty, out, transB):
                 check(dg.gemm_act_grad(A, B, Z, transB=transB, R=R, H=keep, splits=splits, kernel=kernel), want["C"], (M, N, K, kernel, splits))
                 check(keep, want["H"])
     torch.cuda.synchronize()
+
+
+# ---- operands that lie differently ----------------------------------------------------------------
+PAIRS = [("f16", "f16"), ("bf16", "bf16"), ("f16", "f32"), ("bf16", "f32")]
+EVEN = [(65, 130, 200), (300, 516, 72), (17, 258, 192), (129, 64, 130), (5, 40, 514), (64, 64, 64)]      # rows that are aligned without padding
+SENTINEL = -77.0
+
+
+def placed(rng, rows, cols, dtype, odd, std=1.0):
+    """A matrix whose rows the direct loads take, or ("stride", "address") do not; NaN around it."""
+    pad, shift = (8 if odd is None else 1 if odd == "stride" else 8), (1 if odd == "address" else 0)
+    whole = torch.full((rows * (cols + pad) + shift,), float("nan"), dtype=dtype, device=DEV)
+    v = whole[shift:].view(rows, cols + pad)[:, :cols]
+    v.copy_(torch.from_numpy(rng.standard_normal((rows, cols)) * std))
+    bits = v.data_ptr() | v.stride(0) * v.element_size()
+    assert (bits % 4 != 0) == (odd is not None)
+    return v
+
+
+def output(rows, cols, dtype):
+    return torch.full((rows, cols + 3), SENTINEL, dtype=dtype, device=DEV)[:, :cols]
+
+
+def same_rows(t, want, offsets, M):
+    """Rows of the groups within their bounds, the others and the padding untouched."""
+    ref, bound = want
+    a, b = (0, M) if offsets is None else (offsets[0], offsets[-1])
+    check(t[a:b], (ref[a:b], bound[a:b]))
+    assert (t[:a] == SENTINEL).all() and (t[b:] == SENTINEL).all() and (t._base[:, t.shape[1]:] == SENTINEL).all()
+
+
+@pytest.mark.parametrize("odd_a,odd_b", [("stride", None), (None, "stride"), ("address", None), (None, "address"), ("stride", "address")])
+@pytest.mark.parametrize("transB", [False, True])
+@pytest.mark.parametrize("ty,out", PAIRS)
+def test_one_operand_unaligned(ty, out, transB, odd_a, odd_b):
+    """A or B alone through registers, dense and grouped, forward and backward."""
+    t, o = T[ty], T[out]
+    for kernel in (-1, 0, 1):
+        for i, (M, N, K) in enumerate(EVEN):
+            rng = np.random.default_rng(i)
+            A, B = placed(rng, M, K, t, odd_a), placed(rng, *((N, K) if transB else (K, N)), t, odd_b, 0.1)
+            R, C, Z = placed(rng, M, N, o, None), output(M, N, o), output(M, N, o)
+            kw = dict(transB=transB, R=R, kernel=kernel)
+            want = layer_ref.forward(np64(A), np64(B), transB=transB, activation="gelu", R=np64(R), out=o)
+            dg.gemm_fused(A, B, C, activation="gelu", Z=Z, splits=(1, 0, 3)[i % 3], **kw)
+            same_rows(C, want["C"], None, M)
+            same_rows(Z, want["Z"], None, M)
+            want = layer_ref.act_grad(np64(A), np64(B), np64(Z), transB=transB, R=np64(R), out=o)
+            dg.gemm_act_grad(A, B, Z, C, splits=(0, 2, 1)[i % 3], **kw)
+            same_rows(C, want["C"], None, M)
+            # groups, a matrix each (rows of odd length: every other matrix is aligned otherwise)
+            offsets = [M // 9, M // 3, M // 3, M // 2 + 1, M - M // 8]
+            rows = B.shape[0]
+            W = placed(rng, 4 * rows, B.shape[1], t, odd_b, 0.1)
+            W3 = W.as_strided((4, rows, B.shape[1]), (rows * W.stride(0), W.stride(0), 1), W.storage_offset())
+            off = torch.tensor(offsets, dtype=torch.int32, device=DEV)
+            C, H = output(M, N, o), output(M, N, o)
+            want = layer_ref.act_grad(np64(A), np64(W3), np64(Z), offsets, transB=transB, R=np64(R), out=o)
+            dg.gemm_grouped_act_grad(A, W3, off, Z, C, H=H, **kw)
+            same_rows(C, want["C"], offsets, M)
+            same_rows(H, want["H"], offsets, M)
+            C = output(M, N, o)
+            dg.gemm_grouped(A, W3, off, C, **kw)
+            same_rows(C, layer_ref.forward(np64(A), np64(W3), offsets, transB=transB, R=np64(R), out=o)["C"], offsets, M)
+            if transB:
+                continue
+            X, Y = placed(rng, M, N, t, odd_a), placed(rng, M, K, t, odd_b)
+            for off3, splits in ((None, (1, 3, 0)[i % 3]), (off, (2, 1, 0)[i % 3])):
+                G = 1 if off3 is None else 4
+                d = torch.empty((N,) if off3 is None else (G, N), device=DEV)
+                want = layer_ref.dw(np64(X), np64(Y), None if off3 is None else offsets, out=o)
+                check(dg.gemm_dw(X, Y, offsets=off3, dbias=d, splits=splits, out_dtype=o, kernel=kernel), want["C"])
+                check(d, want["dbias"])
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("ty,out", PAIRS + [("f32", "f32")])
+@pytest.mark.parametrize("kernel", dg.layer_kernel_names())
+def test_every_kernel_runs(kernel, ty, out):
+    """Forced on aligned operands of whole tiles, a kernel runs every operator but those it does not know:
+    no 256 tile and no deep 128 tile in fp32, no weights with few rows, no stream over a B stored K x N."""
+    k, t, o = dg.layer_kernel_names().index(kernel), T[ty], T[out]
+    never = ty == "f32" and kernel in ("layer_256x256", "layer_128x128_deep")
+    rows, stream = "rows" in kernel, "stream" in kernel
+    A, B = torch.randn(64, 256, device=DEV).to(t), (torch.randn(64, 256, device=DEV) / 16).to(t)
+    W, Z = B.t().contiguous(), torch.randn(64, 64, device=DEV).to(o)
+    off = torch.tensor([0, 20, 64], dtype=torch.int32, device=DEV)
+    for splits in (1, 2):
+        calls = {"fused nt": lambda: dg.gemm_fused(A, B, transB=True, out_dtype=o, splits=splits, kernel=k),
+                 "fused nn": lambda: dg.gemm_fused(A, W, out_dtype=o, splits=splits, kernel=k),
+                 "grad nt": lambda: dg.gemm_act_grad(A, B, Z, transB=True, splits=splits, kernel=k),
+                 "grad nn": lambda: dg.gemm_act_grad(A, W, Z, splits=splits, kernel=k),
+                 "dw": lambda: dg.gemm_dw(A, B, out_dtype=o, splits=splits, kernel=k),
+                 "grouped nt": lambda: dg.gemm_grouped(A, B.expand(2, 64, 256), off, transB=True, out_dtype=o, kernel=k),
+                 "grouped nn": lambda: dg.gemm_grouped(A, W.expand(2, 256, 64), off, out_dtype=o, kernel=k),
+                 "grouped dw": lambda: dg.gemm_dw(A, B, offsets=off, out_dtype=o, splits=splits, kernel=k)}
+        for name, call in calls.items():
+            if never or (rows and "dw" in name) or (stream and "nn" in name):
+                with pytest.raises(dg.LayerError) as e:
+                    call()
+                assert e.value.status == dg.DG_ERR_UNSUPPORTED
+                continue
+            got = call()
+            if "grad" in name:
+                want = layer_ref.act_grad(np64(A), np64(B), np64(Z), transB=True, out=o)["C"]
+            elif "dw" in name:
+                want = layer_ref.dw(np64(A), np64(B), off.tolist() if "grouped" in name else None, out=o)["C"]
+            else:
+                want = layer_ref.forward(np64(A), np64(B), transB=True, out=o)["C"]
+            check(got, want, name)
+    torch.cuda.synchronize()

@@ -272,3 +272,34 @@ def test_every_kernel_runs(kernel, ty, out):
                 want = layer_ref.forward(np64(A), np64(B), transB=True, out=o)["C"]
             check(got, want, name)
     torch.cuda.synchronize()
+
+
+# ---- few rows over long sums ------------------------------------------------------------------------
+@pytest.mark.parametrize("ty,out", PAIRS + [("f32", "f32")])
+@pytest.mark.parametrize("K", [2048, 4352, 5632, 6170])
+def test_streamed_rows_over_many_chunks(K, ty, out):
+    """Weights through LDS, several 512-byte chunks a wave (K = 4352: waves with two and with three of them in
+    16 bits; 6170: a last step that is not whole), with up to four rows and with more."""
+    t, o = T[ty], T[out]
+    stream = dg.layer_kernel_names().index("layer_16_rows_stream")
+    rng = np.random.default_rng(K)
+    r = lambda a, b, d, s=1.0: torch.from_numpy(rng.standard_normal((a, b)) * s).to(d).to(DEV)  # noqa: E731
+    N = 40
+    B, bias = r(N, K, t, K ** -0.5), r(1, N, o)[0]
+    W = r(3 * N, K, t, K ** -0.5).view(3, N, K)
+    for M in (1, 2, 4, 5, 15, 16, 24):
+        A, R, Z = r(M, K + 2, t)[:, :K], r(M, N, o), r(M, N, o)
+        off = torch.tensor([0, M // 3, M // 3, M], dtype=torch.int32, device=DEV)
+        for kernel in (stream, -1):
+            keep = torch.empty(M, N, dtype=o, device=DEV)
+            want = layer_ref.forward(np64(A), np64(B), transB=True, bias=np64(bias), activation="gelu", R=np64(R), out=o)
+            check(dg.gemm_fused(A, B, transB=True, bias=bias, activation="gelu", R=R, Z=keep, out_dtype=o, kernel=kernel), want["C"], (M, kernel))
+            check(keep, want["Z"])
+            want = layer_ref.act_grad(np64(A), np64(B), np64(Z), transB=True, activation="relu", out=o)
+            check(dg.gemm_act_grad(A, B, Z, transB=True, activation="relu", kernel=kernel), want["C"])
+            want = layer_ref.forward(np64(A), np64(W), off.tolist(), transB=True, R=np64(R), beta=0.5, out=o)
+            check(dg.gemm_grouped(A, W, off, transB=True, R=R, beta=0.5, out_dtype=o, kernel=kernel), want["C"])
+        want = layer_ref.forward(np64(A), np64(B), transB=True, out=o)["C"]
+        for splits in (2, 3):
+            check(dg.gemm_fused(A, B, transB=True, out_dtype=o, splits=splits, kernel=stream), want, splits)
+    torch.cuda.synchronize()

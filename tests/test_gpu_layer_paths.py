@@ -303,3 +303,39 @@ def test_streamed_rows_over_many_chunks(K, ty, out):
         for splits in (2, 3):
             check(dg.gemm_fused(A, B, transB=True, out_dtype=o, splits=splits, kernel=stream), want, splits)
     torch.cuda.synchronize()
+
+
+# ---- weight gradients of long groups, the longest first --------------------------------------------------
+ORDERS = {
+    "ascending": [500, 1000, 1500, 2000, 2500], "descending": [2500, 2000, 1500, 1000, 500], "one first behind": [900, 900, 900, 4000],
+    "equal": [1024] * 6, "ties and none": [0, 2100, 700, 2100, 0, 700, 2100], "all in one": [0, 0, 5000, 0], "two": [1000, 1300],
+    "sixty-four": [(97 * i * i) % 2077 + 200 * (i % 3) for i in range(64)], "sixty-five": [(97 * i * i) % 2077 + 200 * (i % 3) for i in range(65)],
+    "one row more": [1024, 1025, 1024, 1025],
+}
+
+
+@pytest.mark.parametrize("ty,out", [("f16", "f16"), ("bf16", "f32"), ("f32", "f32")])
+@pytest.mark.parametrize("name", list(ORDERS))
+def test_dw_in_order_of_length(name, ty, out):
+    """Groups of 1024 rows and more on average, up to 64 of them, go longest first: every order, ties, groups
+    without rows, rows of no group, on every kernel, in one range and more."""
+    sizes, t, o = ORDERS[name], T[ty], T[out]
+    head, tail = (3, 70) if name in ("ascending", "equal") else (0, 0)
+    offsets = [head + sum(sizes[:i]) for i in range(len(sizes) + 1)]
+    rows, G, M, N = offsets[-1] + tail, len(sizes), 72, 40
+    assert rows >= 1024 * G and (G <= 64) == (name != "sixty-five")
+    rng = np.random.default_rng(len(name))
+    X, Y = (torch.from_numpy(rng.standard_normal((rows, n))).to(t).to(DEV) for n in (M, N))
+    X[:head], X[rows - tail:] = float("nan"), float("nan")
+    C0, d0 = torch.randn(G, M, N, device=DEV).to(o), torch.randn(G, M, device=DEV)
+    off = torch.tensor(offsets, dtype=torch.int32, device=DEV)
+    want = layer_ref.dw(np64(X), np64(Y), offsets, beta=0.5, C=np64(C0), dbias=np64(d0), out=o)
+    for k, kernel in [(-1, "auto")] + list(enumerate(dg.layer_kernel_names())):
+        if "rows" in kernel or (ty == "f32" and kernel in ("layer_256x256", "layer_128x128_deep")):
+            continue
+        for splits in (0, 1, 3):
+            C, d = C0.clone(), d0.clone()
+            dg.gemm_dw(X, Y, C, offsets=off, beta=0.5, dbias=d, splits=splits, kernel=k)
+            check(C, want["C"], (kernel, splits))
+            check(d, want["dbias"], (kernel, splits))
+    torch.cuda.synchronize()

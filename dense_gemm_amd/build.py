@@ -29,7 +29,8 @@ SOURCES = ["api.cpp", "gemm_simple.hip", "gemm_f32.hip", "gemm_f16.hip", "gemm_b
 PROBE_LIB = os.path.join(PKG, "libdense_gemm_probe.so")
 PROBE_SOURCES = ["probe.hip"]
 HEADERS = ["gemm_common.hpp", "gemm_mfma.hpp", "gemm_pipe.hpp", "gemm_tables16.hpp", "mx_common.hpp",
-           "mx_tile.hpp", "layer_ranges.hpp", "layer_common.hpp", "layer_tile.hpp", "layer_tables.hpp"]
+           "mx_tile.hpp", "layer_ranges.hpp", "layer_common.hpp", "layer_tile.hpp", "layer_rows.hpp",
+           "layer_tables.hpp"]
 
 FLAGS = [
     "-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",

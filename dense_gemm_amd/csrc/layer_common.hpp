@@ -44,8 +44,6 @@ struct LayerParams {
     float *dbias;                   // weights: [groups][M], or NULL
 };
 
-typedef hipError_t (*layer_launch_fn)(const LayerParams &p, hipStream_t s);
-
 #ifdef __HIPCC__
 
 // Phi(-a) / exp(-a^2 / 2), a >= 0, for 16-bit results: half of erfc(z) exp(z^2), z = a /

@@ -126,18 +126,17 @@ __device__ __forceinline__ void layer_store(const LayerParams &p, const LayerTil
 }
 
 // ---- operands -------------------------------------------------------------------------
-// A 16-bit operand's slab of BK summed indices in LDS, as PipeOperandH lays it out (for
-// a BK of its own).  KCONT (rows of BK): the 16-byte chunk c of row r sits at chunk c
-// ^ swz(r), so that the 16 rows which a quarter wave reads together hit 16 distinct bank
-// groups.  Else (BK rows of BMN): the 64-byte quad q of row k sits at q ^ swz(k), and
-// fragments come from the transposing read.
-template <typename T, int BMN, bool KCONT, int NW, int BK_>
+// A 16-bit operand's slab of 64 summed indices in LDS, as PipeOperandH lays out its own.
+// KCONT (rows of 64): the 16-byte chunk c of row r sits at chunk c ^ swz(r), so that the
+// 16 rows which a quarter wave reads together hit 16 distinct bank groups.  Else (64 rows
+// of BMN): the 64-byte quad q of row k sits at q ^ swz(k), and fragments come from the
+// transposing read.
+template <typename T, int BMN, bool KCONT, int NW>
 struct SlabOperandH {
     typedef T V8 __attribute__((ext_vector_type(8)));
     typedef __attribute__((address_space(3))) V8 lds_v8_t;
-    static constexpr int BK = BK_, BYTES = BMN * BK * 2, SPAN = 1024, LOADS = BYTES / (NW * SPAN);
+    static constexpr int BK = 64, BYTES = BMN * BK * 2, SPAN = 1024, LOADS = BYTES / (NW * SPAN);
     static constexpr int ROW_BYTES = KCONT ? BK * 2 : BMN * 2;
-    static_assert(BK == 32 || BK == 64, "slabs of 32 or 64");
     static_assert(LOADS * NW * SPAN == BYTES, "whole loads");
     static_assert(KCONT || BMN == 64 || BMN % 128 == 0, "two quads, or four and more");
 
@@ -147,7 +146,7 @@ struct SlabOperandH {
 
     __device__ static __forceinline__ int swz(int r)
     {
-        if constexpr (KCONT) return BK == 64 ? (r >> 1) & 7 : (r >> 2) & 3;
+        if constexpr (KCONT) return (r >> 1) & 7;
         else return BMN == 64 ? (r >> 1) & 1 : r & 3;
     }
     // row and first column of the piece at byte b of a stage
@@ -207,10 +206,11 @@ struct SlabOperandS : PipeOperandS<BMN, KCONT, NW, 16, BK_> {
 //   REG = true: any strides and alignment, through registers: fetch() loads a slab
 //     (the GPU takes misaligned vectors), commit() writes it to its stage.
 template <typename T, int BMN, bool KCONT, int NW, int BK_, bool REG>
-struct LayerOperand : std::conditional<sizeof(T) == 2, SlabOperandH<T, BMN, KCONT, NW, BK_>,
+struct LayerOperand : std::conditional<sizeof(T) == 2, SlabOperandH<T, BMN, KCONT, NW>,
                                        SlabOperandS<BMN, KCONT, NW, BK_>>::type {
-    typedef typename std::conditional<sizeof(T) == 2, SlabOperandH<T, BMN, KCONT, NW, BK_>,
+    typedef typename std::conditional<sizeof(T) == 2, SlabOperandH<T, BMN, KCONT, NW>,
                                       SlabOperandS<BMN, KCONT, NW, BK_>>::type Base;
+    static_assert(Base::BK == BK_, "16 bits: slabs of 64");
     static constexpr int PER = 16 / (int)sizeof(T);       // elements of a piece, which a lane loads
     typedef T V __attribute__((ext_vector_type(PER)));
     typedef V __attribute__((aligned(sizeof(T)))) Vu;

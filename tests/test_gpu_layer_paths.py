@@ -339,3 +339,28 @@ def test_dw_in_order_of_length(name, ty, out):
             check(C, want["C"], (kernel, splits))
             check(d, want["dbias"], (kernel, splits))
     torch.cuda.synchronize()
+
+
+# ---- rounding of long fp32 sums -----------------------------------------------------------------------
+@pytest.mark.parametrize("kernel", [k for k in dg.layer_kernel_names() if k not in ("layer_256x256", "layer_128x128_deep")])
+def test_long_fp32_sums(kernel):
+    """fp32 sums go in chains of 1024 products at the most, and their sums in another, in every kernel.
+
+    The bound, by norm, for products that are random with mean zero: after j of them a chain holds sqrt(j) of their
+    size, and a rounding adds an error of at most 2^-24 / sqrt(3) of that by root mean square (uniform within half a
+    step, the step at most 2^-23 of the value). Over a chain of L: sqrt(L / 2) 2^-24 / sqrt(3) of the sum, over n chains'
+    sums sqrt(n / 2) more of it, and a rounding or two behind. A single chain of 8192 has 1.6e-6 to 2.2e-6, this bound 9.6e-7."""
+    k, K, M, N = dg.layer_kernel_names().index(kernel), 8192, 130, 72
+    rms = 2.0 ** -24 / 3 ** 0.5
+    bound = ((1024 / 2) ** 0.5 + (K / 1024 / 2) ** 0.5 + 3) * rms
+    g = torch.Generator(device=DEV).manual_seed(1)
+    r = lambda a, b: torch.randn(a, b, generator=g, device=DEV)  # noqa: E731
+    far = lambda got, want: float((got.double() - want).norm() / want.norm())  # noqa: E731
+    A, W, X = r(M, K), r(N, K), r(K, M)
+    want = A.double() @ W.double().t()
+    assert far(dg.gemm_fused(A, W, transB=True, kernel=k, splits=1), want) < bound
+    if "stream" not in kernel:
+        assert far(dg.gemm_fused(A, W.t().contiguous(), kernel=k, splits=1), want) < bound
+    if "rows" not in kernel:
+        Y = r(K, N)
+        assert far(dg.gemm_dw(X, Y, kernel=k, splits=1), X.double().t() @ Y.double()) < bound

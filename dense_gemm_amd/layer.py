@@ -108,14 +108,6 @@ def _dw_splits(groups, rows, M, N, dtype, A=0, lda=0, B=0, ldb=0):
     return max(dg_gemm_dw_choose_for(groups, rows, M, N, dtype, A, lda, B, ldb), 1)  # noqa: F821
 
 
-def _ranges(splits, choice, groups, M, N, shape):
-    """(what a call passes for `splits`, bytes of workspace to allocate).  Where the choice is the
-    library's and more than one range, the call leaves it to the library, which takes the
-    kernel that belongs to it."""
-    n = splits or choice(*shape)
-    return (splits if n > 1 else 1), dg_layer_workspace_size(groups, M, N, n)  # noqa: F821
-
-
 # (operand, output) -> the library's dtype
 _DTYPES = {(torch.float32, torch.float32): DG_F32, (torch.float16, torch.float16): DG_F16_F32ACC,
            (torch.bfloat16, torch.bfloat16): DG_BF16_F32ACC, (torch.float16, torch.float32): DG_F16_F32OUT,
@@ -180,10 +172,11 @@ def _product(grad, A, B, offsets, C, transB, alpha, bias, activation, Z, R, beta
     r, ldr = (None, N or 1) if R is None else _rows(R, "R", shape, cd)
     if offsets is not None:
         splits = 1
-    if workspace is None and splits != 1:
-        splits, need = _ranges(splits, _fused_splits, 1, M, N, (M, N, K, transB, dtype, a & 3, lda, b & 3, ldb))
-        if need:
-            workspace = _empty(need, torch.uint8, A.device, stream)
+    # more than one range by the library's choice: left to the call, whose kernel belongs to it
+    elif splits == 0 and workspace is None and (n := _fused_splits(M, N, K, transB, dtype, a & 3, lda, b & 3, ldb)) == 1:
+        splits = 1
+    if splits != 1 and workspace is None:
+        workspace = _empty(dg_layer_workspace_size(1, M, N, splits or n), torch.uint8, A.device, stream)  # noqa: F821
     ws, wsb = (None, 0) if workspace is None else _workspace(workspace)
     if grad:
         z, ldz = _rows(Z, "Z", shape, cd)
@@ -244,7 +237,7 @@ def gemm_grouped(A, B, offsets, C=None, transB=False, alpha=1.0, bias=None, acti
     offsets is an int32 tensor of groups + 1 ascending elements on the device (a
     group may be empty); B is [groups, K, N] or (transB) [groups, N, K]; bias is
     [groups, N].  Rows before offsets[0] and from offsets[-1] on are left as
-    they were, in every output."""
+    they were, in every output (in a C allocated here: uninitialised memory)."""
     return _product(False, A, B, offsets, C, transB, alpha, bias, _activation(EPILOGUES, activation), None, R, beta, Z,
                     out_dtype, 1, None, kernel, stream)
 
@@ -304,10 +297,11 @@ def gemm_dw(A, B, C=None, offsets=None, alpha=1.0, beta=0.0, dbias=None, out_dty
                               or not dbias.is_contiguous()):
         raise ValueError("dbias must be a contiguous float32 tensor of " + (f"[{M}]" if groups is None else f"[{groups}, {M}]"))
     lda, ldb, a, b = _plain(A, "A", rows, M), _plain(B, "B", rows, N), A.data_ptr(), B.data_ptr()
-    if workspace is None and splits != 1:
-        splits, need = _ranges(splits, _dw_splits, count, M, N, (count, rows, M, N, dtype, a & 3, lda, b & 3, ldb))
-        if need:
-            workspace = _empty(need, torch.uint8, A.device, stream)
+    # (more than one range by the library's choice, as in _product)
+    if splits == 0 and workspace is None and (n := _dw_splits(count, rows, M, N, dtype, a & 3, lda, b & 3, ldb)) == 1:
+        splits = 1
+    if splits != 1 and workspace is None:
+        workspace = _empty(dg_layer_workspace_size(count, M, N, splits or n), torch.uint8, A.device, stream)  # noqa: F821
     ws, wsb = (None, 0) if workspace is None else _workspace(workspace)
     index, handle = _stream_of(stream, (A, B, C, offsets, dbias, workspace))
     _run("dg_gemm_dw_with_kernel", index,

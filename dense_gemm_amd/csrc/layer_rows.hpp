@@ -19,6 +19,7 @@
 //   B stored K x N: 64 columns; lane l loads columns 4 * (l % 16) .. + 3 of the same
 //     k's rows, 4 x 8 elements that are transposed in registers into four
 //     fragments; fragment j holds columns 4 * (l % 16) + j.
+//     1 x 5632 x 2048 9.4 us; 1 x 2048 x 5632 in ranges of K and their join 10.4 (24 rows 13.2).
 // Any strides and alignment (the GPU takes misaligned vectors).
 #pragma once
 

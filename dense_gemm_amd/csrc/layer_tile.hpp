@@ -7,7 +7,6 @@
 // A group's last tile row and last slab end inside a tile: rows and columns past
 // the end are fetched from valid places and never stored, summed indices past the
 // end are zero.
-//
 #pragma once
 
 #include <type_traits>
@@ -329,7 +328,8 @@ __device__ __forceinline__ float sum8(V8 x)
 //     gelu 421, weight gradients 376; 8192^3 857 us, 1.28 PFLOP/s.
 //   128 tile with two K groups, fp16 512 x 5632 x 2048 through gelu's gradient: 21.6 us; 176
 //     tiles on 256 units, 11.7 us of them products.
-//   64 tile, fp16 over 64 experts of 64 rows, 1032 x 2040 through registers: 102 us for 287 MB.
+//   64 tile, fp16 over 64 experts of 64 rows, A's odd rows through registers, weights 2040 x 1032
+//     direct: 102 us for 287 MB, two slabs in flight (an operand through registers has two stages).
 //   64 tile, fp32 511 x 1031 x 2047 in 3 ranges: 30 us (the matrix cores of units that hold two
 //     of the 408 workgroups 20 us) and 5 of join.
 template <typename T, int BM, int BN, int WM, int WN, int KG, bool DW, bool TB, int STAGES, int BK, bool RA, bool RB>

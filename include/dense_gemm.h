@@ -455,8 +455,9 @@ size_t dg_act_backward_workspace_size(int64_t rows, int64_t cols);
  * are unspecified.  offsets = NULL (with groups = 1): all rows, one matrix.
  *
  * Sums and the epilogue are fp32; each output is rounded once.  With gelu = x Phi(x)
- * and gelu'(x) = Phi(x) + x phi(x), Phi is off by at most 6e-6 of its smaller
- * tail for 16-bit outputs, and by a few fp32 roundings for fp32 ones. */
+ * and gelu'(x) = Phi(x) + x phi(x), Phi's smaller tail is off by at most 6.5e-6 + 4e-7 x^2
+ * of itself for 16-bit outputs, and 1e-6 + 2.4e-7 x^2 for fp32 ones (x^2: the exponential's
+ * argument is an fp32 number). */
 
 /* Z = alpha * A op(B_g) + bias_g;  C = act(Z) + beta * R.
  * A holds M rows of K, C (and R, Z) M rows of N; op(B) is K x N, group g's matrix

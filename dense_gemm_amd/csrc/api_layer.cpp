@@ -107,10 +107,10 @@ bool supports(int k, const LayerShape &s)
 // rounds as the tiles need, `share` of them a round, but no less than the weights'
 // megabytes times `read`; + C's megabytes times `out`.  Fitted to the times, replayed
 // in a graph, of 12182 random problems (1 to 16384 rows, 32 to 6000 columns and summed
-// indices, 0 to 64 groups, aligned and not, all types).  On 8740 others of these sizes the
-// choice, ranges included, is 3.3% slower than the fastest kernel and ranges by geometric mean,
+// indices, 0 to 64 groups, aligned and not, all types).  On 8763 others of these sizes the
+// choice, ranges included, is 3.2% slower than the fastest kernel and ranges by geometric mean,
 // 19% at the 95th of a hundred, 3.2 times at the worst (64 groups with half a row each, K = 43);
-// on 873 with 6000 to 32768 columns or summed indices, which no fit saw, 7.2%, 33% and 2.1 times.
+// on 873 with 6000 to 32768 columns or summed indices, which no fit saw, 7.3%, 33% and 2.1 times.
 // Both sides of some choices (bf16, B stored N x K, M x N x K, us): 24 x 2048 x 5632 stream
 // 8.8, 64 deep in 6 ranges and their join 11.6, in one 18.9; 512 x 5632 x 2048 128 deep 22,
 // 64 deep 27; 16384 x 5632 x 2048 256 343, 128 388.

@@ -142,7 +142,7 @@ size_t workspace_bytes_of(int64_t groups, int64_t M, int64_t N, int splits)
 
 // The kernel, and with *splits = 0 the K ranges, of least time; a forced kernel or
 // number of ranges stays (but groups of rows have one).  More than one range has to
-// gain a tenth, and the workspace holds those that are chosen. The few-rows kernel's
+// gain a tenth, and the workspace holds those that are chosen.  The few-rows kernel's
 // ranges hold 512 bytes of a row or more.  On 500 random problems of 1 to 96 rows the choice is
 // 3.2% slower than the fastest by geometric mean, 17% at the 95th of a hundred, 42% at the
 // worst; with ranges of any length 4.3, 18 and 72%; with that kernel in one range only 11.5, 46
